@@ -67,7 +67,7 @@ typedef struct CUstream_st *dattn_stream_t;
 enum dattn_status {
     DATTN_OK = 0,
     DATTN_ERR_INVALID_ARG = -1, /* null pointer, non-positive size, bad count    */
-    DATTN_ERR_UNSUPPORTED = -2, /* head_dim not a multiple of 8 or above 256       */
+    DATTN_ERR_UNSUPPORTED = -2, /* head_dim not a multiple of 8 (8-bit cache: 16) or above 256 */
     DATTN_ERR_MISALIGNED = -3,  /* a tensor pointer is not 16-byte aligned          */
     DATTN_ERR_WORKSPACE = -4,   /* workspace missing, misaligned or too small       */
     DATTN_ERR_CUDA = -5,        /* a CUDA runtime call or kernel launch failed      */
@@ -340,6 +340,151 @@ int dattn_softmax_f32(const float *x, float *out, long long rows, int cols,
                       dattn_stream_t stream);
 
 /*
+ * Rotary positions of many tokens: the rotation of dattn_rope_append_f16 on its
+ * own, for a prompt or a training batch, with frequencies that may be scaled
+ * for contexts longer than the trained one.  For token t at p = positions[t],
+ * every head and pair i < rope_dims/2 (pairs as in dattn_rope_append_f16):
+ *   (u, w) -> magnitude (u cos a - w sin a, u sin a + w cos a),  a = p theta_i
+ * in fp32, rounded once to the tensor's type; channels from rope_dims on are
+ * copied.  With d = rope_dims, t_i = rope_base^(-2 i / d) and f = factor:
+ *   DATTN_ROPE_UNSCALED  theta_i = t_i
+ *   DATTN_ROPE_LINEAR    theta_i = t_i / f
+ *   DATTN_ROPE_BASE      theta_i = (rope_base f^(d/(d-2)))^(-2 i / d)
+ *   DATTN_ROPE_BY_PARTS  theta_i = t_i (g + (1 - g) / f): pairs that turn often
+ *                        over the trained length keep their frequency;
+ *                        g = clamp((r - low_turns) / (high_turns - low_turns), 0, 1),
+ *                        r = original_len t_i / (2 pi)
+ * The angle is reduced exactly at every uint32 position.  `gradient` non-zero:
+ * x is the gradient of a rotated tensor and out that of the tensor itself, the
+ * rotation by -a times the same magnitude.
+ *   x, out     [tokens, n_heads, head_dim] of `dtype` (dattn_dtype); a token's
+ *              rows are dense, tokens lie x_stride / out_stride elements apart
+ *              (whole multiples of 16 bytes): q or k may be a slice of a fused
+ *              projection.  out may be x with the same stride; otherwise the
+ *              two must not overlap.
+ *   positions  [tokens] uint32, device
+ * head_dim: a multiple of 8, at most 256.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA.
+ */
+enum dattn_dtype { DATTN_F16 = 1, DATTN_BF16 = 2, DATTN_F32 = 3 };
+enum dattn_rope_scaling {
+    DATTN_ROPE_UNSCALED = 0,
+    DATTN_ROPE_LINEAR = 1,
+    DATTN_ROPE_BASE = 2,
+    DATTN_ROPE_BY_PARTS = 3
+};
+typedef struct dattn_rope_params {
+    int rope_dims;       /* channels that are rotated: even, 2 .. head_dim              */
+    int traditional;     /* non-zero: adjacent pairs; zero: halves                      */
+    double rope_base;    /* finite, above 1                                             */
+    int scaling;         /* dattn_rope_scaling                                          */
+    double factor;       /* >= 1; unused when unscaled                                  */
+    double original_len; /* trained length, > 0 (by parts only)                         */
+    double low_turns;    /* 0 <= low_turns < high_turns (by parts only)                 */
+    double high_turns;
+    double magnitude;    /* multiplies the rotated channels: > 0, 1 for a pure rotation */
+} dattn_rope_params;
+int dattn_rope(const void *x, void *out, int dtype, long long tokens, int n_heads, int head_dim,
+               long long x_stride, long long out_stride, const uint32_t *positions,
+               const dattn_rope_params *rope, int gradient, dattn_stream_t stream);
+
+/*
+ * A KV cache held in 8 bits.  K and V are e4m3 or int8 (dattn_kv_type) with one
+ * fp32 scale for each block of `scale_block` positions and key/value head; the
+ * element stands for its 8-bit value times the scale.  Query heads share
+ * key/value heads in groups: n_heads is a multiple of n_kv_heads and query head
+ * h reads key/value head h / (n_heads / n_kv_heads).
+ *   dense   K_cache, V_cache  [batch, seq_len, n_kv_heads, head_dim]              8-bit
+ *           K_scale, V_scale  [batch, ceil(seq_len / scale_block), n_kv_heads]    fp32
+ *   paged   K_pages, V_pages  [num_pages, page_size, n_kv_heads, head_dim]        8-bit
+ *           K_scale, V_scale  [num_pages, page_size / scale_block, n_kv_heads]    fp32
+ *           block_table       [batch, max_pages] int32, as in dattn_decode_paged_f16;
+ *           page_size is a multiple of scale_block
+ * head_dim is a multiple of 16, at most 256.  Scales are finite and not
+ * negative; 0 stands for a block of zeros.
+ */
+enum dattn_kv_type { DATTN_KV_E4M3 = 1, DATTN_KV_INT8 = 2 };
+
+/*
+ * Rotate new tokens and append their keys and values to an 8-bit cache, one
+ * token or several per sequence (a decode step, a prompt, a mixture).  The
+ * tokens of the batch are flattened: sequence b brings tokens token_offsets[b]
+ * .. token_offsets[b+1]-1 (device int32 [batch+1], ascending from 0; a sequence
+ * may bring none), the last of them at position current_pos[b], the ones before
+ * it at the positions before.  token_offsets NULL: one token per sequence,
+ * tokens = batch.  Rows from token_offsets[batch] on are padding: they are not
+ * read and their rows of q_out are left as they were.  The same current_pos
+ * serves the decode that follows.
+ *   q_new  [tokens, n_heads, head_dim], k_new, v_new [tokens, n_kv_heads, head_dim]
+ *          f16, tokens q_stride, k_stride, v_stride elements apart (as in dattn_rope)
+ *   q_out  [tokens, n_heads, head_dim] f16, dense; may be q_new when that is dense
+ * q and k are rotated as by dattn_rope.  For each block that receives rows, per
+ * key/value head and for K and V apart:
+ *   need  = the smallest power of two s >= 2^-32 with |x| <= QMAX s for every
+ *           finite element of the new rows (QMAX = 448 for e4m3, 127 for int8)
+ *   scale = need; where the sequence's first new position lies inside the
+ *           block, max(old scale, need), and the block's earlier rows are
+ *           requantised if that is another scale than before
+ *   row   = the 8-bit value nearest to x / scale, ties to even; infinities
+ *           saturate, NaN is kept by e4m3 and becomes 0 in int8
+ * Rows of the block behind the new ones (left from tokens taken back) keep their
+ * bytes and no longer stand for anything.  Two sequences must not append to one
+ * block in the same call.  A token whose position is outside [0, seq_len) is not
+ * appended and dattn_device_error() reports DATTN_ERR_BAD_POSITION; an invalid
+ * page likewise, DATTN_ERR_BAD_PAGE.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA.
+ */
+int dattn_rope_append_q8(const void *q_new, const void *k_new, const void *v_new, void *q_out,
+                         void *K_cache, void *V_cache, float *K_scale, float *V_scale, int kv_type,
+                         int scale_block, int batch, int tokens, const int32_t *token_offsets,
+                         long long q_stride, long long k_stride, long long v_stride, int n_heads,
+                         int n_kv_heads, int head_dim, int seq_len, const dattn_rope_params *rope,
+                         const uint32_t *current_pos, dattn_stream_t stream);
+int dattn_rope_append_paged_q8(const void *q_new, const void *k_new, const void *v_new, void *q_out,
+                               void *K_pages, void *V_pages, float *K_scale, float *V_scale,
+                               int kv_type, int scale_block, int batch, int tokens,
+                               const int32_t *token_offsets, long long q_stride, long long k_stride,
+                               long long v_stride, int n_heads, int n_kv_heads, int head_dim,
+                               int page_size, int max_pages, long long num_pages,
+                               const int32_t *block_table, const dattn_rope_params *rope,
+                               const uint32_t *current_pos, dattn_stream_t stream);
+
+/*
+ * Plan and workspace of the decode over an 8-bit cache, as dattn_decode_plan and
+ * dattn_decode_workspace_bytes; seq_len = page_size * max_pages for a paged cache.
+ * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
+ */
+int dattn_decode_q8_plan(int batch, int n_heads, int n_kv_heads, int head_dim, int seq_len,
+                         int num_partitions, dattn_plan *plan);
+int dattn_decode_q8_workspace_bytes(int batch, int n_heads, int n_kv_heads, int head_dim,
+                                    int seq_len, int num_partitions, size_t *bytes);
+
+/*
+ * Fused decode attention over an 8-bit cache: the operation of
+ * dattn_decode_f16_ex (dattn_decode_paged_f16) on the values the cache stands
+ * for, with grouped heads.  Products of f16 and 8-bit values accumulate in fp32;
+ * the running maximum and sum are fp32; the softmax weights are rounded to f16
+ * (relative 2^-11) before they meet V; out is rounded to f16.  Positions past
+ * the live length never enter the computation, their rows and scales are not
+ * read.  A live block-table entry outside [0, num_pages) is not dereferenced:
+ * page 0 is read instead and dattn_device_error() reports DATTN_ERR_BAD_PAGE.
+ *   Q, out [batch, n_heads, head_dim] f16; workspace and num_partitions as in
+ *   dattn_decode_f16_ex, with dattn_decode_q8_workspace_bytes.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
+ */
+int dattn_decode_q8(const void *Q, const void *K_cache, const void *V_cache, const float *K_scale,
+                    const float *V_scale, void *out, int kv_type, int scale_block, int batch,
+                    int n_heads, int n_kv_heads, int head_dim, int seq_len,
+                    const uint32_t *current_pos, void *workspace, size_t workspace_bytes,
+                    int num_partitions, dattn_stream_t stream);
+int dattn_decode_paged_q8(const void *Q, const void *K_pages, const void *V_pages,
+                          const float *K_scale, const float *V_scale, void *out, int kv_type,
+                          int scale_block, int batch, int n_heads, int n_kv_heads, int head_dim,
+                          int page_size, int max_pages, long long num_pages,
+                          const int32_t *block_table, const uint32_t *current_pos, void *workspace,
+                          size_t workspace_bytes, int num_partitions, dattn_stream_t stream);
+
+/*
  * Submission batching: the analogue of the fm_batch_begin / fm_batch_end pair
  * of the C API in Foundry's docs/metal.md (section "Command Batching"), which
  * accumulates operations into one GPU submission.  Here the calls issued on a
@@ -354,8 +499,8 @@ int dattn_softmax_f32(const float *x, float *out, long long rows, int cols,
  * Calls that may be recorded: dattn_decode_f16_ex, dattn_decode_paged_f16,
  * dattn_decode_f16_noalloc after its first call on the device, dattn_qk_f16,
  * dattn_pv_f16, dattn_rope_append_f16, dattn_rope_append_paged_f16,
- * dattn_softmax_f32, and dattn_decode_f16 once its workspace is large enough
- * (a recorded call must not allocate).  Copies the caller issues on the same
+ * dattn_softmax_f32, dattn_rope, the q8 calls, and dattn_decode_f16 once its
+ * workspace is large enough (a recorded call must not allocate).  Copies the caller issues on the same
  * stream meanwhile (cudaMemcpyAsync from pinned host memory, for example) are
  * recorded too.  The shape's plan is made when a call is
  * recorded; make one ordinary call per shape first if its set-up should not

@@ -1,0 +1,205 @@
+"""Rotary positions of many tokens against a plain form in 64 bits."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+import token_decode_attention_gb300 as dattn
+from token_decode_attention_gb300 import _native
+
+from . import _q8
+
+pytestmark = pytest.mark.gpu
+
+# (eps, smallest subnormal) of the output type
+STEP = {torch.float16: (2.0 ** -10, 2.0 ** -24), torch.bfloat16: (2.0 ** -7, 2.0 ** -133),
+        torch.float32: (2.0 ** -23, 2.0 ** -149)}
+SCALINGS = {
+    "none": None,
+    "linear": dattn.RopeScaling("linear", 4.0),
+    "base": dattn.RopeScaling("base", 8.0),
+    "by_parts": dattn.RopeScaling("by_parts", 8.0, original_len=4096, low_turns=1, high_turns=32,
+                                  magnitude=1.2079441541679836),
+}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    from token_decode_attention_gb300 import build
+    build.build()
+    dattn.load()
+    yield
+    assert dattn.dattn_device_error(clear=True) == _native.OK
+
+
+def positions(p) -> torch.Tensor:
+    return torch.from_numpy(np.asarray(p, np.int64).astype(np.uint32).view(np.int32)).cuda()
+
+
+def check(got, x, p, rd, base, trad, scaling, gradient, what=""):
+    rd = rd or x.shape[-1]
+    xn = _q8.f64(x)
+    ref = _q8.rotate(xn, p, rd, base, trad, scaling, gradient)
+    mag = 1.0 if scaling is None else scaling.magnitude
+    bound = _q8.ROTATION * _q8.pair_size(xn, rd, trad, mag)
+    eps, tiny = STEP[x.dtype]
+    bound = bound + (np.arange(x.shape[-1]) < rd) * _q8.half_step(np.abs(ref) + bound, eps, tiny)
+    _q8.check(_q8.f64(got), ref, bound, what)
+
+
+CASES = [
+    # tokens, H, D, rope_dims, base
+    (1, 32, 128, 0, 10000.0),
+    (1, 1, 8, 0, 10000.0),
+    (3, 5, 64, 20, 10000.0),      # pairs read one by one
+    (7, 3, 24, 16, 10000.0),      # a head of 24 channels: no whole vectors past the rotated ones
+    (130, 40, 128, 64, 500000.0),
+    (33, 2, 256, 0, 1e6),
+    (1000, 8, 80, 32, 10000.0),
+    (65, 17, 96, 96, 10000.0),
+    (2, 600, 64, 48, 10000.0),    # more heads than a CTA takes
+    (4097, 1, 128, 2, 10000.0),
+]
+
+
+@pytest.mark.parametrize("dtype", list(STEP), ids=["f16", "bf16", "f32"])
+@pytest.mark.parametrize("trad", [False, True], ids=["half", "adjacent"])
+@pytest.mark.parametrize("n,H,D,rd,base", CASES, ids=[f"T{c[0]}H{c[1]}D{c[2]}r{c[3]}" for c in CASES])
+def test_matches_the_plain_form(n, H, D, rd, base, trad, dtype):
+    g = torch.Generator(device="cuda").manual_seed(n + H + D)
+    x = (2 * torch.randn((n, H, D), generator=g, device="cuda")).to(dtype)
+    p = np.random.default_rng(n).integers(0, 200000, n)
+    check(dattn.rope(x, positions(p), rd, base, trad), x, p, rd, base, trad, None, False)
+
+
+@pytest.mark.parametrize("gradient", [False, True])
+@pytest.mark.parametrize("kind", list(SCALINGS))
+def test_scaled_frequencies(kind, gradient):
+    g = torch.Generator(device="cuda").manual_seed(4)
+    x = torch.randn((50, 4, 128), generator=g, device="cuda")
+    p = np.arange(50) * 1777
+    for trad in (False, True):
+        check(dattn.rope(x, positions(p), 0, 10000.0, trad, SCALINGS[kind], gradient), x, p, 0,
+              10000.0, trad, SCALINGS[kind], gradient, f"{kind} {trad}")
+
+
+def test_far_positions_keep_their_digits():
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.randn((6, 3, 64), generator=g, device="cuda")
+    p = [0, 1, 2 ** 24 + 1, 2 ** 31 - 1, 2 ** 31, 2 ** 32 - 1]
+    # theta_i itself is rounded to 64 bits: p theta_i is off by up to 2^32 2^-53 rad,
+    # which the plain form shares (it uses the same theta)
+    check(dattn.rope(x, positions(p)), x, p, 0, 10000.0, False, None, False)
+
+
+def test_gradient_is_the_transpose():
+    g = torch.Generator(device="cuda").manual_seed(6)
+    x, y = (torch.randn((40, 3, 64), generator=g, device="cuda") for _ in range(2))
+    p = positions(np.arange(40) * 911)
+    s = SCALINGS["by_parts"]
+    for trad in (False, True):
+        fx = dattn.rope(x, p, 48, 1e4, trad, s)
+        gy = dattn.rope(y, p, 48, 1e4, trad, s, gradient=True)
+        a, b = (fx.double() * y.double()).sum((1, 2)), (x.double() * gy.double()).sum((1, 2))
+        # per element at most ROTATION (|u| + |w|) of error on either side, 192 of them
+        size = (x.double().abs().sum((1, 2)) * y.double().abs().amax((1, 2)) * 2 * s.magnitude)
+        assert ((a - b).abs() <= 4 * _q8.ROTATION * size).all()
+
+
+def test_gradient_agrees_with_differences():
+    g = torch.Generator(device="cuda").manual_seed(7)
+    x, y, d = (torch.randn((5, 2, 32), generator=g, device="cuda") for _ in range(3))
+    p = positions([3, 70, 1000, 9, 0])
+    s = SCALINGS["by_parts"]
+    f = lambda t: (dattn.rope(t, p, 24, 1e4, False, s).double() * y.double()).sum()  # noqa: E731
+    grad = dattn.rope(y, p, 24, 1e4, False, s, gradient=True)
+    # the map is linear: a difference over a step of 1 has no truncation error
+    num, ana = float(f(x + d) - f(x - d)) / 2, float((grad.double() * d.double()).sum())
+    bound = 8 * 2.0 ** -23 * float((y.double().abs() * (x.double().abs() + d.double().abs())).sum()) * 4
+    assert abs(num - ana) <= bound
+
+
+def test_in_place_and_slices_of_a_projection():
+    g = torch.Generator(device="cuda").manual_seed(8)
+    H, Hk, D, n = 8, 2, 128, 77
+    qkv = torch.randn((n, (H + 2 * Hk) * D), generator=g, device="cuda").half()
+    keep = qkv.clone()
+    q = qkv[:, : H * D].view(n, H, D)
+    k = qkv[:, H * D: (H + Hk) * D].view(n, Hk, D)
+    p = np.arange(n) + 5
+    got_k = dattn.rope(k, positions(p))
+    check(got_k, k, p, 0, 1e4, False, None, False, "k")
+    x = q.clone()
+    dattn.rope(q, positions(p), out=q)
+    check(q, x, p, 0, 1e4, False, None, False, "q in place")
+    assert torch.equal(qkv[:, H * D:], keep[:, H * D:])
+
+
+def test_special_values_stay_in_their_pair():
+    x = torch.ones((2, 1, 32), device="cuda")
+    x[0, 0, 3] = float("nan")
+    x[1, 0, 20] = float("inf")
+    y = dattn.rope(x, positions([5, 0]), 16)
+    bad = ~torch.isfinite(y)
+    want = torch.zeros_like(bad)
+    want[0, 0, [3, 11]] = True
+    want[1, 0, 20] = True  # passes through
+    assert torch.equal(bad, want)
+
+
+def test_agrees_with_the_append_of_one_token():
+    # the rotation of dattn_rope_append_f16, up to one rounding of f16
+    g = torch.Generator(device="cuda").manual_seed(9)
+    B, H, D = 4, 8, 128
+    q = torch.randn((B, H, D), generator=g, device="cuda").half()
+    cache = torch.zeros((B, 600, H, D), dtype=torch.float16, device="cuda")
+    p = [0, 599, 17, 300]
+    a = dattn.rope_append(q, q, q, cache, cache.clone(), positions(p))
+    b = dattn.rope(q, positions(p))
+    step = _q8.half_step(_q8.f64(b), 2.0 ** -10, 2.0 ** -24) * 2
+    _q8.check(_q8.f64(a), _q8.f64(b), step + 1e-6, "one token")
+
+
+def test_graph_replay_and_streams():
+    g = torch.Generator(device="cuda").manual_seed(10)
+    x = torch.randn((100, 4, 64), generator=g, device="cuda").half()
+    p = np.arange(100)
+    tp = positions(p)
+    s = torch.cuda.Stream()
+    out = torch.empty_like(x)
+    torch.cuda.synchronize()
+    dattn.dattn_batch_begin(s)
+    dattn.rope(x, tp, out=out, stream=s)
+    batch = dattn.dattn_batch_end(s)
+    for k in (3, 40):
+        x.normal_(generator=g)
+        tp.copy_(positions(p + k))
+        torch.cuda.synchronize()
+        batch.launch(s)
+        s.synchronize()
+        check(out, x, p + k, 0, 1e4, False, None, False)
+    batch.close()
+
+
+def test_refusals():
+    x = torch.zeros((4, 2, 64), device="cuda")
+    p = positions([0, 1, 2, 3])
+    with pytest.raises(TypeError, match="float16"):
+        dattn.rope(x.double(), p)
+    with pytest.raises(ValueError, match="positions"):
+        dattn.rope(x, p[:3])
+    with pytest.raises(TypeError, match="positions"):
+        dattn.rope(x, p.long())
+    with pytest.raises(ValueError, match="contiguous"):
+        dattn.rope(x.transpose(1, 2), p)
+    with pytest.raises(ValueError, match="out"):
+        dattn.rope(x, p, out=x[:, :1])
+    with pytest.raises(_native.DattnError, match="16-byte"):
+        dattn.rope(torch.zeros(4 * 130 + 8, device="cuda")[: 4 * 130].view(4, 130)[:, :128].view(4, 2, 64), p)
+    with pytest.raises(_native.DattnError, match="rope_dims"):
+        dattn.rope(x, p, 66)
+    with pytest.raises(_native.DattnError, match="INVALID_ARG"):
+        dattn.rope(x[:0], p[:0])
+    with pytest.raises(TypeError, match="RopeScaling"):
+        dattn.rope(x, p, scaling="linear")

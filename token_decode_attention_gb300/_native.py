@@ -38,12 +38,28 @@ class Plan(ctypes.Structure):
         return {name: getattr(self, name) for name, _ in self._fields_}
 
 
+class RopeParams(ctypes.Structure):
+    """struct dattn_rope_params."""
+    _fields_ = [("rope_dims", ctypes.c_int), ("traditional", ctypes.c_int),
+                ("rope_base", ctypes.c_double), ("scaling", ctypes.c_int),
+                ("factor", ctypes.c_double), ("original_len", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double),
+                ("magnitude", ctypes.c_double)]
+
+
 # status codes (enum dattn_status)
 (OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_MISALIGNED, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT,
  ERR_BAD_PAGE, ERR_BAD_POSITION) = (0, -1, -2, -3, -4, -5, -6, -7, -8)
 
+# enum dattn_dtype, dattn_kv_type, dattn_rope_scaling
+_DTYPES = {torch.float16: 1, torch.bfloat16: 2, torch.float32: 3}
+_KV_TYPES = {torch.float8_e4m3fn: 1, torch.int8: 2}
+_ROPE_SCALINGS = {"linear": 1, "base": 2, "by_parts": 3}
+
 _P = ctypes.c_void_p
 _I = ctypes.c_int
+_L = ctypes.c_longlong
+_ROPE = ctypes.POINTER(RopeParams)
 _SIGNATURES = {
     "dattn_version": ([], _I),
     "dattn_status_string": ([_I], ctypes.c_char_p),
@@ -67,6 +83,15 @@ _SIGNATURES = {
                                _P, _P], _I),
     "dattn_rope_append_paged_f16": ([_P, _P, _P, _P, _P, _P, _I, _I, _I, _I, _I,
                                      ctypes.c_longlong, _P, _I, ctypes.c_double, _I, _P, _P], _I),
+    "dattn_rope": ([_P, _P, _I, _L, _I, _I, _L, _L, _P, _ROPE, _I, _P], _I),
+    "dattn_rope_append_q8": ([_P] * 8 + [_I, _I, _I, _I, _P, _L, _L, _L, _I, _I, _I, _I, _ROPE, _P,
+                                         _P], _I),
+    "dattn_rope_append_paged_q8": ([_P] * 8 + [_I, _I, _I, _I, _P, _L, _L, _L, _I, _I, _I, _I, _I,
+                                               _L, _P, _ROPE, _P, _P], _I),
+    "dattn_decode_q8_plan": ([_I] * 6 + [ctypes.POINTER(Plan)], _I),
+    "dattn_decode_q8_workspace_bytes": ([_I] * 6 + [ctypes.POINTER(ctypes.c_size_t)], _I),
+    "dattn_decode_q8": ([_P] * 6 + [_I] * 7 + [_P, _P, ctypes.c_size_t, _I, _P], _I),
+    "dattn_decode_paged_q8": ([_P] * 6 + [_I] * 8 + [_L, _P, _P, _P, ctypes.c_size_t, _I, _P], _I),
     "dattn_batch_begin": ([_P], _I),
     "dattn_batch_end": ([_P, ctypes.POINTER(ctypes.c_void_p)], _I),
     "dattn_batch_launch": ([_P, _P], _I),
@@ -352,13 +377,20 @@ class Batch:
             pass
 
 
+_RECORDING: set[int] = set()  # streams between dattn_batch_begin and dattn_batch_end
+
+
 def dattn_batch_begin(stream) -> None:
-    _check(load().dattn_batch_begin(_stream_handle(stream)), "dattn_batch_begin")
+    handle = _stream_handle(stream)
+    _check(load().dattn_batch_begin(handle), "dattn_batch_begin")
+    _RECORDING.add(handle)
 
 
 def dattn_batch_end(stream) -> Batch:
     h = ctypes.c_void_p(0)
-    _check(load().dattn_batch_end(_stream_handle(stream), ctypes.byref(h)), "dattn_batch_end")
+    handle = _stream_handle(stream)
+    _RECORDING.discard(handle)
+    _check(load().dattn_batch_end(handle, ctypes.byref(h)), "dattn_batch_end")
     return Batch(h.value)
 
 
@@ -405,3 +437,295 @@ def pv(scores, v, out=None, stream=None):
         out = torch.empty((B, H, int(v.shape[3])), dtype=torch.float16, device=v.device)
     dattn_pv_f16(scores, v, out, stream)
     return out
+
+
+# ------------------------------------- rotary positions and the 8-bit KV cache
+
+class RopeScaling:
+    """Frequencies of a rotation scaled for long contexts (enum dattn_rope_scaling):
+    ``kind`` "linear", "base" or "by_parts" (which takes ``original_len``,
+    ``low_turns`` and ``high_turns``); ``magnitude`` multiplies the rotated
+    channels.  Immutable; make it once and pass it to every call."""
+
+    __slots__ = ("kind", "factor", "original_len", "low_turns", "high_turns", "magnitude")
+
+    def __init__(self, kind: str, factor: float, original_len: float = 0.0,
+                 low_turns: float = 1.0, high_turns: float = 32.0, magnitude: float = 1.0):
+        if kind not in _ROPE_SCALINGS:
+            raise ValueError(f"kind must be one of {sorted(_ROPE_SCALINGS)}, got {kind!r}")
+        for name, v in (("kind", kind), ("factor", float(factor)),
+                        ("original_len", float(original_len)), ("low_turns", float(low_turns)),
+                        ("high_turns", float(high_turns)), ("magnitude", float(magnitude))):
+            object.__setattr__(self, name, v)
+
+    def __setattr__(self, name, value):
+        raise AttributeError("RopeScaling is immutable")
+
+    def _key(self):
+        return (self.kind, self.factor, self.original_len, self.low_turns, self.high_turns,
+                self.magnitude)
+
+    def __eq__(self, other):
+        return isinstance(other, RopeScaling) and self._key() == other._key()
+
+    def __hash__(self):
+        return hash(self._key())
+
+    def __repr__(self):
+        return "RopeScaling(" + ", ".join(f"{n}={getattr(self, n)!r}" for n in self.__slots__) + ")"
+
+
+def _rope_params(head_dim: int, rope_dims: int, rope_base: float, traditional: bool,
+                 scaling) -> RopeParams:
+    if scaling is not None and not isinstance(scaling, RopeScaling):
+        raise TypeError(f"scaling must be a RopeScaling, got {type(scaling).__name__}")
+    if scaling is None:
+        return RopeParams(rope_dims or head_dim, 1 if traditional else 0, float(rope_base), 0, 1.0,
+                          0.0, 0.0, 0.0, 1.0)
+    return RopeParams(rope_dims or head_dim, 1 if traditional else 0, float(rope_base),
+                      _ROPE_SCALINGS[scaling.kind], scaling.factor, scaling.original_len,
+                      scaling.low_turns, scaling.high_turns, scaling.magnitude)
+
+
+def _on_device(named) -> None:
+    """Every CUDA tensor on the current device, whose stream the call goes to."""
+    dev = torch.cuda.current_device()
+    for name, t in named:
+        if t.is_cuda and t.get_device() != dev:
+            raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
+                             f"cuda:{dev}")
+
+
+def _like(shape, dtype, device, stream):
+    """A tensor from the pool of the stream that the call goes to."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _index32(t, name: str, shape) -> int:
+    if isinstance(t, torch.Tensor) and t.dtype not in (torch.int32,
+                                                       getattr(torch, "uint32", torch.int32)):
+        raise TypeError(f"{name} must be int32 or uint32, got {t.dtype}")
+    return _tensor(t, name, shape, getattr(t, "dtype", torch.int32))
+
+
+def _tokens(t, name: str, dtype) -> tuple[int, int]:
+    """Pointer and token stride of a [tokens, heads, head_dim] tensor whose tokens
+    are dense inside and may lie apart (a slice of a fused projection)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, head_dim], got {tuple(t.shape)}")
+    if not (t.is_cuda or t.is_pinned()):
+        raise ValueError(f"{name} must be a CUDA tensor or a pinned CPU tensor")
+    n, h, d = t.shape
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and d > 1) or (s1 != d and h > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, strides are {t.stride()}")
+    return t.data_ptr(), (s0 if n > 1 else h * d)
+
+
+def dattn_rope(x, out, positions, rope_dims: int = 0, rope_base: float = 10000.0,
+               traditional: bool = False, scaling=None, gradient: bool = False,
+               stream=None) -> None:
+    dtype = getattr(x, "dtype", None)
+    if dtype not in _DTYPES:
+        raise TypeError(f"x must be float16, bfloat16 or float32, got {dtype}")
+    xp, xs = _tokens(x, "x", dtype)
+    op, os_ = _tokens(out, "out", dtype)
+    n, h, d = x.shape
+    if out.shape != x.shape:
+        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
+    pp = _index32(positions, "positions", (n,))
+    _on_device((("x", x), ("out", out), ("positions", positions)))
+    _check(load().dattn_rope(xp, op, _DTYPES[dtype], n, h, d, xs, os_, pp,
+                             _rope_params(d, rope_dims, rope_base, traditional, scaling),
+                             1 if gradient else 0, _stream_handle(stream)), "dattn_rope")
+
+
+def rope(x, positions, rope_dims: int = 0, rope_base: float = 10000.0, traditional: bool = False,
+         scaling=None, gradient: bool = False, out=None, stream=None):
+    """Rotate x [tokens, heads, head_dim] (f16, bf16 or f32) at ``positions``; with
+    ``gradient`` the gradient of the rotated tensor into that of the tensor."""
+    if out is None:
+        out = _like(x.shape, x.dtype, x.device, stream)
+    dattn_rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
+    return out
+
+
+def _q8_cache(k, v, k_scale, v_scale, scale_block: int, block_table, batch: int):
+    """Shapes and pointers of an 8-bit cache: (kv_type, n_kv_heads, head_dim,
+    capacity, page geometry or None, pointers)."""
+    if not isinstance(k, torch.Tensor) or k.dtype not in _KV_TYPES:
+        raise TypeError("the cache must be float8_e4m3fn or int8, got "
+                        f"{getattr(k, 'dtype', type(k).__name__)}")
+    if k.dim() != 4:
+        raise ValueError("the cache must be [batch, seq_len, n_kv_heads, head_dim] or [num_pages, "
+                         "page_size, n_kv_heads, head_dim]")
+    if scale_block < 1:
+        raise ValueError(f"scale_block={scale_block} must be positive")
+    lead, rows, hk, d = k.shape
+    if block_table is None and lead != batch:
+        raise ValueError(f"the cache holds {lead} sequences, the batch {batch}")
+    sshape = (lead, -(-rows // scale_block), hk)
+    ptrs = (_tensor(k, "K cache", k.shape, k.dtype), _tensor(v, "V cache", k.shape, k.dtype),
+            _tensor(k_scale, "K_scale", sshape, torch.float32),
+            _tensor(v_scale, "V_scale", sshape, torch.float32))
+    pages = None
+    if block_table is not None:
+        if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+            raise ValueError("block_table must be [batch, max_pages]")
+        table = _tensor(block_table, "block_table", (batch, block_table.shape[1]), torch.int32)
+        pages = (rows, block_table.shape[1], lead, table)
+        rows = rows * block_table.shape[1]
+    return _KV_TYPES[k.dtype], hk, d, rows, pages, ptrs
+
+
+def dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, v_scale,
+                         current_pos, scale_block: int, token_offsets=None, rope_dims: int = 0,
+                         rope_base: float = 10000.0, traditional: bool = False, scaling=None,
+                         block_table=None, stream=None) -> None:
+    """The dense call, or the paged one when ``block_table`` is given."""
+    qp, qs = _tokens(q_new, "q_new", torch.float16)
+    kp, kstr = _tokens(k_new, "k_new", torch.float16)
+    vp, vstr = _tokens(v_new, "v_new", torch.float16)
+    n, h, d = q_new.shape
+    batch = current_pos.shape[0] if getattr(current_pos, "ndim", 0) == 1 else -1
+    cp = _index32(current_pos, "current_pos", (batch,))
+    kv, hk, dc, seq_len, pages, ptrs = _q8_cache(k_cache, v_cache, k_scale, v_scale, scale_block,
+                                                 block_table, batch)
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.shape != (n, hk, dc):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, hk, dc)}")
+    if d != dc:
+        raise ValueError(f"q_new has head_dim {d}, the cache {dc}")
+    op = _tensor(q_out, "q_out", q_new.shape)
+    tp = None
+    if token_offsets is not None:
+        tp = _tensor(token_offsets, "token_offsets", (batch + 1,), torch.int32)
+    elif n != batch:
+        raise ValueError(f"without token_offsets each sequence brings one token: {n} tokens, "
+                         f"{batch} sequences")
+    _on_device((("q_new", q_new), ("k_new", k_new), ("v_new", v_new), ("q_out", q_out),
+                ("K cache", k_cache), ("V cache", v_cache), ("K_scale", k_scale),
+                ("V_scale", v_scale), ("current_pos", current_pos)))
+    rp = _rope_params(d, rope_dims, rope_base, traditional, scaling)
+    s = _stream_handle(stream)
+    if pages is None:
+        _check(load().dattn_rope_append_q8(qp, kp, vp, op, *ptrs, kv, scale_block, batch, n, tp, qs,
+                                           kstr, vstr, h, hk, d, seq_len, rp, cp, s),
+               "dattn_rope_append_q8")
+    else:
+        _check(load().dattn_rope_append_paged_q8(qp, kp, vp, op, *ptrs, kv, scale_block, batch, n,
+                                                 tp, qs, kstr, vstr, h, hk, d, *pages, rp, cp, s),
+               "dattn_rope_append_paged_q8")
+
+
+def rope_append_q8(q_new, k_new, v_new, k_cache, v_cache, k_scale, v_scale, current_pos,
+                   scale_block: int, token_offsets=None, rope_dims: int = 0,
+                   rope_base: float = 10000.0, traditional: bool = False, scaling=None,
+                   block_table=None, q_out=None, stream=None):
+    """Rotate the new tokens' q and k and append k, v to an 8-bit cache (dense, or
+    paged when ``block_table`` is given): one token per sequence, or the ragged
+    ``token_offsets`` [batch + 1].  ``current_pos`` holds the position of each
+    sequence's last new token.  Returns the rotated q."""
+    if q_out is None:
+        q_out = _like(q_new.shape, q_new.dtype, q_new.device, stream)
+    dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, v_scale,
+                         current_pos, scale_block, token_offsets, rope_dims, rope_base, traditional,
+                         scaling, block_table, stream)
+    return q_out
+
+
+def dattn_decode_q8_plan(batch: int, n_heads: int, n_kv_heads: int, head_dim: int, seq_len: int,
+                         num_partitions: int = 0) -> dict:
+    plan = Plan()
+    _check(load().dattn_decode_q8_plan(batch, n_heads, n_kv_heads, head_dim, seq_len,
+                                       num_partitions, ctypes.byref(plan)), "dattn_decode_q8_plan")
+    return plan.as_dict()
+
+
+_Q8_WORKSPACE: dict[tuple, int] = {}  # the size depends on the shape and the device only
+
+
+def dattn_decode_q8_workspace_bytes(batch: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                                    seq_len: int, num_partitions: int = 0) -> int:
+    key = (torch.cuda.current_device(), batch, n_heads, n_kv_heads, head_dim, seq_len,
+           num_partitions)
+    n = _Q8_WORKSPACE.get(key)
+    if n is None:
+        size = ctypes.c_size_t(0)
+        _check(load().dattn_decode_q8_workspace_bytes(*key[1:], ctypes.byref(size)),
+               "dattn_decode_q8_workspace_bytes")
+        n = _Q8_WORKSPACE[key] = int(size.value)
+    return n
+
+
+def dattn_decode_q8(q, k, v, k_scale, v_scale, out, current_pos, scale_block: int, workspace=None,
+                    num_partitions: int = 0, block_table=None, stream=None) -> None:
+    """The dense call, or the paged one when ``block_table`` is given."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("Q must be [batch, n_heads, head_dim]")
+    b, h, d = q.shape
+    kv, hk, dc, seq_len, pages, ptrs = _q8_cache(k, v, k_scale, v_scale, scale_block, block_table, b)
+    if d != dc:
+        raise ValueError(f"Q has head_dim {d}, the cache {dc}")
+    qp, op = _tensor(q, "Q"), _tensor(out, "out", q.shape)
+    cp = _index32(current_pos, "current_pos", (b,))
+    _on_device((("Q", q), ("K cache", k), ("V cache", v), ("K_scale", k_scale),
+                ("V_scale", v_scale), ("out", out), ("current_pos", current_pos)))
+    wp, wn = None, 0
+    if workspace is not None:
+        wp = _tensor(workspace, "workspace", None, workspace.dtype)
+        wn = workspace.numel() * workspace.element_size()
+    s = _stream_handle(stream)
+    if pages is None:
+        _check(load().dattn_decode_q8(qp, *ptrs, op, kv, scale_block, b, h, hk, d, seq_len, cp, wp,
+                                      wn, num_partitions, s), "dattn_decode_q8")
+    else:
+        page_size, max_pages, num_pages, table = pages
+        _check(load().dattn_decode_paged_q8(qp, *ptrs, op, kv, scale_block, b, h, hk, d, page_size,
+                                            max_pages, num_pages, table, cp, wp, wn, num_partitions,
+                                            s), "dattn_decode_paged_q8")
+
+
+def _decode_q8(q, k, v, k_scale, v_scale, block_table, current_pos, scale_block, num_partitions,
+               out, workspace, stream):
+    if workspace is None and _RECORDING and _stream_handle(stream) in _RECORDING:
+        raise ValueError("a recorded decode needs a workspace that outlives the batch: pass "
+                         "workspace (dattn_decode_q8_workspace_bytes) and out")
+    if q.dim() != 3 or k.dim() != 4:
+        raise ValueError("Q must be [batch, n_heads, head_dim], the cache 4-dimensional")
+    if out is None:
+        out = _like(q.shape, torch.float16, k.device, stream)
+    if workspace is None:
+        b, h, d = q.shape
+        rows = k.shape[1] if block_table is None else k.shape[1] * block_table.shape[1]
+        n = dattn_decode_q8_workspace_bytes(b, h, k.shape[2], d, rows, num_partitions)
+        if n:
+            workspace = _like((n,), torch.uint8, k.device, stream)
+    dattn_decode_q8(q, k, v, k_scale, v_scale, out, current_pos, scale_block, workspace,
+                    num_partitions, block_table, stream)
+    return out
+
+
+def decode_q8(q, k, v, k_scale, v_scale, current_pos, scale_block: int, num_partitions: int = 0,
+              out=None, workspace=None, stream=None):
+    """Fused decode over an 8-bit cache [batch, seq_len, n_kv_heads, head_dim]
+    (float8_e4m3fn or int8) with scales [batch, ceil(seq_len / scale_block),
+    n_kv_heads]; allocates ``out`` and the workspace if not given."""
+    return _decode_q8(q, k, v, k_scale, v_scale, None, current_pos, scale_block, num_partitions,
+                      out, workspace, stream)
+
+
+def decode_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, current_pos,
+                    scale_block: int, num_partitions: int = 0, out=None, workspace=None,
+                    stream=None):
+    """Fused decode over a paged 8-bit cache [num_pages, page_size, n_kv_heads,
+    head_dim] with scales [num_pages, page_size / scale_block, n_kv_heads]."""
+    return _decode_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, current_pos, scale_block,
+                      num_partitions, out, workspace, stream)

@@ -28,7 +28,7 @@ namespace {
 
 using dattn::DecodeVariant;
 
-constexpr int kVersion = 10000;        // 1.0.0
+constexpr int kVersion = 10100;        // 1.1.0
 constexpr int kMaxPartitions = 65535;  // CTAs of the decode grid
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxHeadsPerLaneGroup = 4;  // register slots per lane group (KMAX)
@@ -388,15 +388,8 @@ int split_plan(int B, int H, int D, int S, int num_partitions, int min_groups, b
         p.prefix_bytes = round_up_sz((static_cast<size_t>(B) + 1) * sizeof(long long), 256);
         p.acc_bytes = round_up_sz(rows * D * sizeof(float), 256);
         p.ws_bytes = p.prefix_bytes + p.acc_bytes + rows * sizeof(float2);
-        // Combine chunk: at most ~8 pieces per thread of a 128-thread CTA, given
-        // the expected pieces per unit (G + U) / U.
-        const double pieces = static_cast<double>(p.G + units) / static_cast<double>(units);
-        int cw = std::min(256, next_pow2(D));
-        while (cw > 8 && pieces * cw / 512.0 > 8.0) cw /= 2;
-        p.combine_chunk = cw;
-        // loads in flight per thread: a thread's expected pieces in one round
-        const double per_thread = pieces / (128.0 / (cw / 4));
-        p.combine_inflight = per_thread <= 2.0 ? 2 : (per_thread <= 4.0 ? 4 : 8);
+        dattn::combine_shape(D, p.G, static_cast<long long>(units), &p.combine_chunk,
+                             &p.combine_inflight);
     }
     *out = p;
     return DATTN_OK;
@@ -713,6 +706,13 @@ std::map<std::pair<int, cudaStream_t>, OwnedWorkspace> g_workspaces;
 
 namespace dattn {
 int set_last_error(int status, const char *message) { return fail(status, "%s", message); }
+
+int device_facts(DeviceFacts *out) {
+    DeviceInfo di;
+    if (int st = device_info(&di)) return st;
+    *out = DeviceFacts{di.sms, di.max_smem_optin, di.err_word};
+    return DATTN_OK;
+}
 }  // namespace dattn
 
 extern "C" {

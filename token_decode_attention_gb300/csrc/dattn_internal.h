@@ -160,4 +160,126 @@ cudaError_t launch_qk(const void *Q, const void *K, void *scores, int B, int H, 
 cudaError_t launch_pv(const void *scores, const void *V, void *out, int B, int H, int D,
                       int S, cudaStream_t stream);
 
+// n / d by a multiplication, exact for 0 <= n < 2^31 (d >= 1): with l = ceil(log2 d),
+// mul = ceil(2^(31+l) / d) <= 2^32 - 1 exceeds 2^(31+l) / d by less than 2^l / d,
+// which n < 2^31 cannot carry into the next integer.
+struct FastDiv {
+    uint32_t mul;
+    int shift;
+};
+inline FastDiv fast_div_of(int d) {
+    int l = 0;
+    while ((1LL << l) < d) ++l;
+    const unsigned long long p = 1ull << (31 + l);
+    return FastDiv{static_cast<uint32_t>((p + d - 1) / d), 31 + l};
+}
+
+// 8-bit cache types (enum dattn_kv_type).
+constexpr int kKvE4m3 = 1, kKvInt8 = 2;
+
+// Bytes of one ring slot of the 8-bit decode: 16 positions of K and V, DP bytes
+// per row, and their 32 scales.
+__host__ __device__ constexpr int q8_tile_bytes(int dp) { return 32 * dp + 128; }
+
+// Arguments of the decode kernel over an 8-bit cache (decode_q8.cu).  A virtual
+// head is a group of gq query heads of one key/value head (a key/value head has
+// vheads_per_kv of them); units are (sequence, group of heads_per_cta virtual
+// heads) and the flattened positions are cut as in DecodeArgs.
+struct Q8DecodeArgs {
+    const void *Q;               // f16 [B,H,D]
+    const unsigned char *K, *V;  // [B,S,Hk,D], or pages [num_pages,page_size,Hk,D]
+    const float *ks, *vs;        // [B,ceil(S/n),Hk], or [num_pages,page_size/n,Hk]
+    void *out;                   // f16 [B,H,D]
+    const uint32_t *cur_pos;     // [B]
+    long long *ws_prefix;        // as in DecodeArgs
+    float *ws_acc;               // [(G+U), heads_per_cta * gq, D]
+    float2 *ws_ml;               // [(G+U), heads_per_cta * gq]
+    unsigned *err;
+    const int *block_table;      // nullptr: dense cache
+    long long num_pages;
+    int page_size, max_pages;
+    int scale_rows;              // scale blocks of a sequence (dense) or of a page
+    FastDiv div_page, div_block;
+    int B, H, D, S;
+    int kv_heads, gq, vheads, vheads_per_kv;
+    int heads_per_cta;           // virtual heads of a CTA
+    int head_groups;
+    int phases;                  // warps that share a virtual head
+    int partitions;
+    float qscale;                // log2(e) / sqrt(D)
+};
+// Warps of a CTA and ring slots of a warp for rows of dp bytes and nt column tiles.
+bool decode_q8_shape(int dp, int nt, int *warps, int *slots);
+cudaError_t decode_q8_configure();
+cudaError_t launch_decode_q8(const Q8DecodeArgs &a, int dp, int nt, int kv, cudaStream_t stream);
+
+// The combine kernel's launch shape for G partitions over `units` units: the
+// chunk of channels per CTA (at most ~8 pieces per thread of a 128-thread CTA,
+// given the expected pieces per unit, (G + U) / U) and a thread's expected
+// pieces in one round as loads in flight.
+inline void combine_shape(int D, long long partitions, long long units, int *chunk, int *inflight) {
+    const double pieces = static_cast<double>(partitions + units) / static_cast<double>(units);
+    int p2 = 1;
+    while (p2 < D) p2 <<= 1;
+    int cw = p2 < 256 ? p2 : 256;
+    while (cw > 8 && pieces * cw / 512.0 > 8.0) cw /= 2;
+    const double per_thread = pieces / (128.0 / (cw / 4));
+    *chunk = cw;
+    *inflight = per_thread <= 2.0 ? 2 : (per_thread <= 4.0 ? 4 : 8);
+}
+
+// What entry points outside dattn_api.cpp need of the current device.
+struct DeviceFacts {
+    int sms;
+    int max_smem_optin;
+    unsigned *err_word;
+};
+int device_facts(DeviceFacts *out);  // a dattn_status, the message recorded
+
+// Rotation of pair i of a token at position p: by the angle p theta_i, cos and
+// sin both multiplied by `magnitude`.  theta_i / (2 pi) travels as a binary
+// fraction in units of 2^-64.
+struct RopeTable {
+    unsigned long long turn_frac[128];  // rope_dims / 2 entries, head_dim <= 256
+    float magnitude;
+    int rope_dims;
+    int traditional;
+};
+
+// Rotation of x [tokens, H, D] (dtype f16, bf16 or f32) by explicit positions.
+struct RopeArgs {
+    RopeTable rope;
+    const void *x;
+    void *out;
+    const uint32_t *positions;  // [tokens]
+    long long x_stride, out_stride;  // elements from token to token
+    long long tokens;
+    int H, D;
+    int gradient;
+};
+constexpr int kDtypeF16 = 1, kDtypeBf16 = 2, kDtypeF32 = 3;
+cudaError_t launch_rope(const RopeArgs &a, int dtype, int sms, cudaStream_t stream);
+
+// Rotation of new tokens and their append to an 8-bit cache (append_q8.cu).
+struct Q8AppendArgs {
+    RopeTable rope;
+    const void *q, *k, *v;                    // f16 [tokens, H or Hk, D]
+    long long q_stride, k_stride, v_stride;   // elements from token to token
+    void *q_out;                              // f16 [tokens, H, D]
+    unsigned char *K, *V;
+    float *ks, *vs;
+    const int *block_table;                   // nullptr: dense cache
+    long long num_pages;
+    int page_size, max_pages;
+    int scale_rows;
+    int scale_block;
+    FastDiv div_page, div_block;
+    const int *offsets;                       // [B+1] or nullptr: one token per sequence
+    const uint32_t *cur_pos;                  // [B] position of each sequence's last new token
+    unsigned *err;
+    long long tokens;
+    int B, H, kv_heads, D, S;
+};
+cudaError_t launch_append_q8(const Q8AppendArgs &a, int kv, int sms, cudaStream_t stream);
+
 }  // namespace dattn
