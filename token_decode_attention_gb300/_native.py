@@ -440,6 +440,33 @@ def pv(scores, v, out=None, stream=None):
 
 
 # ------------------------------------- rotary positions and the 8-bit KV cache
+#
+# A step of one token takes the GPU 2 to 8 us, less than a check of every argument
+# by itself would take the host.  The calls below first test what an ordinary call
+# looks like (CUDA tensors of the current device, right types and shapes) in one
+# expression of attribute reads; only where it does not hold do the checks run
+# that name what is wrong, or accept pinned host memory.
+
+_F16, _F32 = torch.float16, torch.float32
+_INDEX = (torch.int32, getattr(torch, "uint32", torch.int32))
+
+
+def _current_stream(dev: int, stream) -> int:
+    """Handle of `stream`, or of the device's current stream (without the Stream
+    object that torch.cuda.current_stream builds, where torch offers that)."""
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+
+
+def _device() -> int:
+    """The current device, or -2 (no tensor's device) where there is none."""
+    try:
+        return torch.cuda.current_device()
+    except (RuntimeError, AssertionError):
+        return -2
+
 
 class RopeScaling:
     """Frequencies of a rotation scaled for long contexts (enum dattn_rope_scaling):
@@ -477,43 +504,44 @@ class RopeScaling:
 
 def _rope_params(head_dim: int, rope_dims: int, rope_base: float, traditional: bool,
                  scaling) -> RopeParams:
-    if scaling is not None and not isinstance(scaling, RopeScaling):
-        raise TypeError(f"scaling must be a RopeScaling, got {type(scaling).__name__}")
     if scaling is None:
-        return RopeParams(rope_dims or head_dim, 1 if traditional else 0, float(rope_base), 0, 1.0,
-                          0.0, 0.0, 0.0, 1.0)
-    return RopeParams(rope_dims or head_dim, 1 if traditional else 0, float(rope_base),
+        return RopeParams(rope_dims or head_dim, 1 if traditional else 0, rope_base, 0, 1.0, 0.0,
+                          0.0, 0.0, 1.0)
+    if not isinstance(scaling, RopeScaling):
+        raise TypeError(f"scaling must be a RopeScaling, got {type(scaling).__name__}")
+    return RopeParams(rope_dims or head_dim, 1 if traditional else 0, rope_base,
                       _ROPE_SCALINGS[scaling.kind], scaling.factor, scaling.original_len,
                       scaling.low_turns, scaling.high_turns, scaling.magnitude)
 
 
-def _on_device(named) -> None:
+def _on_device(named, dev: int) -> None:
     """Every CUDA tensor on the current device, whose stream the call goes to."""
-    dev = torch.cuda.current_device()
     for name, t in named:
         if t.is_cuda and t.get_device() != dev:
             raise ValueError(f"{name} is on cuda:{t.get_device()}, the current device is "
                              f"cuda:{dev}")
 
 
-def _like(shape, dtype, device, stream):
-    """A tensor from the pool of the stream that the call goes to."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _like(t, stream, shape=None, dtype=None):
+    """A tensor (as `t`, or of that shape and type) from the pool of the stream that
+    the call goes to."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _like(t, None, shape, dtype)
+    if shape is None:
+        return torch.empty_like(t, memory_format=torch.contiguous_format)
+    return torch.empty(shape, dtype=dtype, device=t.device)
 
 
-def _index32(t, name: str, shape) -> int:
-    if isinstance(t, torch.Tensor) and t.dtype not in (torch.int32,
-                                                       getattr(torch, "uint32", torch.int32)):
+def _index32(t, name: str, shape) -> None:
+    if isinstance(t, torch.Tensor) and t.dtype not in _INDEX:
         raise TypeError(f"{name} must be int32 or uint32, got {t.dtype}")
-    return _tensor(t, name, shape, getattr(t, "dtype", torch.int32))
+    _tensor(t, name, shape, getattr(t, "dtype", torch.int32))
 
 
-def _tokens(t, name: str, dtype) -> tuple[int, int]:
-    """Pointer and token stride of a [tokens, heads, head_dim] tensor whose tokens
-    are dense inside and may lie apart (a slice of a fused projection)."""
+def _tokens(t, name: str, dtype, shape=None) -> None:
+    """Check a [tokens, heads, head_dim] tensor whose tokens are dense inside and may
+    lie apart (a slice of a fused projection)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -526,25 +554,43 @@ def _tokens(t, name: str, dtype) -> tuple[int, int]:
     s0, s1, s2 = t.stride()
     if (s2 != 1 and d > 1) or (s1 != d and h > 1):
         raise ValueError(f"{name}: the heads of a token must be contiguous, strides are {t.stride()}")
-    return t.data_ptr(), (s0 if n > 1 else h * d)
+    if shape is not None and tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+
+
+def _token_stride(t) -> int:
+    n, h, d = t.shape
+    return t.stride(0) if n > 1 else h * d
+
+
+def _rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream) -> None:
+    dev = _device()
+    dtype = x.dtype
+    if not (dtype in _DTYPES and out.dtype is dtype and x.ndim == 3 and out.shape == x.shape
+            and x.is_contiguous() and out.is_contiguous() and x.get_device() == dev
+            and out.get_device() == dev and positions.dtype in _INDEX
+            and positions.get_device() == dev and positions.shape == x.shape[:1]
+            and positions.is_contiguous()):
+        if dtype not in _DTYPES:
+            raise TypeError(f"x must be float16, bfloat16 or float32, got {dtype}")
+        _tokens(x, "x", dtype)
+        _tokens(out, "out", dtype, x.shape)
+        _index32(positions, "positions", x.shape[:1])
+        _on_device((("x", x), ("out", out), ("positions", positions)), dev)
+    n, h, d = x.shape
+    _check(load().dattn_rope(x.data_ptr(), out.data_ptr(), _DTYPES[dtype], n, h, d,
+                             _token_stride(x), _token_stride(out), positions.data_ptr(),
+                             _rope_params(d, rope_dims, rope_base, traditional, scaling),
+                             1 if gradient else 0, _current_stream(dev, stream)), "dattn_rope")
 
 
 def dattn_rope(x, out, positions, rope_dims: int = 0, rope_base: float = 10000.0,
                traditional: bool = False, scaling=None, gradient: bool = False,
                stream=None) -> None:
-    dtype = getattr(x, "dtype", None)
-    if dtype not in _DTYPES:
-        raise TypeError(f"x must be float16, bfloat16 or float32, got {dtype}")
-    xp, xs = _tokens(x, "x", dtype)
-    op, os_ = _tokens(out, "out", dtype)
-    n, h, d = x.shape
-    if out.shape != x.shape:
-        raise ValueError(f"out has shape {tuple(out.shape)}, expected {tuple(x.shape)}")
-    pp = _index32(positions, "positions", (n,))
-    _on_device((("x", x), ("out", out), ("positions", positions)))
-    _check(load().dattn_rope(xp, op, _DTYPES[dtype], n, h, d, xs, os_, pp,
-                             _rope_params(d, rope_dims, rope_base, traditional, scaling),
-                             1 if gradient else 0, _stream_handle(stream)), "dattn_rope")
+    for name, t in (("x", x), ("out", out), ("positions", positions)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    _rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
 
 
 def rope(x, positions, rope_dims: int = 0, rope_base: float = 10000.0, traditional: bool = False,
@@ -552,14 +598,13 @@ def rope(x, positions, rope_dims: int = 0, rope_base: float = 10000.0, tradition
     """Rotate x [tokens, heads, head_dim] (f16, bf16 or f32) at ``positions``; with
     ``gradient`` the gradient of the rotated tensor into that of the tensor."""
     if out is None:
-        out = _like(x.shape, x.dtype, x.device, stream)
-    dattn_rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
+        out = _like(x, stream)
+    _rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
     return out
 
 
-def _q8_cache(k, v, k_scale, v_scale, scale_block: int, block_table, batch: int):
-    """Shapes and pointers of an 8-bit cache: (kv_type, n_kv_heads, head_dim,
-    capacity, page geometry or None, pointers)."""
+def _q8_checks(k, v, k_scale, v_scale, scale_block, block_table, batch, current_pos) -> None:
+    """Name what is wrong with an 8-bit cache, its table or the positions."""
     if not isinstance(k, torch.Tensor) or k.dtype not in _KV_TYPES:
         raise TypeError("the cache must be float8_e4m3fn or int8, got "
                         f"{getattr(k, 'dtype', type(k).__name__)}")
@@ -572,17 +617,39 @@ def _q8_cache(k, v, k_scale, v_scale, scale_block: int, block_table, batch: int)
     if block_table is None and lead != batch:
         raise ValueError(f"the cache holds {lead} sequences, the batch {batch}")
     sshape = (lead, -(-rows // scale_block), hk)
-    ptrs = (_tensor(k, "K cache", k.shape, k.dtype), _tensor(v, "V cache", k.shape, k.dtype),
-            _tensor(k_scale, "K_scale", sshape, torch.float32),
-            _tensor(v_scale, "V_scale", sshape, torch.float32))
-    pages = None
+    _tensor(k, "K cache", k.shape, k.dtype)
+    _tensor(v, "V cache", k.shape, k.dtype)
+    _tensor(k_scale, "K_scale", sshape, _F32)
+    _tensor(v_scale, "V_scale", sshape, _F32)
     if block_table is not None:
         if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
             raise ValueError("block_table must be [batch, max_pages]")
-        table = _tensor(block_table, "block_table", (batch, block_table.shape[1]), torch.int32)
-        pages = (rows, block_table.shape[1], lead, table)
-        rows = rows * block_table.shape[1]
-    return _KV_TYPES[k.dtype], hk, d, rows, pages, ptrs
+        _tensor(block_table, "block_table", (batch, block_table.shape[1]), torch.int32)
+    _index32(current_pos, "current_pos", (batch,))
+
+
+def _q8_ordinary(k, v, k_scale, v_scale, scale_block, block_table, batch, current_pos, dev) -> bool:
+    """Whether the cache and its companions are what an ordinary call brings."""
+    dtype, shape = k.dtype, k.shape
+    return (dtype in _KV_TYPES and v.dtype is dtype and k.ndim == 4 and v.shape == shape
+            and scale_block > 0 and k_scale.dtype is _F32 and v_scale.dtype is _F32
+            and k_scale.shape == (shape[0], -(-shape[1] // scale_block), shape[2])
+            and v_scale.shape == k_scale.shape and k.is_contiguous() and v.is_contiguous()
+            and k_scale.is_contiguous() and v_scale.is_contiguous() and k.get_device() == dev
+            and v.get_device() == dev and k_scale.get_device() == dev
+            and v_scale.get_device() == dev and current_pos.dtype in _INDEX
+            and current_pos.shape == (batch,) and current_pos.is_contiguous()
+            and current_pos.get_device() == dev
+            and (shape[0] == batch if block_table is None else
+                 (block_table.dtype is torch.int32 and block_table.ndim == 2
+                  and block_table.shape[0] == batch and block_table.is_contiguous()
+                  and block_table.get_device() == dev)))
+
+
+def _all_tensors(**named) -> None:
+    for name, t in named.items():
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
 
 
 def dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, v_scale,
@@ -590,38 +657,56 @@ def dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, 
                          rope_base: float = 10000.0, traditional: bool = False, scaling=None,
                          block_table=None, stream=None) -> None:
     """The dense call, or the paged one when ``block_table`` is given."""
-    qp, qs = _tokens(q_new, "q_new", torch.float16)
-    kp, kstr = _tokens(k_new, "k_new", torch.float16)
-    vp, vstr = _tokens(v_new, "v_new", torch.float16)
+    _all_tensors(q_new=q_new, k_new=k_new, v_new=v_new, q_out=q_out, k_cache=k_cache,
+                 v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, current_pos=current_pos)
+    dev = _device()
+    batch = current_pos.shape[0] if current_pos.ndim == 1 else -1
+    if not (_q8_ordinary(k_cache, v_cache, k_scale, v_scale, scale_block, block_table, batch,
+                         current_pos, dev)
+            and q_new.dtype is _F16 and k_new.dtype is _F16 and v_new.dtype is _F16
+            and q_out.dtype is _F16 and q_new.ndim == 3 and q_out.shape == q_new.shape
+            and k_new.shape == (q_new.shape[0], k_cache.shape[2], q_new.shape[2])
+            and v_new.shape == k_new.shape and q_new.shape[2] == k_cache.shape[3]
+            and q_new.is_contiguous() and k_new.is_contiguous() and v_new.is_contiguous()
+            and q_out.is_contiguous() and q_new.get_device() == dev and k_new.get_device() == dev
+            and v_new.get_device() == dev and q_out.get_device() == dev
+            and (q_new.shape[0] == batch if token_offsets is None else
+                 (token_offsets.dtype is torch.int32 and token_offsets.shape == (batch + 1,)
+                  and token_offsets.is_contiguous() and token_offsets.get_device() == dev))):
+        _q8_checks(k_cache, v_cache, k_scale, v_scale, scale_block, block_table, batch, current_pos)
+        _tokens(q_new, "q_new", _F16)
+        n, _, d = q_new.shape
+        hk, dc = k_cache.shape[2:]
+        if d != dc:
+            raise ValueError(f"q_new has head_dim {d}, the cache {dc}")
+        _tokens(k_new, "k_new", _F16, (n, hk, d))
+        _tokens(v_new, "v_new", _F16, (n, hk, d))
+        _tensor(q_out, "q_out", q_new.shape)
+        if token_offsets is not None:
+            _tensor(token_offsets, "token_offsets", (batch + 1,), torch.int32)
+        elif n != batch:
+            raise ValueError(f"without token_offsets each sequence brings one token: {n} tokens, "
+                             f"{batch} sequences")
+        _on_device([(name, t) for name, t in
+                    (("q_new", q_new), ("k_new", k_new), ("v_new", v_new), ("q_out", q_out),
+                     ("K cache", k_cache), ("V cache", v_cache), ("K_scale", k_scale),
+                     ("V_scale", v_scale), ("current_pos", current_pos),
+                     ("token_offsets", token_offsets), ("block_table", block_table))
+                    if t is not None], dev)
     n, h, d = q_new.shape
-    batch = current_pos.shape[0] if getattr(current_pos, "ndim", 0) == 1 else -1
-    cp = _index32(current_pos, "current_pos", (batch,))
-    kv, hk, dc, seq_len, pages, ptrs = _q8_cache(k_cache, v_cache, k_scale, v_scale, scale_block,
-                                                 block_table, batch)
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t.shape != (n, hk, dc):
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(n, hk, dc)}")
-    if d != dc:
-        raise ValueError(f"q_new has head_dim {d}, the cache {dc}")
-    op = _tensor(q_out, "q_out", q_new.shape)
-    tp = None
-    if token_offsets is not None:
-        tp = _tensor(token_offsets, "token_offsets", (batch + 1,), torch.int32)
-    elif n != batch:
-        raise ValueError(f"without token_offsets each sequence brings one token: {n} tokens, "
-                         f"{batch} sequences")
-    _on_device((("q_new", q_new), ("k_new", k_new), ("v_new", v_new), ("q_out", q_out),
-                ("K cache", k_cache), ("V cache", v_cache), ("K_scale", k_scale),
-                ("V_scale", v_scale), ("current_pos", current_pos)))
-    rp = _rope_params(d, rope_dims, rope_base, traditional, scaling)
-    s = _stream_handle(stream)
-    if pages is None:
-        _check(load().dattn_rope_append_q8(qp, kp, vp, op, *ptrs, kv, scale_block, batch, n, tp, qs,
-                                           kstr, vstr, h, hk, d, seq_len, rp, cp, s),
-               "dattn_rope_append_q8")
+    lead, rows, hk, _ = k_cache.shape
+    args = (q_new.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(),
+            k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            _KV_TYPES[k_cache.dtype], scale_block, batch, n,
+            None if token_offsets is None else token_offsets.data_ptr(), _token_stride(q_new),
+            _token_stride(k_new), _token_stride(v_new), h, hk, d, rows)
+    tail = (_rope_params(d, rope_dims, rope_base, traditional, scaling), current_pos.data_ptr(),
+            _current_stream(dev, stream))
+    if block_table is None:
+        _check(load().dattn_rope_append_q8(*args, *tail), "dattn_rope_append_q8")
     else:
-        _check(load().dattn_rope_append_paged_q8(qp, kp, vp, op, *ptrs, kv, scale_block, batch, n,
-                                                 tp, qs, kstr, vstr, h, hk, d, *pages, rp, cp, s),
+        _check(load().dattn_rope_append_paged_q8(*args, block_table.shape[1], lead,
+                                                 block_table.data_ptr(), *tail),
                "dattn_rope_append_paged_q8")
 
 
@@ -634,7 +719,7 @@ def rope_append_q8(q_new, k_new, v_new, k_cache, v_cache, k_scale, v_scale, curr
     ``token_offsets`` [batch + 1].  ``current_pos`` holds the position of each
     sequence's last new token.  Returns the rotated q."""
     if q_out is None:
-        q_out = _like(q_new.shape, q_new.dtype, q_new.device, stream)
+        q_out = _like(q_new, stream)
     dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, v_scale,
                          current_pos, scale_block, token_offsets, rope_dims, rope_base, traditional,
                          scaling, block_table, stream)
@@ -652,10 +737,7 @@ def dattn_decode_q8_plan(batch: int, n_heads: int, n_kv_heads: int, head_dim: in
 _Q8_WORKSPACE: dict[tuple, int] = {}  # the size depends on the shape and the device only
 
 
-def dattn_decode_q8_workspace_bytes(batch: int, n_heads: int, n_kv_heads: int, head_dim: int,
-                                    seq_len: int, num_partitions: int = 0) -> int:
-    key = (torch.cuda.current_device(), batch, n_heads, n_kv_heads, head_dim, seq_len,
-           num_partitions)
+def _q8_workspace(*key) -> int:
     n = _Q8_WORKSPACE.get(key)
     if n is None:
         size = ctypes.c_size_t(0)
@@ -665,52 +747,72 @@ def dattn_decode_q8_workspace_bytes(batch: int, n_heads: int, n_kv_heads: int, h
     return n
 
 
-def dattn_decode_q8(q, k, v, k_scale, v_scale, out, current_pos, scale_block: int, workspace=None,
-                    num_partitions: int = 0, block_table=None, stream=None) -> None:
-    """The dense call, or the paged one when ``block_table`` is given."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("Q must be [batch, n_heads, head_dim]")
+def dattn_decode_q8_workspace_bytes(batch: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                                    seq_len: int, num_partitions: int = 0) -> int:
+    return _q8_workspace(_device(), batch, n_heads, n_kv_heads, head_dim,
+                         seq_len, num_partitions)
+
+
+def _decode_q8(q, k, v, k_scale, v_scale, block_table, current_pos, scale_block, num_partitions,
+               out, workspace, stream, allocate):
+    _all_tensors(Q=q, k_cache=k, v_cache=v, k_scale=k_scale, v_scale=v_scale,
+                 current_pos=current_pos)
+    dev = _device()
+    batch = q.shape[0] if q.ndim == 3 else -1
+    fresh = out is None and allocate
+    if not (_q8_ordinary(k, v, k_scale, v_scale, scale_block, block_table, batch, current_pos, dev)
+            and q.dtype is _F16 and q.ndim == 3 and q.shape[2] == k.shape[3] and q.is_contiguous()
+            and q.get_device() == dev
+            and (fresh or (out.dtype is _F16 and out.shape == q.shape and out.is_contiguous()
+                           and out.get_device() == dev))):
+        if q.dim() != 3:
+            raise ValueError("Q must be [batch, n_heads, head_dim]")
+        _q8_checks(k, v, k_scale, v_scale, scale_block, block_table, batch, current_pos)
+        if q.shape[2] != k.shape[3]:
+            raise ValueError(f"Q has head_dim {q.shape[2]}, the cache {k.shape[3]}")
+        _tensor(q, "Q")
+        named = [("Q", q), ("K cache", k), ("V cache", v), ("K_scale", k_scale),
+                 ("V_scale", v_scale), ("current_pos", current_pos)]
+        if not fresh:
+            _tensor(out, "out", q.shape)
+            named.append(("out", out))
+        if block_table is not None:
+            named.append(("block_table", block_table))
+        _on_device(named, dev)
+    handle = _current_stream(dev, stream)
     b, h, d = q.shape
-    kv, hk, dc, seq_len, pages, ptrs = _q8_cache(k, v, k_scale, v_scale, scale_block, block_table, b)
-    if d != dc:
-        raise ValueError(f"Q has head_dim {d}, the cache {dc}")
-    qp, op = _tensor(q, "Q"), _tensor(out, "out", q.shape)
-    cp = _index32(current_pos, "current_pos", (b,))
-    _on_device((("Q", q), ("K cache", k), ("V cache", v), ("K_scale", k_scale),
-                ("V_scale", v_scale), ("out", out), ("current_pos", current_pos)))
+    lead, rows, hk, _ = k.shape
+    seq_len = rows if block_table is None else rows * block_table.shape[1]
+    need = _q8_workspace(dev, b, h, hk, d, seq_len, num_partitions) if workspace is None else 0
+    if handle in _RECORDING and allocate and (fresh or need):
+        raise ValueError("a recorded decode needs buffers that outlive the batch: pass out and "
+                         "workspace (dattn_decode_q8_workspace_bytes)")
+    if need and allocate:
+        workspace = _like(k, stream, (need,), torch.uint8)
+    if fresh:
+        out = _like(q, stream) if q.is_cuda else _like(k, stream, q.shape, _F16)
     wp, wn = None, 0
     if workspace is not None:
         wp = _tensor(workspace, "workspace", None, workspace.dtype)
         wn = workspace.numel() * workspace.element_size()
-    s = _stream_handle(stream)
-    if pages is None:
-        _check(load().dattn_decode_q8(qp, *ptrs, op, kv, scale_block, b, h, hk, d, seq_len, cp, wp,
-                                      wn, num_partitions, s), "dattn_decode_q8")
+    args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+            out.data_ptr(), _KV_TYPES[k.dtype], scale_block, b, h, hk, d, rows)
+    if block_table is None:
+        _check(load().dattn_decode_q8(*args, current_pos.data_ptr(), wp, wn, num_partitions,
+                                      handle), "dattn_decode_q8")
     else:
-        page_size, max_pages, num_pages, table = pages
-        _check(load().dattn_decode_paged_q8(qp, *ptrs, op, kv, scale_block, b, h, hk, d, page_size,
-                                            max_pages, num_pages, table, cp, wp, wn, num_partitions,
-                                            s), "dattn_decode_paged_q8")
-
-
-def _decode_q8(q, k, v, k_scale, v_scale, block_table, current_pos, scale_block, num_partitions,
-               out, workspace, stream):
-    if workspace is None and _RECORDING and _stream_handle(stream) in _RECORDING:
-        raise ValueError("a recorded decode needs a workspace that outlives the batch: pass "
-                         "workspace (dattn_decode_q8_workspace_bytes) and out")
-    if q.dim() != 3 or k.dim() != 4:
-        raise ValueError("Q must be [batch, n_heads, head_dim], the cache 4-dimensional")
-    if out is None:
-        out = _like(q.shape, torch.float16, k.device, stream)
-    if workspace is None:
-        b, h, d = q.shape
-        rows = k.shape[1] if block_table is None else k.shape[1] * block_table.shape[1]
-        n = dattn_decode_q8_workspace_bytes(b, h, k.shape[2], d, rows, num_partitions)
-        if n:
-            workspace = _like((n,), torch.uint8, k.device, stream)
-    dattn_decode_q8(q, k, v, k_scale, v_scale, out, current_pos, scale_block, workspace,
-                    num_partitions, block_table, stream)
+        _check(load().dattn_decode_paged_q8(*args, block_table.shape[1], lead,
+                                            block_table.data_ptr(), current_pos.data_ptr(), wp, wn,
+                                            num_partitions, handle), "dattn_decode_paged_q8")
     return out
+
+
+def dattn_decode_q8(q, k, v, k_scale, v_scale, out, current_pos, scale_block: int, workspace=None,
+                    num_partitions: int = 0, block_table=None, stream=None) -> None:
+    """The dense call, or the paged one when ``block_table`` is given."""
+    _all_tensors(out=out)
+    _decode_q8(q, k, v, k_scale, v_scale, block_table, current_pos, scale_block, num_partitions,
+               out, workspace, stream, False)
 
 
 def decode_q8(q, k, v, k_scale, v_scale, current_pos, scale_block: int, num_partitions: int = 0,
@@ -719,7 +821,7 @@ def decode_q8(q, k, v, k_scale, v_scale, current_pos, scale_block: int, num_part
     (float8_e4m3fn or int8) with scales [batch, ceil(seq_len / scale_block),
     n_kv_heads]; allocates ``out`` and the workspace if not given."""
     return _decode_q8(q, k, v, k_scale, v_scale, None, current_pos, scale_block, num_partitions,
-                      out, workspace, stream)
+                      out, workspace, stream, True)
 
 
 def decode_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, current_pos,
@@ -728,4 +830,4 @@ def decode_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, current_
     """Fused decode over a paged 8-bit cache [num_pages, page_size, n_kv_heads,
     head_dim] with scales [num_pages, page_size / scale_block, n_kv_heads]."""
     return _decode_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, current_pos, scale_block,
-                      num_partitions, out, workspace, stream)
+                      num_partitions, out, workspace, stream, True)

@@ -56,15 +56,17 @@ __global__ void __launch_bounds__(kThreads, INFLIGHT <= 2 ? 8 : (INFLIGHT <= 4 ?
     const long long u = b * a.head_groups + g;
 
     const int tid = threadIdx.x;
-    const long long Lb = merge::live_len(a.cur_pos, b, a.S);
-    // Live positions before sequence b and in total.  For batches of up to
+    // lengths in units of 2^shift positions, rounded up, and `extra` units ahead
+    const int up = (1 << a.shift) - 1;
+    const long long Lb = ((merge::live_len(a.cur_pos, b, a.S) + up) >> a.shift) + a.extra;
+    // Live positions (or units of them) before sequence b and in total.  For batches of up to
     // kInlinePrefix sequences they are summed here from current_pos (an input,
     // readable before the decode kernel finishes); larger batches read the
     // prefix sums the decode kernel wrote.
     long long before = 0, total = 0;
     if (a.B <= kInlinePrefix) {
         for (int i = tid; i < a.B; i += kThreads) {
-            const long long L = merge::live_len(a.cur_pos, i, a.S);
+            const long long L = ((merge::live_len(a.cur_pos, i, a.S) + up) >> a.shift) + a.extra;
             total += L;
             if (i < b) before += L;
         }
@@ -98,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, INFLIGHT <= 2 ? 8 : (INFLIGHT <= 4 ?
     const long long nhg = a.head_groups;
     const long long W = nhg * total;
     const long long Pu = nhg * before + g * Lb;
-    const long long c_first = range_owner(Pu, W, a.partitions);
+    const long long c_first = range_owner(Pu + a.extra, W, a.partitions);
     const long long c_last = range_owner(Pu + Lb - 1, W, a.partitions);
     if (c_first == c_last) return;  // written whole by the decode kernel
     const int npieces = static_cast<int>(c_last - c_first + 1);

@@ -97,6 +97,8 @@ struct CombineArgs {
     int partitions;
     int chunk;     // channels per combine CTA (a multiple of 8)
     int inflight;  // piece loads per thread per round: 2, 4 or 8
+    int shift;     // the ranges are cut in units of 2^shift positions (0 or kQ8TileShift)
+    int extra;     // units ahead of a unit's own that belong to no piece
 };
 
 // Compile-time shape of one decode-kernel instance.
@@ -177,14 +179,31 @@ inline FastDiv fast_div_of(int d) {
 // 8-bit cache types (enum dattn_kv_type).
 constexpr int kKvE4m3 = 1, kKvInt8 = 2;
 
+constexpr int kQ8Tile = 16, kQ8TileShift = 4;  // positions per tile of the 8-bit decode
+
 // Bytes of one ring slot of the 8-bit decode: 16 positions of K and V, DP bytes
 // per row, and their 32 scales.
 __host__ __device__ constexpr int q8_tile_bytes(int dp) { return 32 * dp + 128; }
 
+// Warps of a decode CTA, CTAs of an SM and ring slots of a warp, by the row size and
+// the 8-column tiles of query heads.
+#ifndef Q8_SMALL_WARPS
+#define Q8_SMALL_WARPS 8
+#endif
+__host__ __device__ constexpr bool q8_small(int dp, int nt) { return dp * nt <= 128; }
+__host__ __device__ constexpr int q8_warps(int dp, int nt) { return q8_small(dp, nt) ? Q8_SMALL_WARPS : 8; }
+__host__ __device__ constexpr int q8_ctas_per_sm(int dp, int nt) {
+    return q8_small(dp, nt) ? 16 / Q8_SMALL_WARPS : 1;
+}
+__host__ __device__ constexpr int q8_slots(int dp, int nt) {
+    return 212 * 1024 / (q8_warps(dp, nt) * q8_ctas_per_sm(dp, nt)) / q8_tile_bytes(dp);
+}
+
 // Arguments of the decode kernel over an 8-bit cache (decode_q8.cu).  A virtual
 // head is a group of gq query heads of one key/value head (a key/value head has
 // vheads_per_kv of them); units are (sequence, group of heads_per_cta virtual
-// heads) and the flattened positions are cut as in DecodeArgs.
+// heads) and the flattened tiles of kQ8Tile positions are cut as DecodeArgs cuts
+// positions.
 struct Q8DecodeArgs {
     const void *Q;               // f16 [B,H,D]
     const unsigned char *K, *V;  // [B,S,Hk,D], or pages [num_pages,page_size,Hk,D]
@@ -199,19 +218,23 @@ struct Q8DecodeArgs {
     long long num_pages;
     int page_size, max_pages;
     int scale_rows;              // scale blocks of a sequence (dense) or of a page
-    FastDiv div_page, div_block;
+    FastDiv div_page, div_block, div_gq;
+    int tile_in_page;            // no tile crosses a page (always, in a dense cache)
     int B, H, D, S;
     int kv_heads, gq, vheads, vheads_per_kv;
     int heads_per_cta;           // virtual heads of a CTA
     int head_groups;
     int phases;                  // warps that share a virtual head
-    int partitions;
+    int partitions;              // CTAs
+    int extra;                   // split plan: tiles that a unit counts beyond its own
+    int cluster;                 // CTAs per unit, merged in shared memory; 0: the split plan
     float qscale;                // log2(e) / sqrt(D)
 };
-// Warps of a CTA and ring slots of a warp for rows of dp bytes and nt column tiles.
-bool decode_q8_shape(int dp, int nt, int *warps, int *slots);
-cudaError_t decode_q8_configure();
-cudaError_t launch_decode_q8(const Q8DecodeArgs &a, int dp, int nt, int kv, cudaStream_t stream);
+cudaError_t decode_q8_configure(int max_smem);
+// Clusters of `cluster` CTAs that can be resident at once.
+cudaError_t decode_q8_max_clusters(int dp, int nt, int smem, int cluster, int *clusters);
+cudaError_t launch_decode_q8(const Q8DecodeArgs &a, int dp, int nt, int kv, int smem,
+                             cudaStream_t stream);
 
 // The combine kernel's launch shape for G partitions over `units` units: the
 // chunk of channels per CTA (at most ~8 pieces per thread of a 128-thread CTA,

@@ -22,6 +22,13 @@ namespace {
 constexpr int kMaxHeadDim = 256;
 constexpr int kMaxPartitions = 65535;
 constexpr int kMaxColumns = 16;  // query heads of a key/value head in one CTA
+constexpr int kStaticSmem = 4096;  // the decode kernel's static shared memory at most
+// Tiles of a warp up to which the cluster plan is taken.  Measured (cluster, split):
+// one 7B-class step of 8 key/value heads, 2 tiles, 8.4 and 8.7 us; of 32, 4 tiles, 9.9
+// and 12.1; 32 ragged sequences of 8 heads, 8 tiles, 13.6 and 16.0; 37 of 4 heads, 8
+// tiles, 14.7 and 16.2; 64 query on 8 key/value heads over 32768 positions, 16 tiles
+// and 7 in the split plan, 26.6 and 18.1.
+constexpr long long kClusterTiles = 8;
 
 int fail(int status, const char *fmt, ...) {
     char buf[512];
@@ -171,8 +178,11 @@ int check_cache(int batch, int n_heads, int n_kv_heads, int head_dim, int seq_le
                     head_dim, kMaxHeadDim);
     if (c.scale_block <= 0)
         return fail(DATTN_ERR_INVALID_ARG, "scale_block=%d must be positive", c.scale_block);
+    // rows of the cache are counted in 31 bits
     const double lead = c.page_size > 0 ? static_cast<double>(c.num_pages) * c.page_size
                                         : static_cast<double>(batch) * seq_len;
+    if (lead >= 2147483648.0 || static_cast<double>(n_kv_heads) * head_dim >= 2147483648.0)
+        return fail(DATTN_ERR_UNSUPPORTED, "the cache must hold fewer than 2^31 positions in all");
     if (lead * n_kv_heads * head_dim > 4.0e18 ||
         static_cast<double>(batch) * n_heads * head_dim > 4.0e18)
         return fail(DATTN_ERR_INVALID_ARG, "the cache is too large");
@@ -205,11 +215,52 @@ struct Plan {
     int dp = 0, nt = 0, warps = 0, slots = 0;
     int gq = 0, vheads = 0, vheads_per_kv = 0;
     int HG = 0, NHG = 0, PH = 0, G = 0, sms = 0;
+    int cluster = 0, smem = 0, ctas_per_sm = 1, extra = 0;
     int combine_chunk = 0, combine_inflight = 0;
     size_t prefix_bytes = 0, acc_bytes = 0, ws_bytes = 0;
 };
 
 size_t round_up(size_t x, size_t m) { return (x + m - 1) / m * m; }
+
+// The cluster plan in place of the split plan *p, for calls bound by latency: a cluster
+// of C CTAs for each (sequence, group of heads), all resident at once, merged in the
+// same launch.  Of the head groups and cluster sizes that fit, the one with the fewest
+// tiles for a warp at full length; then fewer CTAs.
+int cluster_plan(int B, int D, long long tiles, const dattn::DeviceFacts &df, Plan *p) {
+    long long best = 0;
+    Plan found;
+    for (int hg = 1; hg <= std::min(p->vheads, p->warps); hg *= 2) {
+        const long long units = static_cast<long long>(B) * ((p->vheads + hg - 1) / hg);
+        const int ph = p->warps / hg;
+        for (int C = 1; C <= 16 && units * C <= df.sms * p->ctas_per_sm; C *= 2) {
+            const long long per_warp = ((tiles + C - 1) / C + ph - 1) / ph;
+            if (best != 0 && per_warp >= best) continue;
+            // the records of a CTA's share of the unit's (query head, channel pair) outputs
+            const long long rec = C > 1 ? (hg * p->gq * (p->dp / 2) + C - 1) / C * C * 16LL : 0;
+            const long long smem = static_cast<long long>(p->warps) * p->slots * dattn::q8_tile_bytes(p->dp) + rec;
+            if (smem > df.max_smem_optin - kStaticSmem) continue;
+            int fit = 0;
+            if (dattn::decode_q8_max_clusters(p->dp, p->nt, static_cast<int>(smem), C, &fit) != cudaSuccess) {
+                cudaGetLastError();  // this cluster size is not available
+                continue;
+            }
+            if (fit < units) continue;
+            best = per_warp;
+            found = *p;
+            found.HG = hg;
+            found.NHG = (p->vheads + hg - 1) / hg;
+            found.PH = ph;
+            found.cluster = C;
+            found.G = static_cast<int>(units * C);
+            found.smem = static_cast<int>(smem);
+        }
+    }
+    // The split plan costs a second launch and the states' way through memory, about
+    // two tiles of a warp; the cluster plan waits for its longest sequence.
+    const double split = static_cast<double>(B) * p->NHG * tiles / (static_cast<double>(p->G) * p->PH);
+    if (best > 0 && best <= kClusterTiles && best <= split + 2.0) *p = found;
+    return DATTN_OK;
+}
 
 int make_plan(int B, int H, int Hk, int D, int S, int num_partitions, Plan *out) {
     if (num_partitions < 0)
@@ -231,7 +282,7 @@ int make_plan(int B, int H, int Hk, int D, int S, int num_partitions, Plan *out)
         return DATTN_OK;
     }
     if (!configured[dev]) {
-        e = dattn::decode_q8_configure();
+        e = dattn::decode_q8_configure(df.max_smem_optin);
         if (e != cudaSuccess) return fail_cuda(e, "cudaFuncSetAttribute(8-bit decode kernel)");
         configured[dev] = true;
     }
@@ -246,37 +297,54 @@ int make_plan(int B, int H, int Hk, int D, int S, int num_partitions, Plan *out)
     p.vheads = Hk * p.vheads_per_kv;
     p.nt = p.gq > 8 ? 2 : 1;
     p.dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-    if (!dattn::decode_q8_shape(p.dp, p.nt, &p.warps, &p.slots))
-        return fail(DATTN_ERR_UNSUPPORTED, "no kernel for head_dim=%d", D);
-    // heads per CTA: the most warps busy, more heads (longer runs of the cache
-    // per position) on a tie
+    p.warps = dattn::q8_warps(p.dp, p.nt);
+    p.slots = dattn::q8_slots(p.dp, p.nt);
+    p.ctas_per_sm = dattn::q8_ctas_per_sm(p.dp, p.nt);
+    // Heads per CTA, of those that keep the most warps busy.  More heads make longer
+    // runs of the cache per position (one 1 GiB sequence of 32 heads: 158 us with 8,
+    // 171 with 4, 169 with 2, 189 with 1), fewer make fewer partial states to write
+    // and merge, (G + U) HG gq D floats of them (64 query on 8 key/value heads, 32768
+    // positions: 29 us with 8, 21 with 4, 19 with 2, 18 with 1).  Taken: the most
+    // heads whose states, written and read, stay within 1 % of the cache's capacity;
+    // else one.
+    const long long slots = static_cast<long long>(df.sms) * p.ctas_per_sm;
+    const double cache_bytes = 2.0 * B * S * static_cast<double>(Hk) * D;
     double best = 0.0;
-    for (int hg = std::min(p.vheads, p.warps); hg >= 1; --hg) {
+    for (int hg = 1; hg <= std::min(p.vheads, p.warps); ++hg) {
         const int nhg = (p.vheads + hg - 1) / hg;
         const double busy = static_cast<double>(p.vheads) / (static_cast<double>(nhg) * hg) *
                             (p.warps / hg * hg) / p.warps;
-        if (busy > best + 1e-9) {
-            best = busy;
+        const double states = (slots + static_cast<double>(B) * nhg) * hg * p.gq * D * 8.0;
+        if (busy > best + 1e-9 || (busy > best - 1e-9 && states <= 0.01 * cache_bytes)) {
+            best = std::max(best, busy);
             p.HG = hg;
             p.NHG = nhg;
         }
     }
     p.PH = p.warps / p.HG;
-    const double capacity = static_cast<double>(B) * p.NHG * S;
-    if (static_cast<double>(p.NHG) * S >= 2147483648.0)
-        return fail(DATTN_ERR_UNSUPPORTED, "head groups x seq_len must stay below 2^31");
+    p.smem = p.warps * p.slots * dattn::q8_tile_bytes(p.dp);
+    const long long tiles = (static_cast<long long>(S) + dattn::kQ8Tile - 1) / dattn::kQ8Tile;
+    // What beginning a unit costs a CTA (the first tiles' latency, the epilogue), in
+    // tiles of a warp.  Measured with 0, 2, 4 and 6: 64 ragged sequences of 32 heads
+    // 99, 92, 90.6, 92 us; 37 of 4 heads 21.1, 17.2, 16.4, 16.5 us.
+    p.extra = 4 * p.PH;
+    const double capacity = static_cast<double>(B) * p.NHG * tiles;
+    if (static_cast<double>(p.NHG) * (tiles + p.extra) >= 2147483648.0)
+        return fail(DATTN_ERR_UNSUPPORTED, "head groups x seq_len must stay below 2^35");
     if (num_partitions > 0) {
         p.G = std::min(num_partitions, kMaxPartitions);
     } else {
-        // one CTA per SM; fewer when a partition would hold less than one tile
-        // per warp
-        const long long tile = 16LL * p.PH;
-        const long long by_work = static_cast<long long>(capacity) / tile;
-        p.G = static_cast<int>(std::max(1LL, std::min<long long>(df.sms, by_work)));
+        // every resident CTA slot; fewer when a partition would hold less than one
+        // tile per warp
+        const long long by_work = static_cast<long long>(capacity) / p.PH;
+        p.G = static_cast<int>(
+            std::max(1LL, std::min<long long>(slots, by_work)));
     }
-    if (capacity * (p.G + 1.0) > 4.0e18)
-        return fail(DATTN_ERR_UNSUPPORTED, "batch of %.3g positions is too large", capacity);
-    if (p.G > 1) {
+    if (static_cast<double>(B) * p.NHG * (tiles + p.extra) * (p.G + 1.0) > 4.0e18)
+        return fail(DATTN_ERR_UNSUPPORTED, "batch of %.3g tiles is too large", capacity);
+    if (num_partitions == 0)
+        if (int st = cluster_plan(B, D, tiles, df, &p)) return st;
+    if (p.G > 1 && p.cluster == 0) {
         const size_t units = static_cast<size_t>(B) * p.NHG;
         const size_t rows = (static_cast<size_t>(p.G) + units) * p.HG * p.gq;
         p.prefix_bytes = round_up((static_cast<size_t>(B) + 1) * sizeof(long long), 256);
@@ -326,7 +394,8 @@ int decode(const void *Q, const void *K, const void *V, const float *K_scale, co
     a.vs = V_scale;
     a.out = out;
     a.cur_pos = current_pos;
-    if (p.G > 1) {
+    const bool split = p.G > 1 && p.cluster == 0;  // partial states go through the workspace
+    if (split) {
         a.ws_prefix = reinterpret_cast<long long *>(ws);
         a.ws_acc = reinterpret_cast<float *>(ws + p.prefix_bytes);
         a.ws_ml = reinterpret_cast<float2 *>(ws + p.prefix_bytes + p.acc_bytes);
@@ -345,16 +414,20 @@ int decode(const void *Q, const void *K, const void *V, const float *K_scale, co
     a.S = seq_len;
     a.kv_heads = n_kv_heads;
     a.gq = p.gq;
+    a.div_gq = dattn::fast_div_of(p.gq);
     a.vheads = p.vheads;
     a.vheads_per_kv = p.vheads_per_kv;
     a.heads_per_cta = p.HG;
     a.head_groups = p.NHG;
     a.phases = p.PH;
     a.partitions = p.G;
+    a.cluster = p.cluster;
+    a.extra = p.extra;
+    a.tile_in_page = c.page_size % dattn::kQ8Tile == 0 ? 1 : 0;
     a.qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(head_dim)));
-    cudaError_t e = dattn::launch_decode_q8(a, p.dp, p.nt, c.kv_type, stream);
+    cudaError_t e = dattn::launch_decode_q8(a, p.dp, p.nt, c.kv_type, p.smem, stream);
     if (e != cudaSuccess) return fail_cuda(e, "8-bit decode kernel launch");
-    if (p.G > 1) {
+    if (split) {
         dattn::CombineArgs m{};
         m.ws_acc = a.ws_acc;
         m.ws_ml = a.ws_ml;
@@ -370,6 +443,8 @@ int decode(const void *Q, const void *K, const void *V, const float *K_scale, co
         m.partitions = p.G;
         m.chunk = p.combine_chunk;
         m.inflight = p.combine_inflight;
+        m.shift = dattn::kQ8TileShift;
+        m.extra = p.extra;
         e = dattn::launch_combine(m, stream);
         if (e != cudaSuccess) return fail_cuda(e, "combine kernel launch");
     }
@@ -533,14 +608,14 @@ int dattn_decode_q8_plan(int batch, int n_heads, int n_kv_heads, int head_dim, i
         plan->partitions = p.G;
         plan->heads_per_cta = p.HG * p.gq;
         plan->head_groups = p.NHG;
-        plan->stage_positions = 16;
+        plan->stage_positions = dattn::kQ8Tile;
         plan->stages = p.slots;
         plan->threads_per_cta = p.warps * 32;
-        plan->smem_bytes = p.warps * p.slots * dattn::q8_tile_bytes(p.dp);
-        plan->ctas_per_sm = 1;
+        plan->smem_bytes = p.smem;
+        plan->ctas_per_sm = p.ctas_per_sm;
         plan->sm_count = p.sms;
         plan->workspace_bytes = p.ws_bytes;
-        plan->cluster_size = 0;
+        plan->cluster_size = p.cluster;
         return DATTN_OK;
     });
 }
