@@ -451,13 +451,17 @@ _F16, _F32 = torch.float16, torch.float32
 _INDEX = (torch.int32, getattr(torch, "uint32", torch.int32))
 
 
+# The current stream's handle, without the Stream object that torch.cuda.current_stream()
+# builds (3 us) where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _current_stream(dev: int, stream) -> int:
-    """Handle of `stream`, or of the device's current stream (without the Stream
-    object that torch.cuda.current_stream builds, where torch offers that)."""
     if stream is not None:
         return stream.cuda_stream
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
+    if _raw_stream is not None:
+        return _raw_stream(dev)
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def _device() -> int:
@@ -474,7 +478,8 @@ class RopeScaling:
     ``low_turns`` and ``high_turns``); ``magnitude`` multiplies the rotated
     channels.  Immutable; make it once and pass it to every call."""
 
-    __slots__ = ("kind", "factor", "original_len", "low_turns", "high_turns", "magnitude")
+    __slots__ = ("kind", "factor", "original_len", "low_turns", "high_turns", "magnitude",
+                 "_hash")
 
     def __init__(self, kind: str, factor: float, original_len: float = 0.0,
                  low_turns: float = 1.0, high_turns: float = 32.0, magnitude: float = 1.0):
@@ -484,6 +489,7 @@ class RopeScaling:
                         ("original_len", float(original_len)), ("low_turns", float(low_turns)),
                         ("high_turns", float(high_turns)), ("magnitude", float(magnitude))):
             object.__setattr__(self, name, v)
+        object.__setattr__(self, "_hash", hash(self._key()))
 
     def __setattr__(self, name, value):
         raise AttributeError("RopeScaling is immutable")
@@ -496,22 +502,31 @@ class RopeScaling:
         return isinstance(other, RopeScaling) and self._key() == other._key()
 
     def __hash__(self):
-        return hash(self._key())
+        return self._hash
 
     def __repr__(self):
-        return "RopeScaling(" + ", ".join(f"{n}={getattr(self, n)!r}" for n in self.__slots__) + ")"
+        return "RopeScaling(" + ", ".join(f"{n}={getattr(self, n)!r}" for n in self.__slots__[:-1]) + ")"
+
+
+_ROPE_PARAMS: dict[tuple, RopeParams] = {}  # read only once made; a program uses a few
 
 
 def _rope_params(head_dim: int, rope_dims: int, rope_base: float, traditional: bool,
                  scaling) -> RopeParams:
-    if scaling is None:
-        return RopeParams(rope_dims or head_dim, 1 if traditional else 0, rope_base, 0, 1.0, 0.0,
-                          0.0, 0.0, 1.0)
-    if not isinstance(scaling, RopeScaling):
-        raise TypeError(f"scaling must be a RopeScaling, got {type(scaling).__name__}")
-    return RopeParams(rope_dims or head_dim, 1 if traditional else 0, rope_base,
-                      _ROPE_SCALINGS[scaling.kind], scaling.factor, scaling.original_len,
-                      scaling.low_turns, scaling.high_turns, scaling.magnitude)
+    key = (rope_dims or head_dim, traditional, rope_base, scaling)
+    p = _ROPE_PARAMS.get(key)
+    if p is None:
+        if scaling is None:
+            extra = (0, 1.0, 0.0, 0.0, 0.0, 1.0)
+        elif isinstance(scaling, RopeScaling):
+            extra = (_ROPE_SCALINGS[scaling.kind], scaling.factor, scaling.original_len,
+                     scaling.low_turns, scaling.high_turns, scaling.magnitude)
+        else:
+            raise TypeError(f"scaling must be a RopeScaling, got {type(scaling).__name__}")
+        p = RopeParams(rope_dims or head_dim, 1 if traditional else 0, rope_base, *extra)
+        if len(_ROPE_PARAMS) < 256:
+            _ROPE_PARAMS[key] = p
+    return p
 
 
 def _on_device(named, dev: int) -> None:
@@ -529,6 +544,8 @@ def _like(t, stream, shape=None, dtype=None):
         with torch.cuda.stream(stream):
             return _like(t, None, shape, dtype)
     if shape is None:
+        if t.is_contiguous():
+            return torch.empty_like(t)
         return torch.empty_like(t, memory_format=torch.contiguous_format)
     return torch.empty(shape, dtype=dtype, device=t.device)
 
@@ -565,31 +582,39 @@ def _token_stride(t) -> int:
 
 def _rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream) -> None:
     dev = _device()
-    dtype = x.dtype
-    if not (dtype in _DTYPES and out.dtype is dtype and x.ndim == 3 and out.shape == x.shape
-            and x.is_contiguous() and out.is_contiguous() and x.get_device() == dev
-            and out.get_device() == dev and positions.dtype in _INDEX
-            and positions.get_device() == dev and positions.shape == x.shape[:1]
-            and positions.is_contiguous()):
+    try:
+        dtype, shape = x.dtype, x.shape
+        n, h, d = shape
+        xs = os_ = h * d
+        ordinary = (dtype in _DTYPES and out.dtype is dtype and out.shape == shape
+                    and x.is_contiguous() and out.is_contiguous() and positions.dtype in _INDEX
+                    and positions.shape == (n,) and positions.is_contiguous()
+                    and x.get_device() == dev == out.get_device()
+                    and positions.get_device() == dev)
+    except (AttributeError, TypeError, ValueError):  # not tensors, or not of three dimensions
+        ordinary = False
+    if not ordinary:
+        _all_tensors(x=x, out=out, positions=positions)
+        dtype = x.dtype
         if dtype not in _DTYPES:
             raise TypeError(f"x must be float16, bfloat16 or float32, got {dtype}")
         _tokens(x, "x", dtype)
         _tokens(out, "out", dtype, x.shape)
         _index32(positions, "positions", x.shape[:1])
         _on_device((("x", x), ("out", out), ("positions", positions)), dev)
-    n, h, d = x.shape
-    _check(load().dattn_rope(x.data_ptr(), out.data_ptr(), _DTYPES[dtype], n, h, d,
-                             _token_stride(x), _token_stride(out), positions.data_ptr(),
-                             _rope_params(d, rope_dims, rope_base, traditional, scaling),
-                             1 if gradient else 0, _current_stream(dev, stream)), "dattn_rope")
+        n, h, d = x.shape
+        xs, os_ = _token_stride(x), _token_stride(out)
+    st = load().dattn_rope(x.data_ptr(), out.data_ptr(), _DTYPES[dtype], n, h, d, xs, os_,
+                           positions.data_ptr(),
+                           _rope_params(d, rope_dims, rope_base, traditional, scaling),
+                           1 if gradient else 0, _current_stream(dev, stream))
+    if st != OK:
+        _check(st, "dattn_rope")
 
 
 def dattn_rope(x, out, positions, rope_dims: int = 0, rope_base: float = 10000.0,
                traditional: bool = False, scaling=None, gradient: bool = False,
                stream=None) -> None:
-    for name, t in (("x", x), ("out", out), ("positions", positions)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch.Tensor")
     _rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
 
 
@@ -630,17 +655,18 @@ def _q8_checks(k, v, k_scale, v_scale, scale_block, block_table, batch, current_
 
 def _q8_ordinary(k, v, k_scale, v_scale, scale_block, block_table, batch, current_pos, dev) -> bool:
     """Whether the cache and its companions are what an ordinary call brings."""
-    dtype, shape = k.dtype, k.shape
-    return (dtype in _KV_TYPES and v.dtype is dtype and k.ndim == 4 and v.shape == shape
-            and scale_block > 0 and k_scale.dtype is _F32 and v_scale.dtype is _F32
-            and k_scale.shape == (shape[0], -(-shape[1] // scale_block), shape[2])
-            and v_scale.shape == k_scale.shape and k.is_contiguous() and v.is_contiguous()
-            and k_scale.is_contiguous() and v_scale.is_contiguous() and k.get_device() == dev
-            and v.get_device() == dev and k_scale.get_device() == dev
-            and v_scale.get_device() == dev and current_pos.dtype in _INDEX
-            and current_pos.shape == (batch,) and current_pos.is_contiguous()
-            and current_pos.get_device() == dev
-            and (shape[0] == batch if block_table is None else
+    dtype = k.dtype
+    lead, rows, hk, _ = shape = k.shape
+    scales = (lead, -(-rows // scale_block), hk)
+    return (dtype in _KV_TYPES and v.dtype is dtype and v.shape == shape and k_scale.dtype is _F32
+            and v_scale.dtype is _F32 and k_scale.shape == scales and v_scale.shape == scales
+            and k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous()
+            and v_scale.is_contiguous() and k.get_device() == dev == v.get_device()
+            and k_scale.get_device() == dev == v_scale.get_device()
+            and current_pos.dtype in _INDEX and current_pos.shape == (batch,)
+            and current_pos.is_contiguous() and current_pos.get_device() == dev
+            and scale_block > 0
+            and (lead == batch if block_table is None else
                  (block_table.dtype is torch.int32 and block_table.ndim == 2
                   and block_table.shape[0] == batch and block_table.is_contiguous()
                   and block_table.get_device() == dev)))
@@ -657,26 +683,36 @@ def dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, 
                          rope_base: float = 10000.0, traditional: bool = False, scaling=None,
                          block_table=None, stream=None) -> None:
     """The dense call, or the paged one when ``block_table`` is given."""
-    _all_tensors(q_new=q_new, k_new=k_new, v_new=v_new, q_out=q_out, k_cache=k_cache,
-                 v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, current_pos=current_pos)
     dev = _device()
-    batch = current_pos.shape[0] if current_pos.ndim == 1 else -1
-    if not (_q8_ordinary(k_cache, v_cache, k_scale, v_scale, scale_block, block_table, batch,
-                         current_pos, dev)
-            and q_new.dtype is _F16 and k_new.dtype is _F16 and v_new.dtype is _F16
-            and q_out.dtype is _F16 and q_new.ndim == 3 and q_out.shape == q_new.shape
-            and k_new.shape == (q_new.shape[0], k_cache.shape[2], q_new.shape[2])
-            and v_new.shape == k_new.shape and q_new.shape[2] == k_cache.shape[3]
-            and q_new.is_contiguous() and k_new.is_contiguous() and v_new.is_contiguous()
-            and q_out.is_contiguous() and q_new.get_device() == dev and k_new.get_device() == dev
-            and v_new.get_device() == dev and q_out.get_device() == dev
-            and (q_new.shape[0] == batch if token_offsets is None else
-                 (token_offsets.dtype is torch.int32 and token_offsets.shape == (batch + 1,)
-                  and token_offsets.is_contiguous() and token_offsets.get_device() == dev))):
+    try:
+        batch, = current_pos.shape
+        n, h, d = shape = q_new.shape
+        lead, rows, hk, dc = k_cache.shape
+        new = (n, hk, dc)
+        qs, ks, vs = h * d, hk * dc, hk * dc
+        ordinary = (_q8_ordinary(k_cache, v_cache, k_scale, v_scale, scale_block, block_table,
+                                 batch, current_pos, dev)
+                    and q_new.dtype is _F16 and k_new.dtype is _F16 and v_new.dtype is _F16
+                    and q_out.dtype is _F16 and q_out.shape == shape and d == dc
+                    and k_new.shape == new and v_new.shape == new and q_new.is_contiguous()
+                    and k_new.is_contiguous() and v_new.is_contiguous() and q_out.is_contiguous()
+                    and q_new.get_device() == dev == k_new.get_device()
+                    and v_new.get_device() == dev == q_out.get_device()
+                    and (n == batch if token_offsets is None else
+                         (token_offsets.dtype is torch.int32
+                          and token_offsets.shape == (batch + 1,)
+                          and token_offsets.is_contiguous()
+                          and token_offsets.get_device() == dev)))
+    except (AttributeError, TypeError, ValueError, ZeroDivisionError):
+        ordinary = False
+    if not ordinary:
+        _all_tensors(q_new=q_new, k_new=k_new, v_new=v_new, q_out=q_out, k_cache=k_cache,
+                     v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, current_pos=current_pos)
+        batch = current_pos.shape[0] if current_pos.ndim == 1 else -1
         _q8_checks(k_cache, v_cache, k_scale, v_scale, scale_block, block_table, batch, current_pos)
         _tokens(q_new, "q_new", _F16)
-        n, _, d = q_new.shape
-        hk, dc = k_cache.shape[2:]
+        n, h, d = q_new.shape
+        lead, rows, hk, dc = k_cache.shape
         if d != dc:
             raise ValueError(f"q_new has head_dim {d}, the cache {dc}")
         _tokens(k_new, "k_new", _F16, (n, hk, d))
@@ -693,21 +729,23 @@ def dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, 
                      ("V_scale", v_scale), ("current_pos", current_pos),
                      ("token_offsets", token_offsets), ("block_table", block_table))
                     if t is not None], dev)
-    n, h, d = q_new.shape
-    lead, rows, hk, _ = k_cache.shape
+        qs, ks, vs = _token_stride(q_new), _token_stride(k_new), _token_stride(v_new)
     args = (q_new.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             _KV_TYPES[k_cache.dtype], scale_block, batch, n,
-            None if token_offsets is None else token_offsets.data_ptr(), _token_stride(q_new),
-            _token_stride(k_new), _token_stride(v_new), h, hk, d, rows)
-    tail = (_rope_params(d, rope_dims, rope_base, traditional, scaling), current_pos.data_ptr(),
-            _current_stream(dev, stream))
+            None if token_offsets is None else token_offsets.data_ptr(), qs, ks, vs, h, hk, d, rows)
+    rp = _rope_params(d, rope_dims, rope_base, traditional, scaling)
     if block_table is None:
-        _check(load().dattn_rope_append_q8(*args, *tail), "dattn_rope_append_q8")
+        st = load().dattn_rope_append_q8(*args, rp, current_pos.data_ptr(),
+                                         _current_stream(dev, stream))
+        if st != OK:
+            _check(st, "dattn_rope_append_q8")
     else:
-        _check(load().dattn_rope_append_paged_q8(*args, block_table.shape[1], lead,
-                                                 block_table.data_ptr(), *tail),
-               "dattn_rope_append_paged_q8")
+        st = load().dattn_rope_append_paged_q8(*args, block_table.shape[1], lead,
+                                               block_table.data_ptr(), rp, current_pos.data_ptr(),
+                                               _current_stream(dev, stream))
+        if st != OK:
+            _check(st, "dattn_rope_append_paged_q8")
 
 
 def rope_append_q8(q_new, k_new, v_new, k_cache, v_cache, k_scale, v_scale, current_pos,
@@ -755,21 +793,28 @@ def dattn_decode_q8_workspace_bytes(batch: int, n_heads: int, n_kv_heads: int, h
 
 def _decode_q8(q, k, v, k_scale, v_scale, block_table, current_pos, scale_block, num_partitions,
                out, workspace, stream, allocate):
-    _all_tensors(Q=q, k_cache=k, v_cache=v, k_scale=k_scale, v_scale=v_scale,
-                 current_pos=current_pos)
     dev = _device()
-    batch = q.shape[0] if q.ndim == 3 else -1
     fresh = out is None and allocate
-    if not (_q8_ordinary(k, v, k_scale, v_scale, scale_block, block_table, batch, current_pos, dev)
-            and q.dtype is _F16 and q.ndim == 3 and q.shape[2] == k.shape[3] and q.is_contiguous()
-            and q.get_device() == dev
-            and (fresh or (out.dtype is _F16 and out.shape == q.shape and out.is_contiguous()
-                           and out.get_device() == dev))):
+    try:
+        b, h, d = shape = q.shape
+        lead, rows, hk, dc = k.shape
+        ordinary = (_q8_ordinary(k, v, k_scale, v_scale, scale_block, block_table, b, current_pos,
+                                 dev)
+                    and q.dtype is _F16 and d == dc and q.is_contiguous() and q.get_device() == dev
+                    and (fresh or (out.dtype is _F16 and out.shape == shape
+                                   and out.is_contiguous() and out.get_device() == dev)))
+    except (AttributeError, TypeError, ValueError, ZeroDivisionError):
+        ordinary = False
+    if not ordinary:
+        _all_tensors(Q=q, k_cache=k, v_cache=v, k_scale=k_scale, v_scale=v_scale,
+                     current_pos=current_pos)
         if q.dim() != 3:
             raise ValueError("Q must be [batch, n_heads, head_dim]")
-        _q8_checks(k, v, k_scale, v_scale, scale_block, block_table, batch, current_pos)
-        if q.shape[2] != k.shape[3]:
-            raise ValueError(f"Q has head_dim {q.shape[2]}, the cache {k.shape[3]}")
+        b, h, d = q.shape
+        _q8_checks(k, v, k_scale, v_scale, scale_block, block_table, b, current_pos)
+        lead, rows, hk, dc = k.shape
+        if d != dc:
+            raise ValueError(f"Q has head_dim {d}, the cache {dc}")
         _tensor(q, "Q")
         named = [("Q", q), ("K cache", k), ("V cache", v), ("K_scale", k_scale),
                  ("V_scale", v_scale), ("current_pos", current_pos)]
@@ -780,37 +825,39 @@ def _decode_q8(q, k, v, k_scale, v_scale, block_table, current_pos, scale_block,
             named.append(("block_table", block_table))
         _on_device(named, dev)
     handle = _current_stream(dev, stream)
-    b, h, d = q.shape
-    lead, rows, hk, _ = k.shape
-    seq_len = rows if block_table is None else rows * block_table.shape[1]
-    need = _q8_workspace(dev, b, h, hk, d, seq_len, num_partitions) if workspace is None else 0
-    if handle in _RECORDING and allocate and (fresh or need):
-        raise ValueError("a recorded decode needs buffers that outlive the batch: pass out and "
-                         "workspace (dattn_decode_q8_workspace_bytes)")
-    if need and allocate:
-        workspace = _like(k, stream, (need,), torch.uint8)
-    if fresh:
-        out = _like(q, stream) if q.is_cuda else _like(k, stream, q.shape, _F16)
     wp, wn = None, 0
     if workspace is not None:
         wp = _tensor(workspace, "workspace", None, workspace.dtype)
         wn = workspace.numel() * workspace.element_size()
+    elif allocate:
+        wn = _q8_workspace(dev, b, h, hk, d,
+                           rows if block_table is None else rows * block_table.shape[1],
+                           num_partitions)
+    if _RECORDING and handle in _RECORDING and (fresh or (wn and wp is None)) and allocate:
+        raise ValueError("a recorded decode needs buffers that outlive the batch: pass out and "
+                         "workspace (dattn_decode_q8_workspace_bytes)")
+    if wn and wp is None:
+        workspace = _like(k, stream, (wn,), torch.uint8)
+        wp = workspace.data_ptr()
+    if fresh:
+        out = _like(q, stream) if q.is_cuda else _like(k, stream, q.shape, _F16)
     args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             out.data_ptr(), _KV_TYPES[k.dtype], scale_block, b, h, hk, d, rows)
     if block_table is None:
-        _check(load().dattn_decode_q8(*args, current_pos.data_ptr(), wp, wn, num_partitions,
-                                      handle), "dattn_decode_q8")
+        st = load().dattn_decode_q8(*args, current_pos.data_ptr(), wp, wn, num_partitions, handle)
+        if st != OK:
+            _check(st, "dattn_decode_q8")
     else:
-        _check(load().dattn_decode_paged_q8(*args, block_table.shape[1], lead,
-                                            block_table.data_ptr(), current_pos.data_ptr(), wp, wn,
-                                            num_partitions, handle), "dattn_decode_paged_q8")
+        st = load().dattn_decode_paged_q8(*args, block_table.shape[1], lead, block_table.data_ptr(),
+                                          current_pos.data_ptr(), wp, wn, num_partitions, handle)
+        if st != OK:
+            _check(st, "dattn_decode_paged_q8")
     return out
 
 
 def dattn_decode_q8(q, k, v, k_scale, v_scale, out, current_pos, scale_block: int, workspace=None,
                     num_partitions: int = 0, block_table=None, stream=None) -> None:
     """The dense call, or the paged one when ``block_table`` is given."""
-    _all_tensors(out=out)
     _decode_q8(q, k, v, k_scale, v_scale, block_table, current_pos, scale_block, num_partitions,
                out, workspace, stream, False)
 

@@ -176,6 +176,14 @@ inline FastDiv fast_div_of(int d) {
     return FastDiv{static_cast<uint32_t>((p + d - 1) / d), 31 + l};
 }
 
+#ifdef __CUDACC__
+// n / d for 0 <= n < 2^31 by one multiplication.
+__device__ __forceinline__ int fast_div(int n, FastDiv d) {
+    return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(n)) * d.mul) >>
+                            d.shift);
+}
+#endif
+
 // 8-bit cache types (enum dattn_kv_type).
 constexpr int kKvE4m3 = 1, kKvInt8 = 2;
 
@@ -274,7 +282,10 @@ struct RopeArgs {
     RopeTable rope;
     const void *x;
     void *out;
-    const uint32_t *positions;  // [tokens]
+    const uint32_t *positions;  // [tokens], or nullptr: from a ragged batch
+    const int *offsets;         // [B+1], or nullptr: one token per sequence
+    const uint32_t *cur_pos;    // [B] position of each sequence's last token
+    int B;
     long long x_stride, out_stride;  // elements from token to token
     long long tokens;
     int H, D;

@@ -80,12 +80,6 @@ __device__ __forceinline__ float lg2(float x) {
     return y;
 }
 
-// n / d for 0 <= n < 2^31 by one multiplication (d's constants from the host).
-__device__ __forceinline__ int fast_div(int n, FastDiv d) {
-    return static_cast<int>((static_cast<unsigned long long>(static_cast<unsigned>(n)) * d.mul) >>
-                            d.shift);
-}
-
 // bytes == 0: the 16 bytes are zero filled and src is not read.
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
     asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -689,7 +683,7 @@ __global__ void __launch_bounds__(NW * 32, q8_ctas_per_sm(DP, NT)) decode_q8_ker
         if constexpr (CLUSTER) cluster_wait();
         for (int i = tid; i < heads * (DP / 2); i += kThreads) {
             const int hq = i / (DP / 2), pair = i % (DP / 2);  // DP is a power of two
-            const int w0 = static_cast<int>((static_cast<unsigned long long>(hq) * a.div_gq.mul) >> a.div_gq.shift);
+            const int w0 = fast_div(hq, a.div_gq);
             const int h = hq - w0 * a.gq;
             const int m = pair >> 3, pg = pair & 7;
             const int ch = DP == 64 ? 8 * pg + 2 * m : (m >> 3) * 128 + 16 * pg + 2 * (m & 7);

@@ -1,12 +1,13 @@
 // rope_items.cuh -- the pieces of a head row that the rotary kernels work on.
 //
 // A row of D channels, the first rope_dims of them rotated in pairs, is cut
-// into items of 16 channels, one thread each: an item holds eight pairs (u, w),
-// channels (i, i + rope_dims/2) in the half layout and (2i, 2i + 1) in the
-// interleaved one, or 16 channels that pass through.  In either layout an
-// item is two runs of eight channels, so a thread reads 16-byte vectors and
-// needs no other thread's data.  VEC: rope_dims and D are multiples of 16, and
-// the runs are whole vectors; otherwise the elements are read one by one.
+// into items of 16 channels, one thread each: eight pairs (u, w), channels
+// (i, i + rope_dims/2) in the half layout and (2i, 2i + 1) in the interleaved
+// one, or 16 channels that pass through.  A thread needs no other thread's
+// data.  VEC (rope_dims and D multiples of 16): an item is sizeof(T) runs of 16
+// bytes, spread evenly over the rotated (or the passing) channels, so that in
+// either layout neighbouring threads read and write neighbouring vectors.
+// Otherwise the elements are read one by one.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -22,19 +23,47 @@ namespace dattn {
 // cos and sin of the angle p * theta_i from the turn fraction f = theta_i / 2pi
 // (units of 2^-64).  p * f mod 1 is an exact wrapping product.  Its top 32 bits
 // are split into the nearest quarter turn and a rest within an eighth of a turn
-// either way, which a float holds to 2^-27 of a half turn; sincospif of the
-// rest, then the quarter turns by exchange and sign.  The error is that of
-// sincospif plus 2.4e-8 rad at every position.
+// either way, which a float holds to 2^-27 of a half turn.  The rest's sine and
+// cosine are their Taylor series (|z| <= pi / 4: the first term left out is below
+// 2e-9), then the quarter turns by exchange and sign.  The angle is off by 2.4e-8
+// rad from the float and by z's rounding (at most 3e-8), each series by about an
+// ulp, at every position.  A general sincospif took more than twice the
+// instructions: it reduces its argument once more.
 __device__ __forceinline__ float2 turn_cos_sin(uint32_t p, unsigned long long f) {
     const uint32_t turn =
         static_cast<uint32_t>((static_cast<unsigned long long>(p) * f) >> 32);
     const uint32_t quarter = (turn + 0x20000000u) >> 30;
     const int rest = static_cast<int>(turn - (quarter << 30));
-    float s, c;
-    sincospif(static_cast<float>(rest) * 0x1p-31f, &s, &c);
-    const float x = quarter & 1u ? s : c, y = quarter & 1u ? c : s;
+    const float x = static_cast<float>(rest) * 0x1p-31f;                 // half turns
+    const float z = fmaf(x, 3.14159274f, x * -8.74227766e-8f);           // pi in two floats
+    const float w = z * z;
+    const float ps = fmaf(w, fmaf(w, fmaf(w, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6);
+    const float s = fmaf(z * w, ps, z);
+    const float pc = fmaf(w, fmaf(w, fmaf(w, -1.f / 3628800, 1.f / 40320), -1.f / 720), 1.f / 24);
+    const float c = fmaf(w, fmaf(w, pc, -0.5f), 1.f);
+    const float u = quarter & 1u ? s : c, v = quarter & 1u ? c : s;
     // quarter turns 0: (c, s)  1: (-s, c)  2: (-c, -s)  3: (s, -c)
-    return make_float2((quarter == 1u || quarter == 2u) ? -x : x, quarter & 2u ? -y : y);
+    return make_float2((quarter == 1u || quarter == 2u) ? -u : u, quarter & 2u ? -v : v);
+}
+
+// The sequence of flattened token t: the largest b with offsets[b] <= t, by a
+// warp-wide search (every lane returns it).  t lies below offsets[B].
+__device__ __forceinline__ int find_sequence(const int *offsets, int B, long long t, int lane) {
+    int lo = 0, n = B;  // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int i = lo + lane * step;
+        const bool le = i < lo + n && __ldg(offsets + i) <= t;
+        const int k = max(__popc(__ballot_sync(0xffffffffu, le)), 1) - 1;
+        n = min(step, n - k * step);
+        lo += k * step;
+    }
+    return lo;
+}
+
+// Tokens of a ragged batch that belong to a sequence.
+__device__ __forceinline__ long long used_tokens(const int *offsets, int B, long long tokens) {
+    return offsets ? min(tokens, max(0LL, static_cast<long long>(__ldg(offsets + B)))) : tokens;
 }
 
 __host__ __device__ inline int rope_items(int rope_dims, bool vec) {
@@ -45,7 +74,7 @@ __host__ __device__ inline int row_items(int rope_dims, int D, bool vec) {
     return rope_items(rope_dims, vec) + (D - rope_dims + 15) / 16;
 }
 
-// Sixteen elements of an item: runs x[0..7] and x[8..15].
+// Sixteen elements of an item.
 template <typename T>
 struct ItemData {
     uint4 v[sizeof(T)];
@@ -69,41 +98,49 @@ __device__ __forceinline__ float from_float<float>(float x) {
     return x;
 }
 
-// Item j of a row.
-template <bool VEC>
+// Item j of a row of T.  Elements k = 0 .. 15: in the half layout u of pair e is
+// element e and w element e + 8, in the interleaved one 2e and 2e + 1.
+template <typename T, bool VEC>
 struct Item {
+    static constexpr int kRuns = sizeof(T), kRun = 16 / kRuns;  // runs of 16 bytes
     int j, rope_dims, D;
     bool rot, trad;
-    int o0, o1;  // VEC: first channels of the two runs
+    int first, hop;  // VEC: channel of run r: first + r hop
 
     __device__ __forceinline__ Item(int j_, int rope_dims_, int D_, bool trad_)
         : j(j_), rope_dims(rope_dims_), D(D_), trad(trad_) {
         const int ir = rope_items(rope_dims, VEC);
         rot = j < ir;
-        if (rot) {
-            o0 = trad ? 16 * j : 8 * j;
-            o1 = trad ? o0 + 8 : rope_dims / 2 + o0;
+        if constexpr (VEC) {
+            first = rot ? kRun * j : rope_dims + kRun * (j - ir);
+            hop = (rot ? rope_dims : D - rope_dims) / kRuns;
         } else {
-            o0 = rope_dims + 16 * (j - ir);
-            o1 = o0 + 8;
+            first = rope_dims + 16 * (j - ir);
+            hop = 0;
         }
+    }
+    // The pair that slot e of item j rotates, or one past the last.
+    static __device__ __forceinline__ int pair_of(int e, int j, int rope_dims, bool trad) {
+        if constexpr (VEC) {
+            const int k = trad ? 2 * e : e;
+            const int c = k / kRun * (rope_dims / kRuns) + kRun * j + k % kRun;
+            return trad ? c >> 1 : c;
+        }
+        return 8 * j + e;
     }
     // Channel of element k, or -1 past the item's end (the scalar form).
     __device__ __forceinline__ int channel(int k) const {
-        if (!rot) return o0 + k < D ? o0 + k : -1;
+        if (!rot) return first + k < D ? first + k : -1;
         const int half = rope_dims / 2;
         const int pair = 8 * j + (trad ? k >> 1 : k & 7);
         if (pair >= half) return -1;
         return trad ? 2 * pair + (k & 1) : pair + (k >> 3) * half;
     }
-    template <typename T>
     __device__ __forceinline__ void load(const T *row, ItemData<T> &x) const {
         if constexpr (VEC) {
-            constexpr int N = sizeof(T) / 2;
-            const uint4 *a = reinterpret_cast<const uint4 *>(row + o0);
-            const uint4 *b = reinterpret_cast<const uint4 *>(row + o1);
 #pragma unroll
-            for (int i = 0; i < N; ++i) x.v[i] = a[i], x.v[N + i] = b[i];
+            for (int r = 0; r < kRuns; ++r)
+                x.v[r] = *reinterpret_cast<const uint4 *>(row + first + r * hop);
         } else {
             T *e = reinterpret_cast<T *>(x.v);
 #pragma unroll
@@ -113,14 +150,11 @@ struct Item {
             }
         }
     }
-    template <typename T>
     __device__ __forceinline__ void store(T *row, const ItemData<T> &x) const {
         if constexpr (VEC) {
-            constexpr int N = sizeof(T) / 2;
-            uint4 *a = reinterpret_cast<uint4 *>(row + o0);
-            uint4 *b = reinterpret_cast<uint4 *>(row + o1);
 #pragma unroll
-            for (int i = 0; i < N; ++i) a[i] = x.v[i], b[i] = x.v[N + i];
+            for (int r = 0; r < kRuns; ++r)
+                *reinterpret_cast<uint4 *>(row + first + r * hop) = x.v[r];
         } else {
             const T *e = reinterpret_cast<const T *>(x.v);
 #pragma unroll
@@ -130,41 +164,68 @@ struct Item {
             }
         }
     }
-};
-
-// The sixteen elements in fp32, rotated by (cos, sin) = cs[e] of pair e.
-template <bool VEC, typename T>
-__device__ __forceinline__ void rotate_item(const Item<VEC> &it, const ItemData<T> &x,
-                                            const float2 *cs, float *y) {
-    const T *e = reinterpret_cast<const T *>(x.v);
-    if (!it.rot) {
+    // The elements in fp32, those of a rotated item turned by the (cos, sin) of its
+    // slots, at table[0], table[items], ...
+    __device__ __forceinline__ void values(const ItemData<T> &x, const float2 *table, int items,
+                                           float *y) const {
+        const T *e = reinterpret_cast<const T *>(x.v);
+        if (!rot) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) y[k] = to_float(e[k]);
-    } else if (it.trad) {
+            for (int k = 0; k < 16; ++k) y[k] = to_float(e[k]);
+        } else if (trad) {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float u = to_float(e[2 * k]), w = to_float(e[2 * k + 1]);
-            y[2 * k] = u * cs[k].x - w * cs[k].y;
-            y[2 * k + 1] = u * cs[k].y + w * cs[k].x;
-        }
-    } else {
+            for (int k = 0; k < 8; ++k) {
+                const float2 cs = table[k * items];
+                const float u = to_float(e[2 * k]), w = to_float(e[2 * k + 1]);
+                y[2 * k] = u * cs.x - w * cs.y;
+                y[2 * k + 1] = u * cs.y + w * cs.x;
+            }
+        } else {
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float u = to_float(e[k]), w = to_float(e[k + 8]);
-            y[k] = u * cs[k].x - w * cs[k].y;
-            y[k + 8] = u * cs[k].y + w * cs[k].x;
+            for (int k = 0; k < 8; ++k) {
+                const float2 cs = table[k * items];
+                const float u = to_float(e[k]), w = to_float(e[k + 8]);
+                y[k] = u * cs.x - w * cs.y;
+                y[k + 8] = u * cs.y + w * cs.x;
+            }
         }
     }
-}
+};
 
-// cos/sin table of one position: pair 8 j + e at index e * items + j, so that
-// threads on neighbouring items read neighbouring entries.
-__device__ __forceinline__ void rope_table_entry(float2 *table, int items, int i, uint32_t pos,
-                                                 const RopeTable &r, bool gradient) {
-    float2 cs = turn_cos_sin(pos, r.turn_frac[i]);
-    cs.x *= r.magnitude;
-    cs.y *= gradient ? -r.magnitude : r.magnitude;
-    table[(i & 7) * items + (i >> 3)] = cs;
-}
+// A thread's part in building the cos/sin tables of some positions, 8 * items entries
+// each: slot e of item j at e * items + j, so that threads on neighbouring items read
+// neighbouring entries.  The CTA's threads (a power of two, 256 or more) keep one slot
+// each and go through the positions; the turn fraction, which neighbouring threads
+// fetch from different places of the parameters, is fetched once.
+template <typename T, bool VEC>
+struct RopeFiller {
+    int entries, slot, row0, hop;  // row0 < 0: no part
+    float mag_c, mag_s;
+    unsigned long long frac;
+
+    __device__ __forceinline__ RopeFiller(int items, const RopeTable &r, bool gradient)
+        : entries(8 * items), slot(0), row0(-1), hop(1), mag_c(r.magnitude),
+          mag_s(gradient ? -r.magnitude : r.magnitude), frac(0) {
+        if (items == 0) return;
+        int lanes = 8;
+        while (lanes < entries) lanes *= 2;
+        slot = threadIdx.x & (lanes - 1);
+        hop = blockDim.x / lanes;
+        const int e = slot / items;
+        const int pair = Item<T, VEC>::pair_of(e, slot - e * items, r.rope_dims, r.traditional != 0);
+        if (slot < entries && pair < r.rope_dims / 2) {
+            row0 = threadIdx.x / lanes;
+            frac = r.turn_frac[pair];
+        }
+    }
+    template <typename Pos>
+    __device__ __forceinline__ void fill(float2 *table, int rows, Pos position) const {
+        if (row0 < 0) return;
+        for (int row = row0; row < rows; row += hop) {
+            const float2 cs = turn_cos_sin(position(row), frac);
+            table[row * entries + slot] = make_float2(cs.x * mag_c, cs.y * mag_s);
+        }
+    }
+};
 
 }  // namespace dattn
