@@ -17,17 +17,17 @@
 // becomes 0 in int8.
 //
 // What bounds it: 2 bytes read per new element and one written for k and v, two
-// and two for q; a step of one token is bound by latency.  A segment of a warp (or
-// a warp) owns a (block, head) pair, so the maximum needs no second launch and no
-// atomics: its lanes hold the block's new rows in registers
-// (an item of 16 channels per row), join their maxima with shuffles and write the
-// 8-bit rows; large blocks take several warps.  Each input is read once unless a
-// block has more rows than its warps hold.  The CTA shares one cos/sin table of the block's positions, K and V go to
-// different CTAs.  The grid cannot know the ragged lengths, so it is cut by tokens:
-// a CTA looks through a window of the flattened tokens for those that open a block
-// (the first of a sequence, or a position at a multiple of scale_block) and takes
-// their blocks.  q is rotated by further CTAs of the same launch, or, when it is
-// large, by the kernel of rope.cu, whose CTAs need fewer registers.
+// and two for q; a step of one token is bound by latency, a prompt by instructions: a
+// rotated element is converted and turned twice, for the maximum and for the store,
+// and needs a cosine.  A thread holds one row's item of 16 channels of kHeads
+// heads, so a (row, pair)'s cosine is made once, in registers, for all of them, and the
+// maximum of a (block, head) pair is joined by warp reductions and one exchange in
+// shared memory: no second launch, no atomics.  Each input is read once unless a block
+// has more rows than its warps.  The grid cannot know the ragged lengths, so it is cut
+// by tokens: a CTA looks through a window of the flattened tokens for those that open a
+// block (the first of a sequence, or a position at a multiple of scale_block) and takes
+// their blocks.  K and V go to different CTAs.  q is rotated by further CTAs of the same
+// launch (rope_tiles.cuh), which stream while the others compute.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -36,27 +36,26 @@
 
 #include "dattn_internal.h"
 #include "ptx.cuh"
-#include "rope_items.cuh"
+#include "rope_tiles.cuh"
 
 namespace dattn {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kThreads = kRopeThreads, kWarps = kThreads / 32;
 constexpr int kMinExp = -32;  // scales are at least 2^-32
-constexpr int kQTokens = 4;   // tokens of a CTA that rotates q
-constexpr long long kQApart = 4 << 20;  // elements of q from which rope.cu's kernel takes it
+
+constexpr int kHeads = 4;     // heads of a thread
 
 struct AppendGrid {
-    int items_k, items_v, items_q;  // per row
-    int lanes;             // lanes of a row: a power of two, items_k and items_v at most
+    int items_k, items_v;  // per row
+    int lanes;             // lanes of a row: a power of two, items_k and items_v at least
     int rows;              // rows of a block side by side in a segment of lanes
-    int heads_per_warp;    // segments of a warp
-    int warps_per_head;    // warps that share the rows of their heads
+    int groups_per_warp;   // segments of a warp, kHeads heads each
+    int warps;             // warps that share the rows of their heads
     int heads_per_cta;
     int head_chunks;
     int window;            // tokens a CTA looks through
-    long long kv_ctas;
-    int q_tokens, q_heads, q_chunks;
+    unsigned kv_ctas, q_ctas;
 };
 
 // Smallest power of two s >= 2^kMinExp with amax <= QMAX s, from the bits of
@@ -71,14 +70,16 @@ __device__ __forceinline__ float need_scale(uint32_t amax_bits) {
     return __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
 }
 
-// x / scale is x times the reciprocal, exactly, where the scale is a power of two (or
-// infinite or NaN).
+// x / scale is x times the reciprocal, exactly, where the scale is a power of two; its
+// reciprocal is found in the exponent (for 2^-126 .. 2^126).
 struct Divider {
     float inv;
     bool exact;
 };
 __device__ __forceinline__ Divider divider(float scale) {
-    return Divider{1.f / scale, (__float_as_uint(scale) & 0x7fffffu) == 0};
+    const uint32_t bits = __float_as_uint(scale);
+    return Divider{__uint_as_float((254u << 23) - bits),
+                   (bits & 0x807fffffu) == 0 && bits - (1u << 23) < (253u << 23)};
 }
 
 template <int KV>
@@ -113,47 +114,96 @@ __device__ __forceinline__ float value_of(unsigned char x) {
     }
 }
 
-// RPT rows per lane held in registers.
-template <int KV, int RPT, bool VEC>
-__device__ __forceinline__ void append_kv(const Q8AppendArgs &a, const AppendGrid &gr, bool is_v,
-                                          long long window, int chunk, float2 *table,
-                                          float *s_mx) {
-    using It = Item<__half, VEC>;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int D = a.D, n_block = a.scale_block;
-    const int rd = is_v ? 0 : a.rope.rope_dims;
-    const int ir = rope_items(rd, VEC);
-    const int items = is_v ? gr.items_v : gr.items_k;
-    const int seg = gr.lanes * gr.rows;  // lanes of a head: a power of two
-    const int item = lane & (gr.lanes - 1), rs = (lane & (seg - 1)) / gr.lanes;
-    const int wph = gr.warps_per_head, wr = warp & (wph - 1);  // a power of two
-    const int head = chunk * gr.heads_per_cta + warp / wph * gr.heads_per_warp + lane / seg;
-    const int rs0 = wr * gr.rows * RPT + rs;  // this lane's first row of a pass
-    const bool mine = item < items && head < a.kv_heads;
-    const It it(item, rd, D, a.rope.traditional != 0);
-    const __half *src = reinterpret_cast<const __half *>(is_v ? a.v : a.k) + static_cast<long long>(head) * D;
-    const long long stride = is_v ? a.v_stride : a.k_stride;
-    unsigned char *cache = (is_v ? a.V : a.K) + static_cast<size_t>(head) * D;
-    float *scales = (is_v ? a.vs : a.ks) + head;
-    const int span = gr.rows * RPT * wph;  // rows of a pass
-
-    const RopeFiller<__half, VEC> filler(ir, a.rope, false);
-    const long long used = used_tokens(a.offsets, a.B, a.tokens);
-    long long tok = window * gr.window;
-    const long long w1 = min(tok + gr.window, used);
-    while (tok < w1) {
-        // ---- the sequence and position of token tok ----
-        int b;
-        long long s0, s1;  // its sequence's tokens
-        if (a.offsets == nullptr) {
-            b = static_cast<int>(tok);
-            s0 = tok;
-            s1 = tok + 1;
-        } else {
-            b = find_sequence(a.offsets, a.B, tok, lane);
-            s0 = __ldg(a.offsets + b);
-            s1 = __ldg(a.offsets + b + 1);
+// Put `before` earlier rows of a (block, head) on a scale `f` times finer to coarser:
+// value * f, rounded again.  Lane `item` of `lanes` and row `r0`, r0 + hop, ... are this
+// thread's; sixteen neighbouring channels at a time, whatever the pairs are.
+template <int KV>
+__device__ __forceinline__ void requantise(unsigned char *block0, size_t row_elems, int D, int before,
+                                           float f, int item, int lanes, int r0, int hop) {
+    for (int r = r0; r < before; r += hop) {
+        for (int c = item * 16; c < D; c += lanes * 16) {
+            uint4 *v = reinterpret_cast<uint4 *>(block0 + r * row_elems + c);
+            uint4 x = *v;
+            uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                w[e] = pack4<KV>(value_of<KV>(w[e] & 255u) * f, value_of<KV>(w[e] >> 8 & 255u) * f,
+                                 value_of<KV>(w[e] >> 16 & 255u) * f, value_of<KV>(w[e] >> 24) * f);
+            *v = x;
         }
+    }
+}
+
+// Largest finite magnitude of an item (0 if it has none).
+__device__ __forceinline__ float item_max(const float *y) {
+    float m = 0.f;  // fmaxf passes over NaN
+#pragma unroll
+    for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(y[e]));
+    if (m == INFINITY) {  // among infinities only the finite ones count
+        m = 0.f;
+#pragma unroll
+        for (int e = 0; e < 16; ++e) m = fabsf(y[e]) < INFINITY ? fmaxf(m, fabsf(y[e])) : m;
+    }
+    return m;
+}
+
+// y / scale in 8 bits into the item's channels of row o.
+template <int KV, bool VEC>
+__device__ __forceinline__ void store_item(const Item<__half, VEC> &it, unsigned char *o, float *y,
+                                           float scale, const Divider &div) {
+    if (div.exact) {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] *= div.inv;
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) y[e] = y[e] / scale;
+    }
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = pack4<KV>(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+    if constexpr (VEC) {
+        *reinterpret_cast<uint2 *>(o + it.first) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>(o + it.first + it.hop) = make_uint2(w[2], w[3]);
+    } else {
+        unsigned char *u = o + it.first, *v = u + it.hop;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (k < it.n0) u[k] = static_cast<unsigned char>(w[k >> 2] >> (8 * (k & 3)));
+            if (k < it.n1) v[k] = static_cast<unsigned char>(w[2 + (k >> 2)] >> (8 * (k & 3)));
+        }
+    }
+}
+
+// The place of position `pos` of sequence b: the first row of its scale block and the
+// block's row of scales.  False where the page is not in the pool.
+__device__ __forceinline__ bool block_place(const Q8AppendArgs &a, int b, int pos, int blk, int before,
+                                            long long *row0, long long *srow) {
+    if (a.block_table == nullptr) {
+        *row0 = static_cast<long long>(b) * a.S + pos - before;
+        *srow = static_cast<long long>(b) * a.scale_rows + blk;
+        return true;
+    }
+    const int pi = fast_div(pos, a.div_page);
+    const long long page = __ldg(a.block_table + static_cast<long long>(b) * a.max_pages + pi);
+    *row0 = page * a.page_size + (pos - pi * a.page_size - before);
+    *srow = page * a.scale_rows + blk - pi * a.scale_rows;
+    return page >= 0 && page < a.num_pages;
+}
+
+// The block that a CTA works on: its first new token, position and row, how many rows are
+// new and how many the sequence has in it from before, and its row of scales.
+struct Unit {
+    long long token, row0, srow;
+    int pos, n, before;
+};
+
+// The next block that a token of [tok, end) opens (by one warp; lane 0 reports tokens that
+// cannot be appended).  tok is left behind the block; false: none is left.
+__device__ __forceinline__ bool next_unit(const Q8AppendArgs &a, long long used, long long &tok,
+                                          long long end, int lane, Unit &u) {
+    while (tok < end) {
+        const int b = find_sequence(a.offsets, a.B, tok, lane);
+        const long long s0 = __ldg(a.offsets + b), s1 = __ldg(a.offsets + b + 1);  // its tokens
         const long long stop = min(s1, used);
         if (stop <= tok) {  // offsets that do not ascend: no token of a sequence
             ++tok;
@@ -161,298 +211,360 @@ __device__ __forceinline__ void append_kv(const Q8AppendArgs &a, const AppendGri
         }
         const long long p = static_cast<long long>(__ldg(a.cur_pos + b)) - (s1 - 1 - tok);
         if (p < 0 || p >= a.S) {
-            if (threadIdx.x == 0) atomicOr(a.err, kErrAppendPosition);
+            if (lane == 0) atomicOr(a.err, kErrAppendPosition);
             tok = p < 0 ? min(tok - p, stop) : stop;
             continue;
         }
-        const int pos = static_cast<int>(p);
-        const int blk = fast_div(pos, a.div_block);
-        const int before = pos - blk * n_block;  // rows of the block before this one
-        const int n = static_cast<int>(min(min(static_cast<long long>(n_block - before), stop - tok),
-                                           static_cast<long long>(a.S - pos)));
-        if (before != 0 && tok != s0) {  // inside a block that an earlier token opens
-            tok += n;
-            continue;
-        }
-
-        // ---- load the first rows; the block's first row and its scale's row ----
-        ItemData<__half> d[RPT];
-        auto load_pass = [&](int r0) {
-#pragma unroll
-            for (int r = 0; r < RPT; ++r) {
-                const int row = r0 + rs0 + r * gr.rows;
-                if (mine && row < n) it.load(src + (tok + row) * stride, d[r]);
-            }
-        };
-        load_pass(0);
-        long long row0, srow;
-        bool ok = true;
-        if (a.block_table == nullptr) {
-            row0 = static_cast<long long>(b) * a.S + pos - before;
-            srow = static_cast<long long>(b) * a.scale_rows + blk;
-        } else {
-            const int pi = fast_div(pos, a.div_page);
-            const long long page = __ldg(a.block_table + static_cast<long long>(b) * a.max_pages + pi);
-            ok = page >= 0 && page < a.num_pages;
-            if (!ok && threadIdx.x == 0) atomicOr(a.err, kErrPageIndex);
-            row0 = page * a.page_size + (pos - pi * a.page_size - before);
-            srow = page * a.scale_rows + blk - pi * a.scale_rows;
-        }
-        if (!ok) {
-            tok += n;
-            continue;
-        }
-        float *const scale = scales + srow * a.kv_heads;
-        const float old = before > 0 && head < a.kv_heads ? *scale : 0.f;
-
-        // ---- pass 1: rotate, largest finite magnitude of the head ----
-        auto fill_table = [&](int r0) {
-            filler.fill(table, min(span, n - r0), [&](int r) { return static_cast<uint32_t>(pos + r0 + r); });
-        };
-        float mx = 0.f;
-        for (int r0 = 0; r0 < n; r0 += span) {
-            if (r0 > 0) {
-                load_pass(r0);
-                if (ir > 0) __syncthreads();  // the table of the pass before has been read
-            }
-            if (ir > 0) {
-                fill_table(r0);
-                __syncthreads();
-            }
-#pragma unroll
-            for (int r = 0; r < RPT; ++r) {
-                const int row = rs0 + r * gr.rows;
-                if (mine && r0 + row < n) {
-                    float y[16];
-                    it.values(d[r], table + row * 8 * ir + item, ir, y);
-                    float m = 0.f;  // fmaxf passes over NaN
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(y[e]));
-                    if (m == INFINITY) {  // among infinities only the finite ones count
-                        m = 0.f;
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) m = fabsf(y[e]) < INFINITY ? fmaxf(m, fabsf(y[e])) : m;
-                    }
-                    mx = fmaxf(mx, m);
-                }
-            }
-        }
-        for (int o = seg / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (wph > 1) {  // then a warp is one segment
-            if (lane == 0) s_mx[warp] = mx;
-            __syncthreads();
-            for (int w = 0; w < wph; ++w) mx = fmaxf(mx, s_mx[(warp & ~(wph - 1)) + w]);
-        }
-
-        // ---- the head's scale; its earlier rows on the new scale ----
-        const float need = need_scale<KV>(__float_as_uint(mx));
-        const float now = before > 0 ? fmaxf(old, need) : need;
-        if (head < a.kv_heads && wr == 0 && (lane & (seg - 1)) == 0) *scale = now;
-        const size_t row_elems = static_cast<size_t>(a.kv_heads) * D;
-        unsigned char *const block0 = cache + static_cast<size_t>(row0) * row_elems;
-        if (before > 0 && now != old && head < a.kv_heads) {
-            const float f = old / now;
-            for (int r = wr * gr.rows + rs; r < before; r += gr.rows * wph) {
-                // sixteen neighbouring channels, whatever the pairs are
-                for (int c = item * 16; c < D; c += gr.lanes * 16) {
-                    uint4 *v = reinterpret_cast<uint4 *>(block0 + r * row_elems + c);
-                    uint4 x = *v;
-                    uint32_t *w = reinterpret_cast<uint32_t *>(&x);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = pack4<KV>(value_of<KV>(w[e] & 255u) * f, value_of<KV>(w[e] >> 8 & 255u) * f,
-                                         value_of<KV>(w[e] >> 16 & 255u) * f, value_of<KV>(w[e] >> 24) * f);
-                    *v = x;
-                }
-            }
-        }
-        // ---- pass 2: the new rows ----
-        const Divider div = divider(now);
-        for (int r0 = 0; r0 < n; r0 += span) {
-            if (n > span) {  // more rows than the lanes hold: read them again
-                load_pass(r0);
-                if (ir > 0) {
-                    __syncthreads();
-                    fill_table(r0);
-                    __syncthreads();
-                }
-            }
-#pragma unroll
-            for (int r = 0; r < RPT; ++r) {
-                const int row = rs0 + r * gr.rows;
-                if (!mine || r0 + row >= n) continue;
-                float y[16];
-                it.values(d[r], table + row * 8 * ir + item, ir, y);
-                if (div.exact) {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) y[e] *= div.inv;
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) y[e] = y[e] / now;
-                }
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] = pack4<KV>(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-                unsigned char *o = block0 + static_cast<size_t>(before + r0 + row) * row_elems;
-                if constexpr (VEC) {
-                    *reinterpret_cast<uint2 *>(o + it.first) = make_uint2(w[0], w[1]);
-                    *reinterpret_cast<uint2 *>(o + it.first + it.hop) = make_uint2(w[2], w[3]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const int ch = it.channel(e);
-                        if (ch >= 0) o[ch] = static_cast<unsigned char>(w[e >> 2] >> (8 * (e & 3)));
-                    }
-                }
-            }
-        }
-        tok += n;
-        if (ir > 0 || wph > 1) __syncthreads();  // the table and s_mx may be written again
+        u.token = tok;
+        u.pos = static_cast<int>(p);
+        const int blk = fast_div(u.pos, a.div_block);
+        u.before = u.pos - blk * a.scale_block;
+        u.n = static_cast<int>(min(min(static_cast<long long>(a.scale_block - u.before), stop - tok),
+                                   static_cast<long long>(a.S - u.pos)));
+        tok += u.n;
+        if (u.before != 0 && u.token != s0) continue;  // inside a block that an earlier token opens
+        if (block_place(a, b, u.pos, blk, u.before, &u.row0, &u.srow)) return true;
+        if (lane == 0) atomicOr(a.err, kErrPageIndex);
     }
+    return false;
 }
 
-// q: some tokens with some of their heads.
-template <bool VEC>
-__device__ __forceinline__ void rotate_q(const Q8AppendArgs &a, const AppendGrid &gr,
-                                         long long cta, float2 *table, uint32_t *s_pos) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int D = a.D, rd = a.rope.rope_dims;
-    const int ir = rope_items(rd, VEC);
-    const long long t0 = cta / gr.q_chunks * gr.q_tokens;
-    const int h0 = static_cast<int>(cta % gr.q_chunks) * gr.q_heads;
-    const int nh = min(gr.q_heads, a.H - h0);
+struct AppendShared {
+    unsigned long long frac[128];           // turn fraction of slot e of item j at 8 j + e
+    Unit unit;
+    int more;
+    float mx[kHeads * 32 * kWarps];         // of each head of the CTA, by each of its warps
+    float now[kHeads * 32 * kWarps], old[kHeads * 32 * kWarps];  // its scale, and before
+};
+
+template <int KV, bool VEC, bool IS_V>
+__device__ __forceinline__ void append_kv(const Q8AppendArgs &a, const AppendGrid &gr, long long window,
+                                          int chunk, AppendShared &sh) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int D = a.D, rd = IS_V ? 0 : a.rope.rope_dims;
+    const int seg = gr.lanes * gr.rows;  // lanes of a group of heads: a power of two
+    const int item = lane & (gr.lanes - 1), rs = (lane & (seg - 1)) / gr.lanes;
+    const int wr = warp & (gr.warps - 1);  // a power of two
+    const int local = (warp / gr.warps * gr.groups_per_warp + lane / seg) * kHeads;
+    const int first_head = chunk * gr.heads_per_cta, head0 = first_head + local;
+    const int nh = min(kHeads, a.kv_heads - head0);  // 0 or less: no heads
+    const bool mine = item < (IS_V ? gr.items_v : gr.items_k);
+    const int myrow = wr * gr.rows + rs, span = gr.rows * gr.warps;  // rows of a pass
+    const size_t row_elems = static_cast<size_t>(a.kv_heads) * D;
+    const Item<__half, VEC> it(item, rd, D, a.rope.traditional != 0);
+    const __half *const src = reinterpret_cast<const __half *>(IS_V ? a.v : a.k) + static_cast<long long>(head0) * D;
+    const long long stride = IS_V ? a.v_stride : a.k_stride;
+    const float mag = a.rope.magnitude;
+
     const long long used = used_tokens(a.offsets, a.B, a.tokens);
-    const int nt = static_cast<int>(min(static_cast<long long>(gr.q_tokens), used - t0));
-    if (nt <= 0) return;
-    for (int s = warp; s < nt; s += kWarps) {
-        const long long t = t0 + s;
-        long long p;
-        if (a.offsets == nullptr) {
-            p = __ldg(a.cur_pos + t);
-        } else {
-            const int b = find_sequence(a.offsets, a.B, t, lane);
-            p = static_cast<long long>(__ldg(a.cur_pos + b)) - (__ldg(a.offsets + b + 1) - 1 - t);
+    long long tok = window * gr.window;
+    const long long end = min(tok + gr.window, used);
+    for (;;) {
+        if (warp == 0) {
+            Unit u;
+            const bool more = next_unit(a, used, tok, end, lane, u);
+            if (lane == 0) {
+                sh.more = more;
+                if (more) sh.unit = u;
+            }
         }
-        // the rotation is defined at every position; the append reports those
-        // outside the cache
-        if (lane == 0) s_pos[s] = static_cast<uint32_t>(p);
-    }
-    __syncthreads();
-    RopeFiller<__half, VEC>(ir, a.rope, false).fill(table, nt, [&](int s) { return s_pos[s]; });
-    __syncthreads();
-    const __half *q = reinterpret_cast<const __half *>(a.q);
-    __half *out = reinterpret_cast<__half *>(a.q_out);
-    const int total = nt * nh * gr.items_q;
-    for (int n = threadIdx.x; n < total; n += kThreads) {
-        const int th = n / gr.items_q, item = n - th * gr.items_q;
-        const int s = th / nh, head = h0 + th - s * nh;
-        const Item<__half, VEC> it(item, rd, D, a.rope.traditional != 0);
-        ItemData<__half> d;
-        it.load(q + (t0 + s) * a.q_stride + static_cast<long long>(head) * D, d);
-        float y[16];
-        it.values(d, table + s * 8 * ir + item, ir, y);
-        __half *e = reinterpret_cast<__half *>(d.v);
+        __syncthreads();
+        if (!sh.more) return;
+        const Unit u = sh.unit;
+        const int n = u.n, before = u.before;
+
+        // this thread's row of a pass: the inputs of its heads, and its cosines
+        ItemData<__half> d[kHeads];
+        float2 cs[8];
+        auto load_row = [&](int r0) {
+            const int row = r0 + myrow;
+            if (!mine || row >= n) return;
+            const __half *x = src + (u.token + row) * stride;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) e[i] = __float2half_rn(y[i]);
-        it.store(out + ((t0 + s) * a.H + head) * D, d);
+            for (int h = 0; h < kHeads; ++h)
+                if (h < nh) it.load(x + h * D, d[h]);
+            if (!IS_V && it.rot) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float2 c = turn_cos_sin(static_cast<uint32_t>(u.pos + row), sh.frac[item * 8 + e]);
+                    cs[e] = make_float2(c.x * mag, c.y * mag);
+                }
+            }
+        };
+
+        // ---- pass 1: largest finite magnitude of each head's rotated rows ----
+        float mx[kHeads];
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) mx[h] = 0.f;
+        for (int r0 = 0; r0 < n; r0 += span) {
+            load_row(r0);
+            if (!mine || r0 + myrow >= n) continue;
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                if (h >= nh) break;
+                float y[16];
+                it.values(d[h], cs, 1, y);
+                mx[h] = fmaxf(mx[h], item_max(y));
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < kHeads; ++h) {
+            if (seg == 32) {  // not negative: they order as their bits do
+                mx[h] = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx[h])));
+            } else {
+                for (int o = seg / 2; o > 0; o >>= 1)
+                    mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], o));
+            }
+        }
+        if ((lane & (seg - 1)) == 0) {
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) sh.mx[(local + h) * gr.warps + wr] = mx[h];
+        }
+        __syncthreads();
+        // ---- each head's scale, by one thread ----
+        for (int i = threadIdx.x; i < min(gr.heads_per_cta, a.kv_heads - first_head); i += kThreads) {
+            float *const scale = (IS_V ? a.vs : a.ks) + u.srow * a.kv_heads + first_head + i;
+            const float old = before > 0 ? *scale : 0.f;
+            float m = 0.f;
+            for (int w = 0; w < gr.warps; ++w) m = fmaxf(m, sh.mx[i * gr.warps + w]);
+            const float need = need_scale<KV>(__float_as_uint(m));
+            const float now = before > 0 ? fmaxf(old, need) : need;
+            sh.now[i] = now;
+            sh.old[i] = before > 0 ? old : now;
+            *scale = now;
+        }
+        __syncthreads();
+        // ---- earlier rows on the new scale; pass 2: the new rows ----
+        unsigned char *const block0 = (IS_V ? a.V : a.K) + static_cast<size_t>(u.row0) * row_elems +
+                                      static_cast<size_t>(head0) * D;
+        if (before > 0) {
+            for (int h = 0; h < nh; ++h) {
+                const float now = sh.now[local + h], old = sh.old[local + h];
+                if (now != old)
+                    requantise<KV>(block0 + h * D, row_elems, D, before, old / now, item, gr.lanes, myrow, span);
+            }
+        }
+        for (int r0 = 0; r0 < n; r0 += span) {
+            if (n > span) load_row(r0);  // more rows than the warps hold: read them again
+            if (!mine || r0 + myrow >= n) continue;
+            unsigned char *o = block0 + static_cast<size_t>(before + r0 + myrow) * row_elems;
+#pragma unroll
+            for (int h = 0; h < kHeads; ++h) {
+                if (h >= nh) break;
+                const float now = sh.now[local + h];
+                float y[16];
+                it.values(d[h], cs, 1, y);
+                store_item<KV, VEC>(it, o + h * D, y, now, divider(now));
+            }
+        }
     }
 }
 
-template <int KV, int RPT, bool VEC>
-__global__ void __launch_bounds__(kThreads, 3)
-    append_q8_kernel(const __grid_constant__ Q8AppendArgs a, const AppendGrid gr) {
-    extern __shared__ float2 table[];
-    __shared__ uint32_t s_pos[kQTokens];
-    __shared__ float s_mx[kWarps];
+// CTAs [0, q_ctas) rotate q and stay while K's blocks and then V's, which take less time,
+// go through the other slots (K and V alternating left every other SM with K only).  HP:
+// heads of a thread that rotates q.
+template <int KV, bool VEC, bool FIXED, int HP>
+__global__ void __launch_bounds__(kThreads, 2)
+    append_q8_kernel(const __grid_constant__ Q8AppendArgs a, const __grid_constant__ RopeArgs q,
+                     const AppendGrid gr, const RopeGrid qgr) {
+    extern __shared__ __align__(16) unsigned char smem[];
+    union Shared {
+        AppendShared kv;
+        uint32_t pos[2][kRopeThreads];
+    };
+    __shared__ Shared sh;
     pdl_launch_dependents();
-    pdl_wait_primary();
-    const long long cta = blockIdx.x;
-    if (cta < gr.kv_ctas) {
-        const unsigned rest = static_cast<unsigned>(cta >> 1), w = rest / static_cast<unsigned>(gr.head_chunks);
-        append_kv<KV, RPT, VEC>(a, gr, (cta & 1) != 0, w, static_cast<int>(rest - w * gr.head_chunks), table,
-                               s_mx);
-    } else {
-        rotate_q<VEC>(a, gr, cta - gr.kv_ctas, table, s_pos);
+    const unsigned q_ctas = gr.q_ctas;
+    if (blockIdx.x < q_ctas) {
+        pdl_wait_primary();
+        rope_tiles<__half, VEC, FIXED, HP>(q, a.rope, qgr, blockIdx.x, q_ctas, smem, sh.pos);
+        return;
     }
+    const int ir = rope_items(a.rope.rope_dims, VEC);
+    for (int i = threadIdx.x; i < 8 * ir; i += kThreads) {
+        const int pair = Item<__half, VEC>::pair_of(i & 7, i >> 3, a.rope.rope_dims, a.rope.traditional != 0);
+        sh.kv.frac[i] = a.rope.turn_frac[min(pair, a.rope.rope_dims / 2 - 1)];
+    }
+    pdl_wait_primary();
+    const unsigned i = blockIdx.x - q_ctas, half = gr.kv_ctas / 2;
+    const unsigned rest = i < half ? i : i - half, w = rest / static_cast<unsigned>(gr.head_chunks);
+    const int chunk = static_cast<int>(rest - w * gr.head_chunks);
+    if (i < half) append_kv<KV, VEC, false>(a, gr, w, chunk, sh.kv);
+    else append_kv<KV, VEC, true>(a, gr, w, chunk, sh.kv);
 }
+
+template <int KV>
+const void *kernel_of(bool vec, bool fixed, int hp) {
+    if (!vec) return reinterpret_cast<const void *>(append_q8_kernel<KV, false, false, 1>);
+    if (fixed)
+        return hp == 2 ? reinterpret_cast<const void *>(append_q8_kernel<KV, true, true, 2>)
+                       : reinterpret_cast<const void *>(append_q8_kernel<KV, true, true, 1>);
+    return hp == 2 ? reinterpret_cast<const void *>(append_q8_kernel<KV, true, false, 2>)
+                   : reinterpret_cast<const void *>(append_q8_kernel<KV, true, false, 1>);
+}
+
+// One token per sequence (a decode step), bound by latency: a CTA takes some of the
+// heads of q, k and v of a token, one item per thread, the lanes of a head side by side
+// in a warp.  The inputs' addresses need no position, so they are under way while the
+// position, the page and the old scales are looked up one after another.  (Three items
+// per thread, a CTA for all heads: 7.4 against 7.0 us for 256 tokens of 40 heads.)
+struct TokenGrid {
+    int items_k, items_v;  // per row of q and k; of v
+    int lanes;             // lanes of a head, a power of two
+    int chunks;            // CTAs of a token
+};
 
 template <int KV, bool VEC>
-const void *kernel_of(int rpt) {
-    if (rpt == 1) return reinterpret_cast<const void *>(append_q8_kernel<KV, 1, VEC>);
-    if (rpt == 2) return reinterpret_cast<const void *>(append_q8_kernel<KV, 2, VEC>);
-    // elements read one by one take too many registers for more rows
-    if constexpr (VEC) return reinterpret_cast<const void *>(append_q8_kernel<KV, 4, VEC>);
-    return nullptr;
+__global__ void __launch_bounds__(kThreads, 3)
+    append_token_kernel(const __grid_constant__ Q8AppendArgs a, const TokenGrid gr) {
+    __shared__ float2 table[128];  // rope_dims / 2 entries at most, in slots of eight
+    pdl_launch_dependents();
+    pdl_wait_primary();
+    const unsigned ub = blockIdx.x / static_cast<unsigned>(gr.chunks);
+    const int b = static_cast<int>(ub), chunk = static_cast<int>(blockIdx.x - ub * gr.chunks);
+    const int D = a.D, ir = rope_items(a.rope.rope_dims, VEC);
+    const int item = threadIdx.x & (gr.lanes - 1);
+    const uint32_t p = __ldg(a.cur_pos + b);
+
+    // heads are numbered q, k, v one after another
+    int head = chunk * (kThreads / gr.lanes) + threadIdx.x / gr.lanes;
+    const bool is_q = head < a.H, is_v = head >= a.H + a.kv_heads;
+    const int items = is_v ? gr.items_v : gr.items_k;
+    const bool mine = head < a.H + 2 * a.kv_heads && item < items;
+    if (!is_q) head -= is_v ? a.H + a.kv_heads : a.H;
+    const Item<__half, VEC> it(item, is_v ? 0 : a.rope.rope_dims, D, a.rope.traditional != 0);
+    ItemData<__half> d;
+    if (mine) {
+        const __half *src = reinterpret_cast<const __half *>(is_q ? a.q : is_v ? a.v : a.k);
+        const long long stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
+        it.load(src + b * stride + static_cast<long long>(head) * D, d);
+    }
+    // The rotation is defined at every position; an append outside the cache is reported.
+    RopeFiller<__half, VEC>(ir, a.rope, false).fill(table, 1, [&](int) { return p; });
+    bool ok = p < static_cast<uint32_t>(a.S);
+    long long row0 = 0, srow = 0;
+    int before = 0;
+    if (ok) {
+        const int pos = static_cast<int>(p), blk = fast_div(pos, a.div_block);
+        before = pos - blk * a.scale_block;
+        ok = block_place(a, b, pos, blk, before, &row0, &srow);
+        if (!ok && threadIdx.x == 0) atomicOr(a.err, kErrPageIndex);
+    } else if (threadIdx.x == 0) {
+        atomicOr(a.err, kErrAppendPosition);
+    }
+    float *const scale = (is_v ? a.vs : a.ks) + srow * a.kv_heads + head;
+    const float old = ok && before > 0 && mine && !is_q ? *scale : 0.f;
+    __syncthreads();
+    float y[16], mx = 0.f;
+    if (mine) {
+        it.values(d, table + item, ir, y);
+        if (!is_q) mx = item_max(y);
+    }
+    for (int o = gr.lanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    if (!mine) return;
+    if (is_q) {
+        round_item(y, d);
+        it.store(reinterpret_cast<__half *>(a.q_out) + (static_cast<long long>(b) * a.H + head) * D, d);
+        return;
+    }
+    if (!ok) return;
+    const float need = need_scale<KV>(__float_as_uint(mx));
+    const float now = before > 0 ? fmaxf(old, need) : need;
+    const size_t row_elems = static_cast<size_t>(a.kv_heads) * D;
+    unsigned char *const block0 =
+        (is_v ? a.V : a.K) + static_cast<size_t>(row0) * row_elems + static_cast<size_t>(head) * D;
+    if (before > 0 && now != old)
+        requantise<KV>(block0, row_elems, D, before, old / now, item, items, 0, 1);
+    if (item == 0) *scale = now;
+    store_item<KV, VEC>(it, block0 + before * row_elems, y, now, divider(now));
+}
+
+cudaError_t launch_append_token(const Q8AppendArgs &a, int kv, cudaStream_t stream) {
+    const bool vec = a.rope.rope_dims % 16 == 0;
+    TokenGrid gr{};
+    gr.items_k = row_items(a.rope.rope_dims, a.D, vec);
+    gr.items_v = row_items(0, a.D, vec);
+    gr.lanes = 1;
+    while (gr.lanes < std::max(gr.items_k, gr.items_v)) gr.lanes *= 2;
+    const long long chunks = ((a.H + 2LL * a.kv_heads) * gr.lanes + kThreads - 1) / kThreads;
+    const long long blocks = a.B * chunks;
+    if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
+    gr.chunks = static_cast<int>(chunks);
+    const void *fn = kv == kKvE4m3 ? (vec ? reinterpret_cast<const void *>(append_token_kernel<kKvE4m3, true>)
+                                          : reinterpret_cast<const void *>(append_token_kernel<kKvE4m3, false>))
+                                   : (vec ? reinterpret_cast<const void *>(append_token_kernel<kKvInt8, true>)
+                                          : reinterpret_cast<const void *>(append_token_kernel<kKvInt8, false>));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void *args[] = {const_cast<Q8AppendArgs *>(&a), &gr};
+    return cudaLaunchKernelExC(&cfg, fn, args);
 }
 
 }  // namespace
 
 cudaError_t launch_append_q8(const Q8AppendArgs &a, int kv, int sms, cudaStream_t stream) {
+    if (a.offsets == nullptr) return launch_append_token(a, kv, stream);
     const int rd = a.rope.rope_dims;
-    const bool vec = rd % 16 == 0;  // D is a multiple of 16
+    RopeGrid qgr{};
+    int hp = 1;
+    bool vec = false, fixed = false;
+    if (!rope_grid(a.tokens, a.H, a.D, rd, 2, sms, &qgr, &hp, &vec, &fixed)) return cudaErrorInvalidValue;
     AppendGrid gr{};
     gr.items_k = row_items(rd, a.D, vec);
     gr.items_v = row_items(0, a.D, vec);
-    gr.items_q = gr.items_k;
     gr.lanes = 1;
     while (gr.lanes < std::max(gr.items_k, gr.items_v)) gr.lanes *= 2;
-    // rows of a block: side by side in the lanes of a warp first, then up to four in a
-    // lane's registers, then in more warps; one in a step of one token per sequence
-    const int want = a.offsets == nullptr ? 1 : a.scale_block;
+    // rows of a block: side by side in the lanes of a warp first, then in more warps
     gr.rows = 1;
-    while (gr.rows < want && 2 * gr.rows * gr.lanes <= 32) gr.rows *= 2;
-    int rpt = 1;
-    while (rpt < (vec ? 4 : 2) && rpt * gr.rows < want) rpt *= 2;
-    gr.warps_per_head = 1;
-    while (gr.warps_per_head < kWarps && gr.warps_per_head * rpt * gr.rows < want) gr.warps_per_head *= 2;
-    gr.heads_per_warp = 32 / (gr.lanes * gr.rows);
-    gr.heads_per_cta = gr.heads_per_warp * (kWarps / gr.warps_per_head);
+    while (gr.rows < a.scale_block && 2 * gr.rows * gr.lanes <= 32) gr.rows *= 2;
+    gr.warps = 1;
+    while (gr.warps < kWarps && gr.warps * gr.rows < a.scale_block) gr.warps *= 2;
+    gr.groups_per_warp = 32 / (gr.lanes * gr.rows);
+    gr.heads_per_cta = kHeads * gr.groups_per_warp * (kWarps / gr.warps);
     gr.head_chunks = (a.kv_heads + gr.heads_per_cta - 1) / gr.heads_per_cta;
-    // about one block per window when sequences are long, one token when short
+    // about one block per window when sequences are long, one token when short; smaller
+    // where that leaves CTA slots empty, since a CTA takes its blocks one after another
+    // (301 tokens of 13 sequences, 8 heads: 12.5 us with windows of 16 tokens, 8.8 with 1)
     const long long mean = std::max(1LL, a.tokens / a.B);
-    gr.window = static_cast<int>(a.offsets == nullptr ? 1 : std::min<long long>(mean, a.scale_block));
+    gr.window = static_cast<int>(std::min<long long>(mean, a.scale_block));
+    while (gr.window > 1 && a.tokens / gr.window * gr.head_chunks < 2LL * sms) gr.window = (gr.window + 1) / 2;
     const long long windows = (a.tokens + gr.window - 1) / gr.window;
-    gr.kv_ctas = windows * gr.head_chunks * 2;
-    // q with the kernel of rope.cu where it is large enough for the second launch
-    const bool apart = a.tokens * a.H * static_cast<long long>(a.D) >= kQApart;
-    if (apart) {
-        RopeArgs r{};
-        r.rope = a.rope;
-        r.x = a.q;
-        r.out = a.q_out;
-        r.offsets = a.offsets;
-        r.cur_pos = a.cur_pos;
-        r.B = a.B;
-        r.x_stride = a.q_stride;
-        r.out_stride = static_cast<long long>(a.H) * a.D;
-        r.tokens = a.tokens;
-        r.H = a.H;
-        r.D = a.D;
-        const cudaError_t e = launch_rope(r, kDtypeF16, sms, stream);
-        if (e != cudaSuccess) return e;
-    }
-    gr.q_tokens = a.tokens >= 4LL * sms * kQTokens ? kQTokens : 1;
-    gr.q_heads = a.H;
-    while (gr.q_heads > 1 && a.tokens / gr.q_tokens * ((a.H + gr.q_heads - 1) / gr.q_heads) < 2LL * sms &&
-           gr.q_heads * gr.items_q > 64)
-        gr.q_heads = (gr.q_heads + 1) / 2;
-    gr.q_chunks = (a.H + gr.q_heads - 1) / gr.q_heads;
-    const long long q_ctas = apart ? 0 : (a.tokens + gr.q_tokens - 1) / gr.q_tokens * gr.q_chunks;
-    const long long blocks = gr.kv_ctas + q_ctas;
-    if (blocks <= 0 || blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
-    const void *fn = kv == kKvE4m3 ? (vec ? kernel_of<kKvE4m3, true>(rpt) : kernel_of<kKvE4m3, false>(rpt))
-                                   : (vec ? kernel_of<kKvInt8, true>(rpt) : kernel_of<kKvInt8, false>(rpt));
-    // the table: at most 8 warps x 32 lanes x 4 rows of them x 8 pairs, 64 KB
-    const int rows = std::max(std::min(gr.rows * rpt * gr.warps_per_head, want), gr.q_tokens);
-    const size_t smem = static_cast<size_t>(rows) * 8 * rope_items(rd, vec) * sizeof(float2);
-    if (smem > 48 * 1024) {
+    const long long kv_ctas = windows * gr.head_chunks * 2;
+    // q by one CTA of each SM's two slots
+    const long long q_ctas = std::min<long long>(qgr.tiles, sms);
+    if (kv_ctas + q_ctas > 0x7fffffffLL) return cudaErrorInvalidValue;
+    gr.kv_ctas = static_cast<unsigned>(kv_ctas);
+    gr.q_ctas = static_cast<unsigned>(q_ctas);
+    RopeArgs q{};
+    q.x = a.q;
+    q.out = a.q_out;
+    q.offsets = a.offsets;
+    q.cur_pos = a.cur_pos;
+    q.B = a.B;
+    q.x_stride = a.q_stride;
+    q.out_stride = static_cast<long long>(a.H) * a.D;
+    q.tokens = a.tokens;
+    q.H = a.H;
+    q.D = a.D;
+    const void *fn = kv == kKvE4m3 ? kernel_of<kKvE4m3>(vec, fixed, hp) : kernel_of<kKvInt8>(vec, fixed, hp);
+    const int ring = !vec   ? 0
+                     : hp == 2 ? kStages<__half, 2> * kTileBytes<__half, 2>
+                               : kStages<__half, 1> * kTileBytes<__half, 1>;
+    const size_t smem = rope_smem(qgr, rd, vec, ring);
+    if (smem > 32 * 1024) {  // with the static part past the default limit
         const cudaError_t e =
             cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks));
+    cfg.gridDim = dim3(static_cast<unsigned>(kv_ctas + q_ctas));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
@@ -461,7 +573,7 @@ cudaError_t launch_append_q8(const Q8AppendArgs &a, int kv, int sms, cudaStream_
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    void *args[] = {const_cast<Q8AppendArgs *>(&a), &gr};
+    void *args[] = {const_cast<Q8AppendArgs *>(&a), &q, &gr, &qgr};
     return cudaLaunchKernelExC(&cfg, fn, args);
 }
 

@@ -80,24 +80,6 @@ __device__ __forceinline__ float lg2(float x) {
     return y;
 }
 
-// bytes == 0: the 16 bytes are zero filled and src is not read.
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-                 "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() {
-    asm volatile("cp.async.commit_group;" ::: "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Two neighbouring 8-bit values (the low or high half of a word) as f16x2.
 // e4m3: one conversion, exact (NaN stays NaN).  int8: the byte with its sign
 // bit flipped is v + 128; put under the exponent of 1024 it reads 1152 + v.

@@ -132,6 +132,25 @@ __device__ __forceinline__ void tensor3d_prefetch_l2(const void *tmap, int c0, i
                  : "memory");
 }
 
+// Asynchronous copies of 16 and 4 bytes, global -> shared, by groups of the calling
+// thread.  bytes == 0: the destination is zero filled and src is not read.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+                 "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // Thread-block clusters: rank of this CTA in its cluster, the address of the
 // same shared-memory location in another CTA of the cluster, a load from it,
 // and the cluster-wide barrier (every thread of every CTA of the cluster

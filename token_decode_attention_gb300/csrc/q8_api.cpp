@@ -533,8 +533,8 @@ int dattn_rope(const void *x, void *out, int dtype, long long tokens, int n_head
         if (head_dim % 8 != 0 || head_dim > kMaxHeadDim)
             return fail(DATTN_ERR_UNSUPPORTED, "head_dim=%d: must be a multiple of 8 and <= %d",
                         head_dim, kMaxHeadDim);
-        if (tokens > 0x7fffffffLL || n_heads > (1 << 20))
-            return fail(DATTN_ERR_UNSUPPORTED, "at most 2^31-1 tokens of 2^20 heads");
+        if (tokens > 0x7ffffc00LL || n_heads > (1 << 20))
+            return fail(DATTN_ERR_UNSUPPORTED, "at most 2^31-1024 tokens of 2^20 heads");
         const long long row = static_cast<long long>(n_heads) * head_dim;
         const int elem = dtype == DATTN_F32 ? 4 : 2;
         if (int st = check_stride(x_stride, row, elem, "x_stride")) return st;

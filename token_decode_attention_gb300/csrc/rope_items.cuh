@@ -80,6 +80,23 @@ struct ItemData {
     uint4 v[sizeof(T)];
 };
 
+// Sixteen fp32 values rounded to T.
+__device__ __forceinline__ void round_item(const float *y, ItemData<__half> &x) {
+    __half2 *h = reinterpret_cast<__half2 *>(x.v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+}
+__device__ __forceinline__ void round_item(const float *y, ItemData<__nv_bfloat16> &x) {
+    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(x.v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) h[i] = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+}
+__device__ __forceinline__ void round_item(const float *y, ItemData<float> &x) {
+    float *f = reinterpret_cast<float *>(x.v);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = y[i];
+}
+
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
 __device__ __forceinline__ float to_float(float x) { return x; }
@@ -105,7 +122,9 @@ struct Item {
     static constexpr int kRuns = sizeof(T), kRun = 16 / kRuns;  // runs of 16 bytes
     int j, rope_dims, D;
     bool rot, trad;
-    int first, hop;  // VEC: channel of run r: first + r hop
+    int first, hop;  // VEC: channel of run r: first + r hop; else two runs of eight
+                     // channels at most, at first and first + hop, n0 and n1 long
+    int n0, n1;
 
     __device__ __forceinline__ Item(int j_, int rope_dims_, int D_, bool trad_)
         : j(j_), rope_dims(rope_dims_), D(D_), trad(trad_) {
@@ -114,9 +133,14 @@ struct Item {
         if constexpr (VEC) {
             first = rot ? kRun * j : rope_dims + kRun * (j - ir);
             hop = (rot ? rope_dims : D - rope_dims) / kRuns;
+            n0 = n1 = kRun;
         } else {
-            first = rope_dims + 16 * (j - ir);
-            hop = 0;
+            const bool halves = rot && !trad;
+            first = halves ? 8 * j : rot ? 16 * j : rope_dims + 16 * (j - ir);
+            hop = halves ? rope_dims / 2 : 8;
+            const int left = halves ? rope_dims / 2 - first : (rot ? rope_dims : D) - first;
+            n0 = min(left, 8);
+            n1 = halves ? n0 : min(max(left - 8, 0), 8);
         }
     }
     // The pair that slot e of item j rotates, or one past the last.
@@ -128,25 +152,25 @@ struct Item {
         }
         return 8 * j + e;
     }
-    // Channel of element k, or -1 past the item's end (the scalar form).
-    __device__ __forceinline__ int channel(int k) const {
-        if (!rot) return first + k < D ? first + k : -1;
-        const int half = rope_dims / 2;
-        const int pair = 8 * j + (trad ? k >> 1 : k & 7);
-        if (pair >= half) return -1;
-        return trad ? 2 * pair + (k & 1) : pair + (k >> 3) * half;
-    }
     __device__ __forceinline__ void load(const T *row, ItemData<T> &x) const {
         if constexpr (VEC) {
 #pragma unroll
             for (int r = 0; r < kRuns; ++r)
-                x.v[r] = *reinterpret_cast<const uint4 *>(row + first + r * hop);
+                x.v[r] = __ldg(reinterpret_cast<const uint4 *>(row + first + r * hop));
         } else {
+            // without branches, so that all sixteen are in flight: what is past the
+            // end of a run (which may be empty, but for the first) is read elsewhere
+            const T *u = row + first, *w = n1 > 0 ? u + hop : u;
             T *e = reinterpret_cast<T *>(x.v);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const int c = channel(k);
-                e[k] = c >= 0 ? row[c] : from_float<T>(0.f);
+            for (int k = 0; k < 8; ++k) {
+                e[k] = u[k < n0 ? k : 0];
+                e[k + 8] = w[k < n1 ? k : 0];
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                e[k] = k < n0 ? e[k] : from_float<T>(0.f);
+                e[k + 8] = k < n1 ? e[k + 8] : from_float<T>(0.f);
             }
         }
     }
@@ -156,11 +180,12 @@ struct Item {
             for (int r = 0; r < kRuns; ++r)
                 *reinterpret_cast<uint4 *>(row + first + r * hop) = x.v[r];
         } else {
+            T *u = row + first, *w = u + hop;
             const T *e = reinterpret_cast<const T *>(x.v);
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                const int c = channel(k);
-                if (c >= 0) row[c] = e[k];
+            for (int k = 0; k < 8; ++k) {
+                if (k < n0) u[k] = e[k];
+                if (k < n1) w[k] = e[k + 8];
             }
         }
     }
