@@ -348,3 +348,29 @@ def test_refusals():
     s.tq = tq
     run()
     s.check()
+
+
+def _mixed(n, top, seed):
+    return np.random.default_rng(seed).integers(0, top, n).tolist()
+
+
+LARGER = [
+    # counts, first position's offset, H, Hk, D, S, block, page, pad, rope_dims, trad
+    (_mixed(300, 40, 1), 5, 6, 6, 32, 64, 16, 32, 3, 0, False),
+    ([2000], 77, 16, 8, 64, 2112, 16, 16, 0, 0, False),
+    ([700, 0, 513], 1, 6, 3, 128, 768, 256, 256, 9, 64, True),
+    (_mixed(64, 30, 2), 0, 7, 7, 80, 40, 8, 0, 0, 40, False),   # odd heads, pairs one by one
+    (_mixed(64, 30, 3), 9, 12, 4, 96, 40, 40, 0, 1, 20, True),
+    (_mixed(1500, 4, 4), 2, 2, 1, 16, 8, 4, 4, 0, 0, False),
+    ([33] * 9, 31, 40, 20, 256, 64, 64, 64, 0, 128, False),
+]
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+@pytest.mark.parametrize("case", LARGER, ids=[f"T{sum(c[0])}B{len(c[0])}H{c[2]}k{c[3]}D{c[4]}n{c[6]}p{c[7]}" for c in LARGER])
+def test_larger_batches(case, kv):
+    counts, first, H, Hk, D, S, block, page, pad, rd, trad = case
+    last = [min(first + i % 3 + c - 1, S - 1) if c else first for i, c in enumerate(counts)]
+    s = Step(counts, last, H, Hk, D, S, block, kv, page, pad, rd, trad=trad)
+    s.run()
+    s.check()

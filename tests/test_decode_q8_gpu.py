@@ -312,3 +312,56 @@ def test_long_cache_offsets_pass_32_bits():
     one = np.ones((1, 2, Hk), np.float32)
     ref, size, dot, top = _q8.decode(q.cpu().numpy(), kk, vv, one, one, [page * 2 - 1], block)
     _q8.check(_q8.f64(got), ref, _q8.decode_bound(ref, size, dot, top, 2 * page, D, one), "far rows")
+
+
+MANY = [
+    # B, H, Hk, D, S, block, page: more (sequence, head group) units than CTAs fit at once
+    (160, 16, 8, 64, 40, 8, 8),
+    (330, 10, 5, 128, 96, 16, 32),     # groups of four heads: the second holds one
+    (170, 8, 2, 256, 48, 16, 0),
+    (210, 24, 24, 80, 64, 32, 64),
+    (640, 3, 3, 32, 200, 1, 0),
+    (320, 48, 3, 128, 33, 16, 0),      # sixteen query heads each
+    (700, 2, 1, 16, 1, 1, 1),
+]
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+@pytest.mark.parametrize("B,H,Hk,D,S,block,page", MANY,
+                         ids=[f"B{s[0]}H{s[1]}k{s[2]}D{s[3]}S{s[4]}" for s in MANY])
+def test_many_short_sequences_in_several_waves(B, H, Hk, D, S, block, page, kv):
+    assert dattn.dattn_decode_q8_workspace_bytes(B, H, Hk, D, S) == 0
+    plan = dattn.dattn_decode_q8_plan(B, H, Hk, D, S)
+    assert plan["cluster_size"] == 1 and plan["partitions"] > plan["sm_count"] * plan["ctas_per_sm"]
+    cp = np.random.default_rng(B).integers(0, S, B).tolist()
+    c = Case(B, H, Hk, D, S, block, kv, cp, page)
+    got = c.run()
+    c.check(got)
+    assert torch.equal(got, c.run())
+    # any other split of the same work agrees within the bound
+    c.check(c.run(num_partitions=100), "split")
+
+
+def test_bad_page_among_many_short_sequences():
+    c = Case(330, 4, 4, 64, 32, 8, "e4m3", [31] * 330, page=16)
+    good = c.run()
+    c.tt[7, 1] = 10 ** 6
+    c.tt[300, 0] = -5
+    got = c.run()
+    assert dattn.dattn_device_error(clear=True) == _native.ERR_BAD_PAGE
+    keep = torch.ones(330, dtype=torch.bool, device="cuda")
+    keep[7] = keep[300] = False
+    assert torch.equal(got[keep], good[keep])
+
+
+@pytest.mark.parametrize("B,H,Hk,D,S", [(1, 8, 8, 64, 500), (2, 32, 8, 128, 900), (1, 32, 32, 128, 4096),
+                                        (5, 20, 4, 80, 700), (1, 16, 4, 256, 1000), (1, 12, 3, 128, 600)])
+@pytest.mark.parametrize("short", [False, True], ids=["full", "ragged"])
+def test_clusters_merge_in_shared_memory(B, H, Hk, D, S, short):
+    # no workspace: the CTAs of a sequence's head group exchange their states
+    assert dattn.dattn_decode_q8_workspace_bytes(B, H, Hk, D, S) == 0
+    cp = [S - 1] * B if not short else [(17 * b + 3) % S for b in range(B)]
+    c = Case(B, H, Hk, D, S, 16, "e4m3", cp)
+    got = c.run()
+    c.check(got)
+    assert torch.equal(got, c.run())

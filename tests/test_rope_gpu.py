@@ -203,3 +203,28 @@ def test_refusals():
         dattn.rope(x[:0], p[:0])
     with pytest.raises(TypeError, match="RopeScaling"):
         dattn.rope(x, p, scaling="linear")
+
+
+@pytest.mark.parametrize("dtype", list(STEP), ids=["f16", "bf16", "f32"])
+@pytest.mark.parametrize("n,H,D,rd,trad", [
+    (20011, 4, 64, 0, False),      # several tiles for each CTA, four heads at a time
+    (9001, 6, 32, 32, True),       # two at a time
+    (7003, 7, 48, 16, False),      # one
+    (5001, 4, 80, 40, True),       # pairs one by one
+    (5001, 4, 80, 20, False),
+    (3001, 6, 40, 12, False),
+    (501, 130, 128, 0, False),     # more heads than a tile
+])
+def test_many_tiles_in_place_of_a_slice(n, H, D, rd, trad, dtype):
+    g = torch.Generator(device="cuda").manual_seed(n + H)
+    whole = torch.randn((n, H + 3, D), generator=g, device="cuda").to(dtype)
+    keep = whole.clone()
+    x = whole[:, 1: H + 1]
+    p = torch.arange(n, dtype=torch.int32, device="cuda") * 7
+    kw = dict(rope_dims=rd, traditional=trad)
+    apart = dattn.rope(x, p, **kw)
+    same = dattn.rope(x, p, out=x, **kw)
+    assert same.data_ptr() == x.data_ptr() and torch.equal(same, apart)
+    assert torch.equal(whole[:, :1], keep[:, :1]) and torch.equal(whole[:, H + 1:], keep[:, H + 1:])
+    rows = np.unique(np.r_[0:70, n // 2: n // 2 + 70, n - 70: n])
+    check(apart[rows], keep[:, 1: H + 1][rows], rows * 7, rd, 10000.0, trad, None, False)

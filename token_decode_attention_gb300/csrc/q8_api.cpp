@@ -29,6 +29,7 @@ constexpr int kStaticSmem = 4096;  // the decode kernel's static shared memory a
 // tiles, 14.7 and 16.2; 64 query on 8 key/value heads over 32768 positions, 16 tiles
 // and 7 in the split plan, 26.6 and 18.1.
 constexpr long long kClusterTiles = 8;
+constexpr long long kUnitTiles = 16;  // the same with a CTA for each unit
 
 int fail(int status, const char *fmt, ...) {
     char buf[512];
@@ -222,43 +223,69 @@ struct Plan {
 
 size_t round_up(size_t x, size_t m) { return (x + m - 1) / m * m; }
 
-// The cluster plan in place of the split plan *p, for calls bound by latency: a cluster
-// of C CTAs for each (sequence, group of heads), all resident at once, merged in the
-// same launch.  Of the head groups and cluster sizes that fit, the one with the fewest
-// tiles for a warp at full length; then fewer CTAs.
+// A plan without partial states in memory in place of the split plan *p, where that is
+// faster: a CTA, or a cluster of them that merges in shared memory, takes a (sequence,
+// group of hg heads) unit whole.
+//
+// Units of their own CTAs, as many waves of them as it takes, where there are enough to
+// fill most of the SMs' slots and a warp's tiles of a full sequence are at most
+// kUnitTiles: the most heads for which both hold, but no fewer than an eighth of all
+// (shorter runs of the cache per position cost more than the split plan's merge).
+// Measured with ragged lengths, these units and the split plan, us: 512 sequences of 8
+// heads up to 128 positions 28.0, 62.2; 256 of 8 up to 1024 56.8, 70.7; 128 of 32 up to
+// 512 55.8, 59.2; 256 of 8 up to 2048, one head per CTA, 98.2, 108.8; 64 of 32 up to 1024,
+// two heads, which the eighth excludes, 54.2, 53.7.
+//
+// With fewer units, calls bound by latency: clusters of C CTAs, all resident at once.  Of
+// the head groups and cluster sizes that fit, the one with the fewest tiles for a warp at
+// full length; then fewer CTAs.
 int cluster_plan(int B, int D, long long tiles, const dattn::DeviceFacts &df, Plan *p) {
-    long long best = 0;
-    Plan found;
+    const long long slots = static_cast<long long>(df.sms) * p->ctas_per_sm;
+    auto use = [&](int hg, int C, long long smem) {
+        p->HG = hg;
+        p->NHG = (p->vheads + hg - 1) / hg;
+        p->PH = p->warps / hg;
+        p->cluster = C;
+        p->G = static_cast<int>(static_cast<long long>(B) * p->NHG * C);
+        p->smem = static_cast<int>(smem);
+    };
+    const long long ring = static_cast<long long>(p->warps) * p->slots * dattn::q8_tile_bytes(p->dp);
+    for (int hg = 8; hg >= 1 && hg * 8 >= p->vheads; hg /= 2) {
+        if (hg > std::min(p->vheads, p->warps)) continue;
+        const long long units = static_cast<long long>(B) * ((p->vheads + hg - 1) / hg);
+        const int ph = p->warps / hg;
+        if (10 * units < 7 * slots || (tiles + ph - 1) / ph > kUnitTiles || units > 0x7fffffffLL) continue;
+        use(hg, 1, ring);
+        return DATTN_OK;
+    }
+    long long best = 0, best_smem = 0;
+    int best_hg = 0, best_C = 0;
     for (int hg = 1; hg <= std::min(p->vheads, p->warps); hg *= 2) {
         const long long units = static_cast<long long>(B) * ((p->vheads + hg - 1) / hg);
         const int ph = p->warps / hg;
-        for (int C = 1; C <= 16 && units * C <= df.sms * p->ctas_per_sm; C *= 2) {
+        for (int C = 1; C <= 16 && units * C <= slots; C *= 2) {
             const long long per_warp = ((tiles + C - 1) / C + ph - 1) / ph;
             if (best != 0 && per_warp >= best) continue;
             // the records of a CTA's share of the unit's (query head, channel pair) outputs
             const long long rec = C > 1 ? (hg * p->gq * (p->dp / 2) + C - 1) / C * C * 16LL : 0;
-            const long long smem = static_cast<long long>(p->warps) * p->slots * dattn::q8_tile_bytes(p->dp) + rec;
-            if (smem > df.max_smem_optin - kStaticSmem) continue;
+            if (ring + rec > df.max_smem_optin - kStaticSmem) continue;
             int fit = 0;
-            if (dattn::decode_q8_max_clusters(p->dp, p->nt, static_cast<int>(smem), C, &fit) != cudaSuccess) {
+            if (dattn::decode_q8_max_clusters(p->dp, p->nt, static_cast<int>(ring + rec), C, &fit) !=
+                cudaSuccess) {
                 cudaGetLastError();  // this cluster size is not available
                 continue;
             }
             if (fit < units) continue;
             best = per_warp;
-            found = *p;
-            found.HG = hg;
-            found.NHG = (p->vheads + hg - 1) / hg;
-            found.PH = ph;
-            found.cluster = C;
-            found.G = static_cast<int>(units * C);
-            found.smem = static_cast<int>(smem);
+            best_smem = ring + rec;
+            best_hg = hg;
+            best_C = C;
         }
     }
     // The split plan costs a second launch and the states' way through memory, about
     // two tiles of a warp; the cluster plan waits for its longest sequence.
     const double split = static_cast<double>(B) * p->NHG * tiles / (static_cast<double>(p->G) * p->PH);
-    if (best > 0 && best <= kClusterTiles && best <= split + 2.0) *p = found;
+    if (best > 0 && best <= kClusterTiles && best <= split + 2.0) use(best_hg, best_C, best_smem);
     return DATTN_OK;
 }
 
