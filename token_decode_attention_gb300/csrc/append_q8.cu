@@ -135,37 +135,45 @@ __device__ __forceinline__ void requantise(unsigned char *block0, size_t row_ele
 }
 
 // Largest finite magnitude of an item (0 if it has none).
+template <int E>
 __device__ __forceinline__ float item_max(const float *y) {
     float m = 0.f;  // fmaxf passes over NaN
 #pragma unroll
-    for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(y[e]));
+    for (int e = 0; e < E; ++e) m = fmaxf(m, fabsf(y[e]));
     if (m == INFINITY) {  // among infinities only the finite ones count
         m = 0.f;
 #pragma unroll
-        for (int e = 0; e < 16; ++e) m = fabsf(y[e]) < INFINITY ? fmaxf(m, fabsf(y[e])) : m;
+        for (int e = 0; e < E; ++e) m = fabsf(y[e]) < INFINITY ? fmaxf(m, fabsf(y[e])) : m;
     }
     return m;
 }
 
 // y / scale in 8 bits into the item's channels of row o.
-template <int KV, bool VEC>
-__device__ __forceinline__ void store_item(const Item<__half, VEC> &it, unsigned char *o, float *y,
+template <int KV, int N>
+__device__ __forceinline__ void store_item(const Item<__half, N> &it, unsigned char *o, float *y,
                                            float scale, const Divider &div) {
+    constexpr int E = 2 * kPairs<N>;
     if (div.exact) {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] *= div.inv;
+        for (int e = 0; e < E; ++e) y[e] *= div.inv;
     } else {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) y[e] = y[e] / scale;
+        for (int e = 0; e < E; ++e) y[e] = y[e] / scale;
     }
-    uint32_t w[4];
+    uint32_t w[E / 4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) w[e] = pack4<KV>(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-    if constexpr (VEC) {
-        *reinterpret_cast<uint2 *>(o + it.first) = make_uint2(w[0], w[1]);
-        *reinterpret_cast<uint2 *>(o + it.first + it.hop) = make_uint2(w[2], w[3]);
+    for (int e = 0; e < E / 4; ++e) w[e] = pack4<KV>(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+    unsigned char *const u = o + it.first, *const v = u + it.hop;  // the two runs
+    if constexpr (N == 16) {
+        *reinterpret_cast<uint2 *>(u) = make_uint2(w[0], w[1]);
+        *reinterpret_cast<uint2 *>(v) = make_uint2(w[2], w[3]);
+    } else if constexpr (N == 8) {
+        *reinterpret_cast<uint32_t *>(u) = w[0];
+        *reinterpret_cast<uint32_t *>(v) = w[1];
+    } else if constexpr (N == 4) {
+        *reinterpret_cast<unsigned short *>(u) = static_cast<unsigned short>(w[0]);
+        *reinterpret_cast<unsigned short *>(v) = static_cast<unsigned short>(w[0] >> 16);
     } else {
-        unsigned char *u = o + it.first, *v = u + it.hop;
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             if (k < it.n0) u[k] = static_cast<unsigned char>(w[k >> 2] >> (8 * (k & 3)));
@@ -230,14 +238,14 @@ __device__ __forceinline__ bool next_unit(const Q8AppendArgs &a, long long used,
 }
 
 struct AppendShared {
-    unsigned long long frac[128];           // turn fraction of slot e of item j at 8 j + e
+    unsigned long long frac[128];           // turn fraction of each slot, an item's side by side
     Unit unit;
     int more;
     float mx[kHeads * 32 * kWarps];         // of each head of the CTA, by each of its warps
     float now[kHeads * 32 * kWarps], old[kHeads * 32 * kWarps];  // its scale, and before
 };
 
-template <int KV, bool VEC, bool IS_V>
+template <int KV, int N, bool IS_V>
 __device__ __forceinline__ void append_kv(const Q8AppendArgs &a, const AppendGrid &gr, long long window,
                                           int chunk, AppendShared &sh) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -251,7 +259,7 @@ __device__ __forceinline__ void append_kv(const Q8AppendArgs &a, const AppendGri
     const bool mine = item < (IS_V ? gr.items_v : gr.items_k);
     const int myrow = wr * gr.rows + rs, span = gr.rows * gr.warps;  // rows of a pass
     const size_t row_elems = static_cast<size_t>(a.kv_heads) * D;
-    const Item<__half, VEC> it(item, rd, D, a.rope.traditional != 0);
+    const Item<__half, N> it(item, rd, D, a.rope.traditional != 0);
     const __half *const src = reinterpret_cast<const __half *>(IS_V ? a.v : a.k) + static_cast<long long>(head0) * D;
     const long long stride = IS_V ? a.v_stride : a.k_stride;
     const float mag = a.rope.magnitude;
@@ -274,8 +282,8 @@ __device__ __forceinline__ void append_kv(const Q8AppendArgs &a, const AppendGri
         const int n = u.n, before = u.before;
 
         // this thread's row of a pass: the inputs of its heads, and its cosines
-        ItemData<__half> d[kHeads];
-        float2 cs[8];
+        ItemData<__half, N> d[kHeads];
+        float2 cs[kPairs<N>];
         auto load_row = [&](int r0) {
             const int row = r0 + myrow;
             if (!mine || row >= n) return;
@@ -285,8 +293,9 @@ __device__ __forceinline__ void append_kv(const Q8AppendArgs &a, const AppendGri
                 if (h < nh) it.load(x + h * D, d[h]);
             if (!IS_V && it.rot) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float2 c = turn_cos_sin(static_cast<uint32_t>(u.pos + row), sh.frac[item * 8 + e]);
+                for (int e = 0; e < kPairs<N>; ++e) {
+                    const float2 c =
+                        turn_cos_sin(static_cast<uint32_t>(u.pos + row), sh.frac[item * kPairs<N> + e]);
                     cs[e] = make_float2(c.x * mag, c.y * mag);
                 }
             }
@@ -302,9 +311,9 @@ __device__ __forceinline__ void append_kv(const Q8AppendArgs &a, const AppendGri
 #pragma unroll
             for (int h = 0; h < kHeads; ++h) {
                 if (h >= nh) break;
-                float y[16];
+                float y[2 * kPairs<N>];
                 it.values(d[h], cs, 1, y);
-                mx[h] = fmaxf(mx[h], item_max(y));
+                mx[h] = fmaxf(mx[h], item_max<2 * kPairs<N>>(y));
             }
         }
 #pragma unroll
@@ -352,9 +361,9 @@ __device__ __forceinline__ void append_kv(const Q8AppendArgs &a, const AppendGri
             for (int h = 0; h < kHeads; ++h) {
                 if (h >= nh) break;
                 const float now = sh.now[local + h];
-                float y[16];
+                float y[2 * kPairs<N>];
                 it.values(d[h], cs, 1, y);
-                store_item<KV, VEC>(it, o + h * D, y, now, divider(now));
+                store_item<KV, N>(it, o + h * D, y, now, divider(now));
             }
         }
     }
@@ -363,7 +372,7 @@ __device__ __forceinline__ void append_kv(const Q8AppendArgs &a, const AppendGri
 // CTAs [0, q_ctas) rotate q and stay while K's blocks and then V's, which take less time,
 // go through the other slots (K and V alternating left every other SM with K only).  HP:
 // heads of a thread that rotates q.
-template <int KV, bool VEC, bool FIXED, int HP>
+template <int KV, int N, bool FIXED, int HP>
 __global__ void __launch_bounds__(kThreads, 2)
     append_q8_kernel(const __grid_constant__ Q8AppendArgs a, const __grid_constant__ RopeArgs q,
                      const AppendGrid gr, const RopeGrid qgr) {
@@ -377,30 +386,49 @@ __global__ void __launch_bounds__(kThreads, 2)
     const unsigned q_ctas = gr.q_ctas;
     if (blockIdx.x < q_ctas) {
         pdl_wait_primary();
-        rope_tiles<__half, VEC, FIXED, HP>(q, a.rope, qgr, blockIdx.x, q_ctas, smem, sh.pos);
+        rope_tiles<__half, N, FIXED, HP>(q, a.rope, qgr, blockIdx.x, q_ctas, smem, sh.pos);
         return;
     }
-    const int ir = rope_items(a.rope.rope_dims, VEC);
-    for (int i = threadIdx.x; i < 8 * ir; i += kThreads) {
-        const int pair = Item<__half, VEC>::pair_of(i & 7, i >> 3, a.rope.rope_dims, a.rope.traditional != 0);
+    const int ir = rope_items(a.rope.rope_dims, N);
+    for (int i = threadIdx.x; i < kPairs<N> * ir; i += kThreads) {
+        const int j = i / kPairs<N>;
+        const int pair = Item<__half, N>::pair_of(i - j * kPairs<N>, j, a.rope.rope_dims, a.rope.traditional != 0);
         sh.kv.frac[i] = a.rope.turn_frac[min(pair, a.rope.rope_dims / 2 - 1)];
     }
     pdl_wait_primary();
     const unsigned i = blockIdx.x - q_ctas, half = gr.kv_ctas / 2;
     const unsigned rest = i < half ? i : i - half, w = rest / static_cast<unsigned>(gr.head_chunks);
     const int chunk = static_cast<int>(rest - w * gr.head_chunks);
-    if (i < half) append_kv<KV, VEC, false>(a, gr, w, chunk, sh.kv);
-    else append_kv<KV, VEC, true>(a, gr, w, chunk, sh.kv);
+    if (i < half) append_kv<KV, N, false>(a, gr, w, chunk, sh.kv);
+    else append_kv<KV, N, true>(a, gr, w, chunk, sh.kv);
 }
 
+struct Instance {
+    const void *fn;
+    int ring_bytes;
+};
+template <int KV, int N, bool FIXED, int HP>
+Instance instance() {
+    return Instance{reinterpret_cast<const void *>(append_q8_kernel<KV, N, FIXED, HP>), kRingBytes<__half, N, HP>};
+}
+template <int KV, int N>
+Instance instance_of(int hp) {
+    return hp == 4 ? instance<KV, N, false, 4>() : hp == 2 ? instance<KV, N, false, 2>() : instance<KV, N, false, 1>();
+}
 template <int KV>
-const void *kernel_of(bool vec, bool fixed, int hp) {
-    if (!vec) return reinterpret_cast<const void *>(append_q8_kernel<KV, false, false, 1>);
-    if (fixed)
-        return hp == 2 ? reinterpret_cast<const void *>(append_q8_kernel<KV, true, true, 2>)
-                       : reinterpret_cast<const void *>(append_q8_kernel<KV, true, true, 1>);
-    return hp == 2 ? reinterpret_cast<const void *>(append_q8_kernel<KV, true, false, 2>)
-                   : reinterpret_cast<const void *>(append_q8_kernel<KV, true, false, 1>);
+Instance instance_of(int width, bool fixed, int hp) {
+    if (width == 1) return instance<KV, 1, false, 1>();
+    if (width == 4) return instance_of<KV, 4>(hp);
+    if (width == 8) return instance_of<KV, 8>(hp);
+    if (fixed) return hp == 2 ? instance<KV, 16, true, 2>() : instance<KV, 16, true, 1>();
+    return hp == 2 ? instance<KV, 16, false, 2>() : instance<KV, 16, false, 1>();
+}
+
+// Channels of an item, one by one where smaller items would need more than a warp's
+// lanes for a row.
+int append_width(int rope_dims, int D) {
+    const int width = item_width(rope_dims, D);
+    return D > 32 * width ? 1 : width;
 }
 
 // One token per sequence (a decode step), bound by latency: a CTA takes some of the
@@ -414,7 +442,7 @@ struct TokenGrid {
     int chunks;            // CTAs of a token
 };
 
-template <int KV, bool VEC>
+template <int KV, int N>
 __global__ void __launch_bounds__(kThreads, 3)
     append_token_kernel(const __grid_constant__ Q8AppendArgs a, const TokenGrid gr) {
     __shared__ float2 table[128];  // rope_dims / 2 entries at most, in slots of eight
@@ -422,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     pdl_wait_primary();
     const unsigned ub = blockIdx.x / static_cast<unsigned>(gr.chunks);
     const int b = static_cast<int>(ub), chunk = static_cast<int>(blockIdx.x - ub * gr.chunks);
-    const int D = a.D, ir = rope_items(a.rope.rope_dims, VEC);
+    const int D = a.D, ir = rope_items(a.rope.rope_dims, N);
     const int item = threadIdx.x & (gr.lanes - 1);
     const uint32_t p = __ldg(a.cur_pos + b);
 
@@ -432,15 +460,15 @@ __global__ void __launch_bounds__(kThreads, 3)
     const int items = is_v ? gr.items_v : gr.items_k;
     const bool mine = head < a.H + 2 * a.kv_heads && item < items;
     if (!is_q) head -= is_v ? a.H + a.kv_heads : a.H;
-    const Item<__half, VEC> it(item, is_v ? 0 : a.rope.rope_dims, D, a.rope.traditional != 0);
-    ItemData<__half> d;
+    const Item<__half, N> it(item, is_v ? 0 : a.rope.rope_dims, D, a.rope.traditional != 0);
+    ItemData<__half, N> d;
     if (mine) {
         const __half *src = reinterpret_cast<const __half *>(is_q ? a.q : is_v ? a.v : a.k);
         const long long stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
         it.load(src + b * stride + static_cast<long long>(head) * D, d);
     }
     // The rotation is defined at every position; an append outside the cache is reported.
-    RopeFiller<__half, VEC>(ir, a.rope, false).fill(table, 1, [&](int) { return p; });
+    RopeFiller<__half, N>(ir, a.rope, false).fill(table, 1, [&](int) { return p; });
     bool ok = p < static_cast<uint32_t>(a.S);
     long long row0 = 0, srow = 0;
     int before = 0;
@@ -455,10 +483,10 @@ __global__ void __launch_bounds__(kThreads, 3)
     float *const scale = (is_v ? a.vs : a.ks) + srow * a.kv_heads + head;
     const float old = ok && before > 0 && mine && !is_q ? *scale : 0.f;
     __syncthreads();
-    float y[16], mx = 0.f;
+    float y[2 * kPairs<N>], mx = 0.f;
     if (mine) {
         it.values(d, table + item, ir, y);
-        if (!is_q) mx = item_max(y);
+        if (!is_q) mx = item_max<2 * kPairs<N>>(y);
     }
     for (int o = gr.lanes / 2; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
     if (!mine) return;
@@ -476,24 +504,29 @@ __global__ void __launch_bounds__(kThreads, 3)
     if (before > 0 && now != old)
         requantise<KV>(block0, row_elems, D, before, old / now, item, items, 0, 1);
     if (item == 0) *scale = now;
-    store_item<KV, VEC>(it, block0 + before * row_elems, y, now, divider(now));
+    store_item<KV, N>(it, block0 + before * row_elems, y, now, divider(now));
+}
+
+template <int KV>
+const void *token_kernel_of(int width) {
+    if (width == 16) return reinterpret_cast<const void *>(append_token_kernel<KV, 16>);
+    if (width == 8) return reinterpret_cast<const void *>(append_token_kernel<KV, 8>);
+    if (width == 4) return reinterpret_cast<const void *>(append_token_kernel<KV, 4>);
+    return reinterpret_cast<const void *>(append_token_kernel<KV, 1>);
 }
 
 cudaError_t launch_append_token(const Q8AppendArgs &a, int kv, cudaStream_t stream) {
-    const bool vec = a.rope.rope_dims % 16 == 0;
+    const int width = append_width(a.rope.rope_dims, a.D);
     TokenGrid gr{};
-    gr.items_k = row_items(a.rope.rope_dims, a.D, vec);
-    gr.items_v = row_items(0, a.D, vec);
+    gr.items_k = row_items(a.rope.rope_dims, a.D, width);
+    gr.items_v = row_items(0, a.D, width);
     gr.lanes = 1;
     while (gr.lanes < std::max(gr.items_k, gr.items_v)) gr.lanes *= 2;
     const long long chunks = ((a.H + 2LL * a.kv_heads) * gr.lanes + kThreads - 1) / kThreads;
     const long long blocks = a.B * chunks;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     gr.chunks = static_cast<int>(chunks);
-    const void *fn = kv == kKvE4m3 ? (vec ? reinterpret_cast<const void *>(append_token_kernel<kKvE4m3, true>)
-                                          : reinterpret_cast<const void *>(append_token_kernel<kKvE4m3, false>))
-                                   : (vec ? reinterpret_cast<const void *>(append_token_kernel<kKvInt8, true>)
-                                          : reinterpret_cast<const void *>(append_token_kernel<kKvInt8, false>));
+    const void *fn = kv == kKvE4m3 ? token_kernel_of<kKvE4m3>(width) : token_kernel_of<kKvInt8>(width);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(blocks));
     cfg.blockDim = dim3(kThreads);
@@ -514,11 +547,15 @@ cudaError_t launch_append_q8(const Q8AppendArgs &a, int kv, int sms, cudaStream_
     const int rd = a.rope.rope_dims;
     RopeGrid qgr{};
     int hp = 1;
-    bool vec = false, fixed = false;
-    if (!rope_grid(a.tokens, a.H, a.D, rd, 2, sms, &qgr, &hp, &vec, &fixed)) return cudaErrorInvalidValue;
+    bool fixed = false;
+    const int width = append_width(rd, a.D);
+    // of q two heads per thread, of its smaller items four (8192 tokens of 32 query and 8
+    // key/value heads of 96 channels, 24 of them rotated: 44 us with 4, 48 with 2, 62 with 1)
+    if (!rope_grid(a.tokens, a.H, a.D, rd, width == 16 ? 2 : 4, sms, &qgr, &hp, width, &fixed))
+        return cudaErrorInvalidValue;
     AppendGrid gr{};
-    gr.items_k = row_items(rd, a.D, vec);
-    gr.items_v = row_items(0, a.D, vec);
+    gr.items_k = row_items(rd, a.D, width);
+    gr.items_v = row_items(0, a.D, width);
     gr.lanes = 1;
     while (gr.lanes < std::max(gr.items_k, gr.items_v)) gr.lanes *= 2;
     // rows of a block: side by side in the lanes of a warp first, then in more warps
@@ -553,14 +590,11 @@ cudaError_t launch_append_q8(const Q8AppendArgs &a, int kv, int sms, cudaStream_
     q.tokens = a.tokens;
     q.H = a.H;
     q.D = a.D;
-    const void *fn = kv == kKvE4m3 ? kernel_of<kKvE4m3>(vec, fixed, hp) : kernel_of<kKvInt8>(vec, fixed, hp);
-    const int ring = !vec   ? 0
-                     : hp == 2 ? kStages<__half, 2> * kTileBytes<__half, 2>
-                               : kStages<__half, 1> * kTileBytes<__half, 1>;
-    const size_t smem = rope_smem(qgr, rd, vec, ring);
+    const Instance in = kv == kKvE4m3 ? instance_of<kKvE4m3>(width, fixed, hp) : instance_of<kKvInt8>(width, fixed, hp);
+    const size_t smem = rope_smem(qgr, rd, width, in.ring_bytes);
     if (smem > 32 * 1024) {  // with the static part past the default limit
         const cudaError_t e =
-            cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            cudaFuncSetAttribute(in.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -574,7 +608,7 @@ cudaError_t launch_append_q8(const Q8AppendArgs &a, int kv, int sms, cudaStream_
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     void *args[] = {const_cast<Q8AppendArgs *>(&a), &q, &gr, &qgr};
-    return cudaLaunchKernelExC(&cfg, fn, args);
+    return cudaLaunchKernelExC(&cfg, in.fn, args);
 }
 
 }  // namespace dattn

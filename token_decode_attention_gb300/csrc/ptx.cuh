@@ -143,6 +143,11 @@ __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, int byt
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
+template <int N>  // 4, 8 or 16 bytes
+__device__ __forceinline__ void cp_async(uint32_t dst, const void *src) {
+    if constexpr (N == 16) cp_async16(dst, src, 16);
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
+}
 __device__ __forceinline__ void cp_async_commit() {
     asm volatile("cp.async.commit_group;" ::: "memory");
 }

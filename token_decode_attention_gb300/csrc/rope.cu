@@ -21,14 +21,14 @@
 namespace dattn {
 namespace {
 
-template <typename T, bool VEC, bool FIXED, int HP>
-__global__ void __launch_bounds__(kRopeThreads, (kRopeBlocks<T, HP>))
+template <typename T, int N, bool FIXED, int HP>
+__global__ void __launch_bounds__(kRopeThreads, (kRopeBlocks<T, N, HP>))
     rope_kernel(const __grid_constant__ RopeArgs a, const RopeGrid gr) {
     extern __shared__ __align__(16) unsigned char smem[];
     __shared__ uint32_t s_pos[2][kRopeThreads];
     pdl_launch_dependents();
     pdl_wait_primary();
-    rope_tiles<T, VEC, FIXED, HP>(a, a.rope, gr, blockIdx.x, gridDim.x, smem, s_pos);
+    rope_tiles<T, N, FIXED, HP>(a, a.rope, gr, blockIdx.x, gridDim.x, smem, s_pos);
 }
 
 struct Instance {
@@ -36,19 +36,25 @@ struct Instance {
     int min_blocks, ring_bytes;
 };
 
-template <typename T, bool VEC, bool FIXED, int HP>
+template <typename T, int N, bool FIXED, int HP>
 Instance instance() {
-    return Instance{reinterpret_cast<const void *>(rope_kernel<T, VEC, FIXED, HP>), kRopeBlocks<T, HP>,
-                    VEC ? kStages<T, HP> * kTileBytes<T, HP> : 0};
+    return Instance{reinterpret_cast<const void *>(rope_kernel<T, N, FIXED, HP>), kRopeBlocks<T, N, HP>,
+                    kRingBytes<T, N, HP>};
 }
 
+template <typename T, int N>
+Instance instance_of(int hp) {
+    return hp == 4 ? instance<T, N, false, 4>() : hp == 2 ? instance<T, N, false, 2>() : instance<T, N, false, 1>();
+}
 template <typename T>
-Instance instance_of(bool vec, bool fixed, int hp) {
-    if (!vec) return instance<T, false, false, 1>();
+Instance instance_of(int width, bool fixed, int hp) {
+    if (width == 1) return instance<T, 1, false, 1>();
+    if (width == 4) return instance_of<T, 4>(hp);
+    if (width == 8) return instance_of<T, 8>(hp);
     if constexpr (sizeof(T) == 2)
-        if (fixed && hp == 4) return instance<T, true, true, 4>();
-    if (fixed) return hp == 2 ? instance<T, true, true, 2>() : instance<T, true, true, 1>();
-    return hp == 2 ? instance<T, true, false, 2>() : instance<T, true, false, 1>();
+        if (fixed && hp == 4) return instance<T, 16, true, 4>();
+    if (fixed) return hp == 2 ? instance<T, 16, true, 2>() : instance<T, 16, true, 1>();
+    return hp == 2 ? instance<T, 16, false, 2>() : instance<T, 16, false, 1>();
 }
 
 }  // namespace
@@ -56,17 +62,19 @@ Instance instance_of(bool vec, bool fixed, int hp) {
 cudaError_t launch_rope(const RopeArgs &a, int dtype, int sms, cudaStream_t stream) {
     RopeGrid gr{};
     int hp = 1;
-    bool vec = false, fixed = false;
-    // four heads in 16 bits where a thread's item is fixed, two otherwise
-    int most = 2;
-    if (dtype != kDtypeF32 && a.rope.rope_dims % 16 == 0 && a.D % 16 == 0 && kRopeThreads % (a.D / 16) == 0) most = 4;
-    if (!rope_grid(a.tokens, a.H, a.D, a.rope.rope_dims, most, sms, &gr, &hp, &vec, &fixed))
+    bool fixed = false;
+    const int width = item_width(a.rope.rope_dims, a.D);
+    // of items of 16 channels four heads in 16 bits where a thread's item is fixed, two
+    // otherwise; of smaller items four
+    int most = width < 16 ? 4 : 2;
+    if (dtype != kDtypeF32 && width == 16 && kRopeThreads % (a.D / 16) == 0) most = 4;
+    if (!rope_grid(a.tokens, a.H, a.D, a.rope.rope_dims, most, sms, &gr, &hp, width, &fixed))
         return cudaErrorInvalidValue;
-    const Instance in = dtype == kDtypeF16    ? instance_of<__half>(vec, fixed, hp)
-                        : dtype == kDtypeBf16 ? instance_of<__nv_bfloat16>(vec, fixed, hp)
-                                              : instance_of<float>(vec, fixed, hp);
+    const Instance in = dtype == kDtypeF16    ? instance_of<__half>(width, fixed, hp)
+                        : dtype == kDtypeBf16 ? instance_of<__nv_bfloat16>(width, fixed, hp)
+                                              : instance_of<float>(width, fixed, hp);
     const long long ctas = std::min(gr.tiles, static_cast<long long>(sms) * in.min_blocks);
-    const size_t smem = rope_smem(gr, a.rope.rope_dims, vec, in.ring_bytes);
+    const size_t smem = rope_smem(gr, a.rope.rope_dims, width, in.ring_bytes);
     if (smem > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(in.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));

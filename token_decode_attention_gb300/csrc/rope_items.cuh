@@ -1,13 +1,16 @@
 // rope_items.cuh -- the pieces of a head row that the rotary kernels work on.
 //
 // A row of D channels, the first rope_dims of them rotated in pairs, is cut
-// into items of 16 channels, one thread each: eight pairs (u, w), channels
-// (i, i + rope_dims/2) in the half layout and (2i, 2i + 1) in the interleaved
-// one, or 16 channels that pass through.  A thread needs no other thread's
-// data.  VEC (rope_dims and D multiples of 16): an item is sizeof(T) runs of 16
-// bytes, spread evenly over the rotated (or the passing) channels, so that in
-// either layout neighbouring threads read and write neighbouring vectors.
-// Otherwise the elements are read one by one.
+// into items of N = 16, 8 or 4 channels, the most that divide rope_dims and D, one
+// thread each: N / 2 pairs (u, w), channels (i, i + rope_dims/2) in the half layout
+// and (2i, 2i + 1) in the interleaved one, or N channels that pass through.  A thread
+// needs no other thread's data.  An item is two runs or four (16 channels in 32 bits)
+// of at most 16 bytes, spread evenly over the rotated (or the passing) channels, so
+// that in either layout neighbouring threads read and write neighbouring runs.
+// Where four do not divide rope_dims (N = 1) an item has up to 16 channels, read one
+// by one.  Measured on 8192 tokens of 32 heads in f16, us: 80 channels with 16, 20 and 6
+// rotated (N = 16, 4, 1) 18.9, 22.1, 110; 96 channels with 24 rotated (N = 8) 23.7, one by
+// one 135.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -66,36 +69,62 @@ __device__ __forceinline__ long long used_tokens(const int *offsets, int B, long
     return offsets ? min(tokens, max(0LL, static_cast<long long>(__ldg(offsets + B)))) : tokens;
 }
 
-__host__ __device__ inline int rope_items(int rope_dims, bool vec) {
-    return vec ? rope_dims / 16 : (rope_dims / 2 + 7) / 8;
+// Channels of an item; 1: up to 16, one by one.
+__host__ __device__ inline int item_width(int rope_dims, int D) {
+    return (rope_dims | D) % 16 == 0 ? 16 : (rope_dims | D) % 8 == 0 ? 8 : (rope_dims | D) % 4 == 0 ? 4 : 1;
+}
+__host__ __device__ inline int rope_items(int rope_dims, int width) {
+    return width > 1 ? rope_dims / width : (rope_dims / 2 + 7) / 8;
 }
 // Items of a row: the rotated ones, then those of the channels that pass through.
-__host__ __device__ inline int row_items(int rope_dims, int D, bool vec) {
-    return rope_items(rope_dims, vec) + (D - rope_dims + 15) / 16;
+__host__ __device__ inline int row_items(int rope_dims, int D, int width) {
+    return rope_items(rope_dims, width) + (width > 1 ? (D - rope_dims) / width : (D - rope_dims + 15) / 16);
 }
 
-// Sixteen elements of an item.
-template <typename T>
-struct ItemData {
-    uint4 v[sizeof(T)];
+// Pairs of an item, at most.
+template <int N>
+constexpr int kPairs = N == 1 ? 8 : N / 2;
+
+// The elements of an item.
+template <typename T, int N>
+struct __align__(16) ItemData {
+    T e[2 * kPairs<N>];
 };
 
-// Sixteen fp32 values rounded to T.
-__device__ __forceinline__ void round_item(const float *y, ItemData<__half> &x) {
-    __half2 *h = reinterpret_cast<__half2 *>(x.v);
+// fp32 values rounded to T.
+template <int N>
+__device__ __forceinline__ void round_item(const float *y, ItemData<__half, N> &x) {
+    __half2 *h = reinterpret_cast<__half2 *>(x.e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
+    for (int i = 0; i < kPairs<N>; ++i) h[i] = __floats2half2_rn(y[2 * i], y[2 * i + 1]);
 }
-__device__ __forceinline__ void round_item(const float *y, ItemData<__nv_bfloat16> &x) {
-    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(x.v);
+template <int N>
+__device__ __forceinline__ void round_item(const float *y, ItemData<__nv_bfloat16, N> &x) {
+    __nv_bfloat162 *h = reinterpret_cast<__nv_bfloat162 *>(x.e);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) h[i] = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
+    for (int i = 0; i < kPairs<N>; ++i) h[i] = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
 }
-__device__ __forceinline__ void round_item(const float *y, ItemData<float> &x) {
-    float *f = reinterpret_cast<float *>(x.v);
+template <int N>
+__device__ __forceinline__ void round_item(const float *y, ItemData<float, N> &x) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) f[i] = y[i];
+    for (int i = 0; i < 2 * kPairs<N>; ++i) x.e[i] = y[i];
 }
+
+// BYTES moved at once.
+template <int BYTES>
+struct PieceOf;
+template <>
+struct PieceOf<4> {
+    using type = uint32_t;
+};
+template <>
+struct PieceOf<8> {
+    using type = uint2;
+};
+template <>
+struct PieceOf<16> {
+    using type = uint4;
+};
 
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
@@ -115,22 +144,26 @@ __device__ __forceinline__ float from_float<float>(float x) {
     return x;
 }
 
-// Item j of a row of T.  Elements k = 0 .. 15: in the half layout u of pair e is
-// element e and w element e + 8, in the interleaved one 2e and 2e + 1.
-template <typename T, bool VEC>
+// Item j of a row of T.  Elements k = 0 .. 2 P - 1, P = kPairs<N>: in the half layout u
+// of pair e is element e and w element e + P, in the interleaved one 2e and 2e + 1.
+template <typename T, int N>
 struct Item {
-    static constexpr int kRuns = sizeof(T), kRun = 16 / kRuns;  // runs of 16 bytes
+    static constexpr bool kVec = N > 1;
+    static constexpr int P = kPairs<N>;
+    static constexpr int kRuns = N * sizeof(T) > 32 ? 4 : 2, kRun = 2 * P / kRuns;
+    static constexpr int kRunBytes = kVec ? kRun * static_cast<int>(sizeof(T)) : 16;
+    using Run = typename PieceOf<kRunBytes>::type;
     int j, rope_dims, D;
     bool rot, trad;
-    int first, hop;  // VEC: channel of run r: first + r hop; else two runs of eight
+    int first, hop;  // kVec: channel of run r: first + r hop; else two runs of eight
                      // channels at most, at first and first + hop, n0 and n1 long
     int n0, n1;
 
     __device__ __forceinline__ Item(int j_, int rope_dims_, int D_, bool trad_)
         : j(j_), rope_dims(rope_dims_), D(D_), trad(trad_) {
-        const int ir = rope_items(rope_dims, VEC);
+        const int ir = rope_items(rope_dims, N);
         rot = j < ir;
-        if constexpr (VEC) {
+        if constexpr (kVec) {
             first = rot ? kRun * j : rope_dims + kRun * (j - ir);
             hop = (rot ? rope_dims : D - rope_dims) / kRuns;
             n0 = n1 = kRun;
@@ -145,99 +178,96 @@ struct Item {
     }
     // The pair that slot e of item j rotates, or one past the last.
     static __device__ __forceinline__ int pair_of(int e, int j, int rope_dims, bool trad) {
-        if constexpr (VEC) {
+        if constexpr (kVec) {
             const int k = trad ? 2 * e : e;
             const int c = k / kRun * (rope_dims / kRuns) + kRun * j + k % kRun;
             return trad ? c >> 1 : c;
         }
         return 8 * j + e;
     }
-    __device__ __forceinline__ void load(const T *row, ItemData<T> &x) const {
-        if constexpr (VEC) {
+    __device__ __forceinline__ void load(const T *row, ItemData<T, N> &x) const {
+        if constexpr (kVec) {
 #pragma unroll
             for (int r = 0; r < kRuns; ++r)
-                x.v[r] = __ldg(reinterpret_cast<const uint4 *>(row + first + r * hop));
+                reinterpret_cast<Run *>(x.e)[r] = __ldg(reinterpret_cast<const Run *>(row + first + r * hop));
         } else {
             // without branches, so that all sixteen are in flight: what is past the
             // end of a run (which may be empty, but for the first) is read elsewhere
             const T *u = row + first, *w = n1 > 0 ? u + hop : u;
-            T *e = reinterpret_cast<T *>(x.v);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                e[k] = u[k < n0 ? k : 0];
-                e[k + 8] = w[k < n1 ? k : 0];
+                x.e[k] = u[k < n0 ? k : 0];
+                x.e[k + 8] = w[k < n1 ? k : 0];
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                e[k] = k < n0 ? e[k] : from_float<T>(0.f);
-                e[k + 8] = k < n1 ? e[k + 8] : from_float<T>(0.f);
+                x.e[k] = k < n0 ? x.e[k] : from_float<T>(0.f);
+                x.e[k + 8] = k < n1 ? x.e[k + 8] : from_float<T>(0.f);
             }
         }
     }
-    __device__ __forceinline__ void store(T *row, const ItemData<T> &x) const {
-        if constexpr (VEC) {
+    __device__ __forceinline__ void store(T *row, const ItemData<T, N> &x) const {
+        if constexpr (kVec) {
 #pragma unroll
             for (int r = 0; r < kRuns; ++r)
-                *reinterpret_cast<uint4 *>(row + first + r * hop) = x.v[r];
+                *reinterpret_cast<Run *>(row + first + r * hop) = reinterpret_cast<const Run *>(x.e)[r];
         } else {
             T *u = row + first, *w = u + hop;
-            const T *e = reinterpret_cast<const T *>(x.v);
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                if (k < n0) u[k] = e[k];
-                if (k < n1) w[k] = e[k + 8];
+                if (k < n0) u[k] = x.e[k];
+                if (k < n1) w[k] = x.e[k + 8];
             }
         }
     }
     // The elements in fp32, those of a rotated item turned by the (cos, sin) of its
     // slots, at table[0], table[items], ...
-    __device__ __forceinline__ void values(const ItemData<T> &x, const float2 *table, int items,
+    __device__ __forceinline__ void values(const ItemData<T, N> &x, const float2 *table, int items,
                                            float *y) const {
-        const T *e = reinterpret_cast<const T *>(x.v);
         if (!rot) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) y[k] = to_float(e[k]);
+            for (int k = 0; k < 2 * P; ++k) y[k] = to_float(x.e[k]);
         } else if (trad) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < P; ++k) {
                 const float2 cs = table[k * items];
-                const float u = to_float(e[2 * k]), w = to_float(e[2 * k + 1]);
+                const float u = to_float(x.e[2 * k]), w = to_float(x.e[2 * k + 1]);
                 y[2 * k] = u * cs.x - w * cs.y;
                 y[2 * k + 1] = u * cs.y + w * cs.x;
             }
         } else {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < P; ++k) {
                 const float2 cs = table[k * items];
-                const float u = to_float(e[k]), w = to_float(e[k + 8]);
+                const float u = to_float(x.e[k]), w = to_float(x.e[k + P]);
                 y[k] = u * cs.x - w * cs.y;
-                y[k + 8] = u * cs.y + w * cs.x;
+                y[k + P] = u * cs.y + w * cs.x;
             }
         }
     }
 };
 
-// A thread's part in building the cos/sin tables of some positions, 8 * items entries
+// A thread's part in building the cos/sin tables of some positions, kPairs<N> * items entries
 // each: slot e of item j at e * items + j, so that threads on neighbouring items read
 // neighbouring entries.  The CTA's threads (a power of two, 256 or more) keep one slot
 // each and go through the positions; the turn fraction, which neighbouring threads
 // fetch from different places of the parameters, is fetched once.
-template <typename T, bool VEC>
+template <typename T, int N>
 struct RopeFiller {
     int entries, slot, row0, hop;  // row0 < 0: no part
     float mag_c, mag_s;
     unsigned long long frac;
 
     __device__ __forceinline__ RopeFiller(int items, const RopeTable &r, bool gradient)
-        : entries(8 * items), slot(0), row0(-1), hop(1), mag_c(r.magnitude),
+        : entries(kPairs<N> * items), slot(0), row0(-1), hop(1), mag_c(r.magnitude),
           mag_s(gradient ? -r.magnitude : r.magnitude), frac(0) {
         if (items == 0) return;
-        int lanes = 8;
+        int lanes = 1;
         while (lanes < entries) lanes *= 2;
         slot = threadIdx.x & (lanes - 1);
         hop = blockDim.x / lanes;
         const int e = slot / items;
-        const int pair = Item<T, VEC>::pair_of(e, slot - e * items, r.rope_dims, r.traditional != 0);
+        const int pair = Item<T, N>::pair_of(e, slot - e * items, r.rope_dims, r.traditional != 0);
         if (slot < entries && pair < r.rope_dims / 2) {
             row0 = threadIdx.x / lanes;
             frac = r.turn_frac[pair];

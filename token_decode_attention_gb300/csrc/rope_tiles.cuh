@@ -22,14 +22,16 @@ namespace {
 constexpr int kRopeThreads = 256;
 // A thread's share of a tile is the same item of HP neighbouring heads: their cosines
 // are fetched once and the bookkeeping of a tile is paid once.
-// Bytes of a tile, stages of the ring and CTAs of an SM, which keep 120 to 190 KB of
+// Bytes of a tile, stages of the ring and CTAs of an SM, which keep up to 190 KB of
 // an SM's shared memory and its registers busy.
-template <typename T, int HP>
-constexpr int kTileBytes = kRopeThreads * HP * 16 * static_cast<int>(sizeof(T));
-template <typename T, int HP>
-constexpr int kStages = kTileBytes<T, HP> > 16384 ? 2 : 3;
-template <typename T, int HP>
-constexpr int kRopeBlocks = HP == 4 ? 2 : sizeof(T) == 4 ? 3 : 4;
+template <typename T, int N, int HP>
+constexpr int kTileBytes = kRopeThreads * HP * static_cast<int>(sizeof(ItemData<T, N>::e));
+template <typename T, int N, int HP>
+constexpr int kStages = N == 1 ? 0 : kTileBytes<T, N, HP> > 16384 ? 2 : kTileBytes<T, N, HP> < 8192 ? 4 : 3;
+template <typename T, int N, int HP>
+constexpr int kRopeBlocks = N == 16 && HP == 4 ? 2 : N == 16 && sizeof(T) == 4 ? 3 : 4;
+template <typename T, int N, int HP>
+constexpr int kRingBytes = kStages<T, N, HP> * kTileBytes<T, N, HP>;
 
 struct RopeGrid {
     long long tiles;
@@ -42,16 +44,18 @@ struct RopeGrid {
 // threads), so what depends on it is computed once.
 // CTA `cta` of `ctas` (kRopeThreads threads) rotates its run of tiles; smem: rope_smem()
 // bytes.
-template <typename T, bool VEC, bool FIXED, int HP>
+template <typename T, int N, bool FIXED, int HP>
 __device__ __forceinline__ void rope_tiles(const RopeArgs &a, const RopeTable &rope, const RopeGrid &gr,
                                            unsigned cta, unsigned ctas, unsigned char *smem,
                                            uint32_t (*s_pos)[kRopeThreads]) {
-    constexpr int kRuns = sizeof(T), kRing = kStages<T, HP>;
-    // behind the ring of the vector form: [2][max_tokens][8 * rotated items]
-    float2 *const table = reinterpret_cast<float2 *>(smem + (VEC ? kRing * kTileBytes<T, HP> : 0));
+    using It = Item<T, N>;
+    constexpr int kRing = kStages<T, N, HP>;
+    constexpr bool kVec = It::kVec;
+    // behind the ring: [2][max_tokens][pairs of an item * rotated items]
+    float2 *const table = reinterpret_cast<float2 *>(smem + kRingBytes<T, N, HP>);
     const int D = a.D, rd = rope.rope_dims, tid = threadIdx.x;
     const bool trad = rope.traditional != 0;
-    const int ir = rope_items(rd, VEC), entries = 8 * ir;
+    const int ir = rope_items(rd, N), entries = kPairs<N> * ir;
     // token numbers fit 31 bits
     const int used = static_cast<int>(used_tokens(a.offsets, a.B, a.tokens));
     const int first = static_cast<int>(gr.tiles * cta / ctas);
@@ -139,35 +143,36 @@ __device__ __forceinline__ void rope_tiles(const RopeArgs &a, const RopeTable &r
         }
         return from + static_cast<uint32_t>(n);
     };
-    const RopeFiller<T, VEC> filler(ir, rope, a.gradient != 0);
+    const RopeFiller<T, N> filler(ir, rope, a.gradient != 0);
     auto fill = [&](const Tile &t, int half) {
         const int touched = min(gr.max_tokens, fast_div(t.skip + kRopeThreads - 1, gr.div_token) + 1);
         filler.fill(table + half * gr.max_tokens * entries, touched, [&](int s) { return s_pos[half][s]; });
     };
-    const Item<T, VEC> fixed(p.item, rd, D, trad);
+    const It fixed(p.item, rd, D, trad);
     auto item_of = [&](const Place &x) {
         if constexpr (FIXED) return fixed;
-        return Item<T, VEC>(x.item, rd, D, trad);
+        return It(x.item, rd, D, trad);
     };
     // run r of head h of this thread's item in a stage of the ring
     auto slot = [&](int stage, int h, int r) {
-        return (((stage * HP + h) * kRuns + r) * kRopeThreads + tid) * 16;
+        return (((stage * HP + h) * It::kRuns + r) * kRopeThreads + tid) * It::kRunBytes;
     };
     const uint32_t ring = smem_addr(smem);
     auto fetch = [&](const Place &q, int stage) {
         if (q.token < used) {
-            const Item<T, VEC> it = item_of(q);
+            const It it = item_of(q);
             const T *x = q.x + it.first;
 #pragma unroll
             for (int h = 0; h < HP; ++h)
 #pragma unroll
-                for (int r = 0; r < kRuns; ++r) cp_async16(ring + slot(stage, h, r), x + h * D + r * it.hop, 16);
+                for (int r = 0; r < It::kRuns; ++r)
+                    cp_async<It::kRunBytes>(ring + slot(stage, h, r), x + h * D + r * it.hop);
         }
     };
 
     if (count <= 0) return;
     Place pf = p;  // the item that is fetched next
-    if constexpr (VEC) {
+    if constexpr (kVec) {
 #pragma unroll
         for (int i = 0; i < kRing - 1; ++i) {
             if (i < count) fetch(pf, i);
@@ -185,7 +190,7 @@ __device__ __forceinline__ void rope_tiles(const RopeArgs &a, const RopeTable &r
     int stage = 0;
     for (int k = 0; k < count; ++k) {
         const int half = k & 1;
-        if constexpr (VEC) {
+        if constexpr (kVec) {
             const int into = stage == 0 ? kRing - 1 : stage - 1;
             if (k + kRing - 1 < count) fetch(pf, into);
             cp_async_commit();
@@ -195,30 +200,31 @@ __device__ __forceinline__ void rope_tiles(const RopeArgs &a, const RopeTable &r
         next(ahead);  // two tiles on
         const uint32_t pos = k + 2 < count ? position(ahead) : 0u;
         if (p.token < used) {
-            const Item<T, VEC> it = item_of(p);
+            const It it = item_of(p);
             const float2 *const entry = table + (half * gr.max_tokens + p.token - cur.token) * entries + it.j;
-            float2 cs[8];
+            float2 cs[kPairs<N>];
             if (it.rot) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) cs[e] = entry[e * ir];
+                for (int e = 0; e < kPairs<N>; ++e) cs[e] = entry[e * ir];
             }
 #pragma unroll
             for (int h = 0; h < HP; ++h) {
-                ItemData<T> d;
-                if constexpr (VEC) {
+                ItemData<T, N> d;
+                if constexpr (kVec) {
 #pragma unroll
-                    for (int r = 0; r < kRuns; ++r)
-                        d.v[r] = *reinterpret_cast<const uint4 *>(smem + slot(stage, h, r));
+                    for (int r = 0; r < It::kRuns; ++r)
+                        reinterpret_cast<typename It::Run *>(d.e)[r] =
+                            *reinterpret_cast<const typename It::Run *>(smem + slot(stage, h, r));
                 } else {
                     it.load(p.x + h * D, d);
                 }
-                float y[16];
+                float y[2 * kPairs<N>];
                 it.values(d, cs, 1, y);
                 round_item(y, d);
                 it.store(p.out + h * D, d);
             }
         }
-        if constexpr (VEC) stage = stage + 1 == kRing ? 0 : stage + 1;
+        if constexpr (kVec) stage = stage + 1 == kRing ? 0 : stage + 1;
         if (k + 1 == count) break;
         step(p);
         next(cur);
@@ -231,12 +237,11 @@ __device__ __forceinline__ void rope_tiles(const RopeArgs &a, const RopeTable &r
 // The launch of rows of `elem_bytes`: the heads of a thread, as many as divide the heads
 // (at most `most`) and leave every SM two CTAs, and the cut of the tokens into tiles.
 inline bool rope_grid(long long tokens, int H, int D, int rope_dims, int most, int sms, RopeGrid *gr,
-                      int *hp, bool *vec, bool *fixed) {
-    *vec = rope_dims % 16 == 0 && D % 16 == 0;
-    gr->items = row_items(rope_dims, D, *vec);
+                      int *hp, int width, bool *fixed) {
+    gr->items = row_items(rope_dims, D, width);
     if (static_cast<long long>(H) * gr->items > (1 << 30) || tokens > 0x7ffffc00LL) return false;
     *fixed = kRopeThreads % gr->items == 0;
-    *hp = *vec ? most : 1;
+    *hp = width > 1 ? most : 1;
     while (*hp > 1 && (H % *hp != 0 || tokens * H * gr->items < 2LL * sms * kRopeThreads * *hp)) *hp /= 2;
     gr->per_token = H / *hp * gr->items;
     gr->tiles = (tokens * gr->per_token + kRopeThreads - 1) / kRopeThreads;
@@ -248,9 +253,10 @@ inline bool rope_grid(long long tokens, int H, int D, int rope_dims, int most, i
 }
 
 // Shared memory behind a ring of `ring_bytes`: two tables of at most (256 / items + 2)
-// tokens of 8 items entries, 36 KB.
-inline size_t rope_smem(const RopeGrid &gr, int rope_dims, bool vec, int ring_bytes) {
-    return ring_bytes + static_cast<size_t>(2) * gr.max_tokens * 8 * rope_items(rope_dims, vec) * sizeof(float2);
+// tokens of 8 entries for 16 channels, 36 KB.
+inline size_t rope_smem(const RopeGrid &gr, int rope_dims, int width, int ring_bytes) {
+    const int entries = (width > 1 ? width / 2 : 8) * rope_items(rope_dims, width);
+    return ring_bytes + static_cast<size_t>(2) * gr.max_tokens * entries * sizeof(float2);
 }
 
 }  // namespace
