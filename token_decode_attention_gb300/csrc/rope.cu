@@ -73,8 +73,10 @@ cudaError_t launch_rope(const RopeArgs &a, int dtype, int sms, cudaStream_t stre
     const Instance in = dtype == kDtypeF16    ? instance_of<__half>(width, fixed, hp)
                         : dtype == kDtypeBf16 ? instance_of<__nv_bfloat16>(width, fixed, hp)
                                               : instance_of<float>(width, fixed, hp);
-    const long long ctas = std::min(gr.tiles, static_cast<long long>(sms) * in.min_blocks);
     const size_t smem = rope_smem(gr, a.rope.rope_dims, width, in.ring_bytes);
+    // resident CTAs: 228 KB an SM, 2 KB of positions and 1 KB of the system's for each
+    const long long fit = 228 * 1024 / (static_cast<long long>(smem) + 3 * 1024);
+    const long long ctas = std::min(gr.tiles, sms * std::max(1LL, std::min<long long>(in.min_blocks, fit)));
     if (smem > 48 * 1024) {
         const cudaError_t e =
             cudaFuncSetAttribute(in.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
