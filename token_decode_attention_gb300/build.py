@@ -20,10 +20,11 @@ OUT_DIR = os.path.join(HERE, "_build")
 LIB = os.path.join(OUT_DIR, "libdattn.so")
 SOURCES = ["decode_streamk.cu", "decode_cluster.cu", "decode_cluster_paged.cu", "combine.cu",
            "split_calls.cu", "decode_noalloc.cu", "selftest.cu", "softmax.cu", "rope_append.cu",
-           "decode_q8.cu", "decode_q8_int8.cu", "append_q8.cu", "rope.cu", "q8_api.cpp",
+           "decode_q8.cu", "decode_q8_int8.cu", "append_q8.cu", "append_q8_int8.cu", "rope.cu", "q8_api.cpp",
            "dattn_api.cpp"]
 HEADERS = ["dattn_internal.h", "ptx.cuh", "streamk.h", "merge.cuh", "decode_kernel.cuh",
-           "rope_items.cuh", "rope_tiles.cuh", "decode_q8_kernel.cuh"]
+           "rope_items.cuh", "rope_tiles.cuh", "decode_q8_kernel.cuh",
+           "append_q8_kernel.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xptxas", "-v",
