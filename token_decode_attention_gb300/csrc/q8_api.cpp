@@ -30,6 +30,7 @@ constexpr int kStaticSmem = 4096;  // the decode kernel's static shared memory a
 // and 7 in the split plan, 26.6 and 18.1.
 constexpr long long kClusterTiles = 8;
 constexpr long long kUnitTiles = 16;  // the same with a CTA for each unit
+constexpr long long kShortUnitTiles = 10;
 
 int fail(int status, const char *fmt, ...) {
     char buf[512];
@@ -229,12 +230,14 @@ size_t round_up(size_t x, size_t m) { return (x + m - 1) / m * m; }
 //
 // Units of their own CTAs, as many waves of them as it takes, where there are enough to
 // fill most of the SMs' slots and a warp's tiles of a full sequence are at most
-// kUnitTiles: the most heads for which both hold, but no fewer than an eighth of all
-// (shorter runs of the cache per position cost more than the split plan's merge).
-// Measured with ragged lengths, these units and the split plan, us: 512 sequences of 8
-// heads up to 128 positions 28.0, 62.2; 256 of 8 up to 1024 56.8, 70.7; 128 of 32 up to
-// 512 55.8, 59.2; 256 of 8 up to 2048, one head per CTA, 98.2, 108.8; 64 of 32 up to 1024,
-// two heads, which the eighth excludes, 54.2, 53.7.
+// kUnitTiles: the most heads for which both hold.  Short runs of the cache per position
+// cost more than the split plan's merge, so no fewer than an eighth of the heads, or a
+// twentieth where a warp's tiles are at most kShortUnitTiles.  Measured with ragged
+// lengths, these units and the split plan, us: 512 sequences of 8 heads up to 128
+// positions 28.0, 62.2; 256 of 8 up to 1024 56.8, 70.7; 128 of 32 up to 512 55.8, 59.2;
+// 256 of 8 up to 2048, one head per CTA, 98.2, 108.8; 16 of 40 up to 576, two heads,
+// 17.1, 18.4.  What the last rule excludes: 64 of 32 up to 1024, two heads, 54.2, 53.7; 16
+// of 40 up to 996, two heads, 25.0, 23.8.
 //
 // With fewer units, calls bound by latency: clusters of C CTAs, all resident at once.  Of
 // the head groups and cluster sizes that fit, the one with the fewest tiles for a warp at
@@ -250,11 +253,12 @@ int cluster_plan(int B, int D, long long tiles, const dattn::DeviceFacts &df, Pl
         p->smem = static_cast<int>(smem);
     };
     const long long ring = static_cast<long long>(p->warps) * p->slots * dattn::q8_tile_bytes(p->dp);
-    for (int hg = 8; hg >= 1 && hg * 8 >= p->vheads; hg /= 2) {
+    for (int hg = 8; hg >= 1 && hg * 20 >= p->vheads; hg /= 2) {
         if (hg > std::min(p->vheads, p->warps)) continue;
         const long long units = static_cast<long long>(B) * ((p->vheads + hg - 1) / hg);
-        const int ph = p->warps / hg;
-        if (10 * units < 7 * slots || (tiles + ph - 1) / ph > kUnitTiles || units > 0x7fffffffLL) continue;
+        const long long per_warp = (tiles + p->warps / hg - 1) / (p->warps / hg);
+        if (10 * units < 7 * slots || units > 0x7fffffffLL) continue;
+        if (per_warp > (hg * 8 >= p->vheads ? kUnitTiles : kShortUnitTiles)) continue;
         use(hg, 1, ring);
         return DATTN_OK;
     }
@@ -332,8 +336,10 @@ int make_plan(int B, int H, int Hk, int D, int S, int num_partitions, Plan *out)
     // 171 with 4, 169 with 2, 189 with 1), fewer make fewer partial states to write
     // and merge, (G + U) HG gq D floats of them (64 query on 8 key/value heads, 32768
     // positions: 29 us with 8, 21 with 4, 19 with 2, 18 with 1).  Taken: the most
-    // heads whose states, written and read, stay within 1 % of the cache's capacity;
-    // else one.
+    // heads whose states, written and read, stay within 2 % of the cache's capacity;
+    // else one.  With 1, 2, 4 and 8 %, us: 16 sequences of 40 heads up to 996 positions
+    // 26.5, 23.3, 23.3, 23.3; 14 of 16 up to 2880 26.2, 23.2, 22.4, 23.3; 32 of 8 up to
+    // 4096 32.6, 31.3, 32.0, 34.9; one of 8 with 131072 47.5, 49.1, 51.4, 51.5.
     const long long slots = static_cast<long long>(df.sms) * p.ctas_per_sm;
     const double cache_bytes = 2.0 * B * S * static_cast<double>(Hk) * D;
     double best = 0.0;
@@ -342,7 +348,7 @@ int make_plan(int B, int H, int Hk, int D, int S, int num_partitions, Plan *out)
         const double busy = static_cast<double>(p.vheads) / (static_cast<double>(nhg) * hg) *
                             (p.warps / hg * hg) / p.warps;
         const double states = (slots + static_cast<double>(B) * nhg) * hg * p.gq * D * 8.0;
-        if (busy > best + 1e-9 || (busy > best - 1e-9 && states <= 0.01 * cache_bytes)) {
+        if (busy > best + 1e-9 || (busy > best - 1e-9 && states <= 0.02 * cache_bytes)) {
             best = std::max(best, busy);
             p.HG = hg;
             p.NHG = nhg;
