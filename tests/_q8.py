@@ -66,9 +66,9 @@ def pair_size(x, rope_dims: int, trad: bool, magnitude: float = 1.0) -> np.ndarr
     return m
 
 
-# Error of a rotated element before its rounding, relative to |u| + |w|: the
-# angle is off by 2.4e-8 rad, sincospif by 2 ulp (1.2e-7), cos and sin times the
-# magnitude and the two products round by 2^-24 each (at most 2.4e-7 together).
+# Error of a rotated element before its rounding, relative to |u| + |w|: cos and
+# sin are off by at most 1.5e-7, cos and sin times the magnitude and the two products
+# round by 2^-24 each (at most 2.4e-7 together).
 ROTATION = 4e-7
 
 
