@@ -361,9 +361,9 @@ int dattn_softmax_f32(const float *x, float *out, long long rows, int cols,
  *              rows are dense, tokens lie x_stride / out_stride elements apart
  *              (whole multiples of 16 bytes): q or k may be a slice of a fused
  *              projection.  out may be x with the same stride; otherwise the
- *              two must not overlap.
+ *              two must not overlap (INVALID_ARG).
  *   positions  [tokens] uint32, device
- * head_dim: a multiple of 8, at most 256.
+ * head_dim: a multiple of 8, at most 256; at most 2^31 - 1024 tokens of 2^20 heads.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, CUDA.
  */
 enum dattn_dtype { DATTN_F16 = 1, DATTN_BF16 = 2, DATTN_F32 = 3 };
@@ -400,7 +400,8 @@ int dattn_rope(const void *x, void *out, int dtype, long long tokens, int n_head
  *           K_scale, V_scale  [num_pages, page_size / scale_block, n_kv_heads]    fp32
  *           block_table       [batch, max_pages] int32, as in dattn_decode_paged_f16;
  *           page_size is a multiple of scale_block
- * head_dim is a multiple of 16, at most 256.  Scales are finite and not
+ * head_dim is a multiple of 16, at most 256; a cache holds fewer than 2^31 positions
+ * in all.  Scales are finite and not
  * negative; 0 stands for a block of zeros.
  */
 enum dattn_kv_type { DATTN_KV_E4M3 = 1, DATTN_KV_INT8 = 2 };
@@ -417,7 +418,8 @@ enum dattn_kv_type { DATTN_KV_E4M3 = 1, DATTN_KV_INT8 = 2 };
  * serves the decode that follows.
  *   q_new  [tokens, n_heads, head_dim], k_new, v_new [tokens, n_kv_heads, head_dim]
  *          f16, tokens q_stride, k_stride, v_stride elements apart (as in dattn_rope)
- *   q_out  [tokens, n_heads, head_dim] f16, dense; may be q_new when that is dense
+ *   q_out  [tokens, n_heads, head_dim] f16, dense; may be q_new when that is dense,
+ *          otherwise the two must not overlap (INVALID_ARG)
  * q and k are rotated as by dattn_rope.  For each block that receives rows, per
  * key/value head and for K and V apart:
  *   need  = the smallest power of two s >= 2^-32 with |x| <= QMAX s for every

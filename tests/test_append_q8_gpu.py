@@ -374,3 +374,52 @@ def test_larger_batches(case, kv):
     s = Step(counts, last, H, Hk, D, S, block, kv, page, pad, rd, trad=trad)
     s.run()
     s.check()
+
+
+def test_far_pages_pass_32_bits():
+    # 2^32 + bytes of each cache: a block of the last page that has earlier rows
+    Hk, H, D, page, n = 8, 8, 128, 64, 16
+    pages = 2 ** 22 // page + 3
+    g = torch.Generator(device="cuda").manual_seed(2)
+    k = torch.zeros((pages, page, Hk, D), dtype=torch.int8, device="cuda")
+    v = torch.zeros_like(k)
+    ks = torch.ones((pages, page // n, Hk), device="cuda")
+    vs = torch.ones_like(ks)
+    near = [t[:2].clone() for t in (k, v, ks, vs)]   # the same step on pages at the front
+    mk = lambda h: torch.randn((20, h, D), generator=g, device="cuda").half()  # noqa: E731
+    x = [mk(H), mk(Hk), mk(Hk)]
+    off = torch.tensor([0, 20], dtype=torch.int32, device="cuda")
+    table = torch.tensor([[pages - 1, pages - 2]], dtype=torch.int32, device="cuda")
+    small = torch.tensor([[1, 0]], dtype=torch.int32, device="cuda")
+    for offsets, cp, take in ((off, 69, 20), (None, 70, 1)):
+        args = [t[:take] for t in x]
+        dattn.rope_append_q8(*args, k, v, ks, vs, cur_pos_tensor([cp]), n, token_offsets=offsets, block_table=table)
+        dattn.rope_append_q8(*args, *near, cur_pos_tensor([cp]), n, token_offsets=offsets, block_table=small)
+    for far, t in zip((k, v, ks, vs), near):
+        assert torch.equal(far[-2:], t)
+    assert torch.count_nonzero(k[:-2]) == 0 and torch.count_nonzero(v[:-2]) == 0
+
+
+def test_a_recorded_append_needs_its_output():
+    s = Step([1, 1], [0, 3], 4, 2, 64, 16, 8, "e4m3")
+    st = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    dattn.dattn_batch_begin(st)
+    try:
+        with pytest.raises(ValueError, match="q_out"):
+            s.run(q_out=None, stream=st)
+    finally:
+        s.run(stream=st)
+        dattn.dattn_batch_end(st).close()
+
+
+@pytest.mark.parametrize("counts,last", [
+    ([1] * 30 + [200] + [1] * 20 + [0, 3], [7 * i % 250 for i in range(30)] + [230] + [50 + i for i in range(20)] + [9, 2]),
+    ([0, 0, 0, 5], [1, 2, 3, 4]),
+    ([0, 64, 0], [0, 63, 0]),
+])
+@pytest.mark.parametrize("block", [1, 2, 16, 256])
+def test_steps_and_a_prompt_in_one_call(counts, last, block):
+    s = Step(counts, last, 8, 4, 64, 256, block, "e4m3", ragged=True)
+    s.run()
+    s.check()

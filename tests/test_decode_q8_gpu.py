@@ -365,3 +365,27 @@ def test_clusters_merge_in_shared_memory(B, H, Hk, D, S, short):
     got = c.run()
     c.check(got)
     assert torch.equal(got, c.run())
+
+
+@pytest.mark.parametrize("S,parts", [(700, 0), (700, 3), (5000, 0)])
+def test_out_may_be_the_queries(S, parts):
+    c = Case(2, 8, 2, 128, S, 16, "e4m3", [S - 1, 40])
+    want = c.run(num_partitions=parts)
+    got = c.run(num_partitions=parts, out=c.tq)
+    assert got.data_ptr() == c.tq.data_ptr() and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+def test_every_8_bit_value(kv):
+    # each code but e4m3's NaN, int8's -128 among them
+    codes = np.arange(256, dtype=np.uint8)
+    t = torch.from_numpy(codes)
+    val = (t.view(torch.float8_e4m3fn) if kv == "e4m3" else t.view(torch.int8)).float().numpy()
+    val = np.where(np.isnan(val), 1.0, val).astype(np.float64)
+
+    def edit(c):
+        for p in range(c.vq.shape[1]):
+            c.vq[0, p, 0] = np.roll(val, 5 * p)[: c.D]
+            c.kq[0, p, 0] = np.roll(val, 11 * p + 3)[: c.D]
+    c = Case(1, 4, 1, 256, 48, 16, kv, [47], edit=edit, qscale=0.01)
+    c.check(c.run())

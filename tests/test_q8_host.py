@@ -185,3 +185,33 @@ int main() {
     subprocess.run(["g++", "-O2", "-std=c++17", f"-I{build.CSRC}", f"-I{build.INCLUDE}", f"-I{cuda}",
                     str(src), "-o", str(exe)], check=True)
     subprocess.run([str(exe)], check=True)
+
+
+@pytest.mark.parametrize("x,xs,out,os,T,bad", [
+    (A, 128, A + 16, 128, 4, True),          # shifted by half a row
+    (A, 128, A + 256, 128, 4, True),         # by a token
+    (A + 256, 128, A, 128, 4, True),
+    (A, 256, A + 256, 256, 4, False),        # neighbouring slices of one buffer
+    (A + 256, 256, A, 256, 4, False),
+    (A, 256, A + 240, 256, 4, True),         # that touch
+    (A, 256, A + 272, 256, 4, True),         # the second reaches into the first's next token
+    (A, 136, A, 128, 4, True),               # the same start, other strides
+    (A, 136, A, 128, 1, False),              # of one token
+    (A, 128, A + 1024, 128, 4, False),       # one behind the other
+    (A, 128, A + 1008, 128, 4, True),
+    (A, 1 << 40, A + 16, 1 << 40, 1 << 30, True),
+])
+def test_rope_refuses_tensors_that_overlap(lib, x, xs, out, os, T, bad):
+    # rows of 2 x 64 f16; what is let through fails later, without a device
+    st = lib.dattn_rope(x, out, 1, T, 2, 64, xs, os, A, params(rd=8), 0, None)
+    assert (st == INVALID) == bad
+    if bad:
+        assert b"overlap" in lib.dattn_last_error() or b"too large" in lib.dattn_last_error()
+
+
+def test_append_refuses_q_out_inside_q_new(lib):
+    assert append(lib, q=A, qo=A + 16) == INVALID
+    assert append(lib, q=A, qo=A, qs=256) == INVALID      # a projection's slice, not dense
+    assert append(lib, q=A, qo=A + 256, qs=256) == INVALID
+    assert append(lib, q=A, qo=A) != INVALID
+    assert append(lib, q=A, qo=A + 4 * 256) != INVALID

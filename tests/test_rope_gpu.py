@@ -228,3 +228,60 @@ def test_many_tiles_in_place_of_a_slice(n, H, D, rd, trad, dtype):
     assert torch.equal(whole[:, :1], keep[:, :1]) and torch.equal(whole[:, H + 1:], keep[:, H + 1:])
     rows = np.unique(np.r_[0:70, n // 2: n // 2 + 70, n - 70: n])
     check(apart[rows], keep[:, 1: H + 1][rows], rows * 7, rd, 10000.0, trad, None, False)
+
+
+def test_offsets_pass_32_bits():
+    # 2^31 elements and more: the last tokens lie behind a 32-bit element count
+    n, H, D = 2 ** 21 + 37, 8, 128
+    x = torch.zeros((n, H, D), dtype=torch.float16, device="cuda")
+    tail = torch.randn((37, H, D), device="cuda").half()
+    x[-37:] = tail
+    p = torch.full((n,), 5, dtype=torch.int32, device="cuda")
+    p[-37:] = torch.arange(37, device="cuda", dtype=torch.int32) + 1000
+    y = dattn.rope(x, p, out=x)
+    assert torch.count_nonzero(y[:-37]) == 0
+    check(y[-37:], tail, np.arange(37) + 1000, 0, 1e4, False, None, False)
+
+
+def test_a_recorded_call_needs_its_output():
+    x = torch.zeros((2, 1, 64), dtype=torch.float16, device="cuda")
+    p = positions([0, 1])
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    dattn.dattn_batch_begin(s)
+    try:
+        with pytest.raises(ValueError, match="out"):
+            dattn.rope(x, p, stream=s)
+        dattn.rope(x, p, out=x, stream=s)
+    finally:
+        dattn.dattn_batch_end(s).close()
+
+
+def test_threads_launch_at_the_same_time():
+    # shapes that ask for different amounts of shared memory of the same kernels
+    import threading
+    cases, bad = [], []
+    for i, (n, H, D, rd) in enumerate([(3000, 8, 128, 0), (3000, 8, 80, 40), (5000, 4, 80, 40),
+                                       (2000, 16, 128, 128)]):
+        g = torch.Generator(device="cuda").manual_seed(i)
+        x = torch.randn((n, H, D), generator=g, device="cuda")
+        p = torch.arange(n, dtype=torch.int32, device="cuda")
+        cases.append((x, p, rd, dattn.rope(x, p, rd)))
+    torch.cuda.synchronize()
+
+    def work(x, p, rd, want):
+        s = torch.cuda.Stream()
+        for _ in range(50):
+            try:
+                got = dattn.rope(x, p, rd, stream=s)
+                s.synchronize()
+                if not torch.equal(got, want):
+                    bad.append("differs")
+            except Exception as e:  # noqa: BLE001
+                bad.append(repr(e))
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad[:3]

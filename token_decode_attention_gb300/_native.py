@@ -550,6 +550,12 @@ def _like(t, stream, shape=None, dtype=None):
     return torch.empty(shape, dtype=dtype, device=t.device)
 
 
+def _not_recorded(stream, name: str) -> None:
+    """A batch that is being recorded on `stream` cannot own a fresh output."""
+    if _RECORDING and _current_stream(_device(), stream) in _RECORDING:
+        raise ValueError(f"a recorded call needs an output that outlives the batch: pass {name}")
+
+
 def _index32(t, name: str, shape) -> None:
     if isinstance(t, torch.Tensor) and t.dtype not in _INDEX:
         raise TypeError(f"{name} must be int32 or uint32, got {t.dtype}")
@@ -623,6 +629,7 @@ def rope(x, positions, rope_dims: int = 0, rope_base: float = 10000.0, tradition
     """Rotate x [tokens, heads, head_dim] (f16, bf16 or f32) at ``positions``; with
     ``gradient`` the gradient of the rotated tensor into that of the tensor."""
     if out is None:
+        _not_recorded(stream, "out")
         out = _like(x, stream)
     _rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
     return out
@@ -757,6 +764,7 @@ def rope_append_q8(q_new, k_new, v_new, k_cache, v_cache, k_scale, v_scale, curr
     ``token_offsets`` [batch + 1].  ``current_pos`` holds the position of each
     sequence's last new token.  Returns the rotated q."""
     if q_out is None:
+        _not_recorded(stream, "q_out")
         q_out = _like(q_new, stream)
     dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, v_scale,
                          current_pos, scale_block, token_offsets, rope_dims, rope_base, traditional,

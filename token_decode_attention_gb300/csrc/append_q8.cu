@@ -107,7 +107,7 @@ cudaError_t launch_append_q8(const Q8AppendArgs &a, int kv, int sms, cudaStream_
     const size_t smem = rope_smem(qgr, rd, width, in.ring_bytes);
     if (smem > 32 * 1024) {  // with the static part past the default limit
         const cudaError_t e =
-            cudaFuncSetAttribute(in.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            cudaFuncSetAttribute(in.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

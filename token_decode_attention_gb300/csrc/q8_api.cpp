@@ -81,6 +81,23 @@ int check_stride(long long stride, long long row, int elem_bytes, const char *na
     return DATTN_OK;
 }
 
+// Two arrays of `tokens` rows of `row` bytes, xs and ys apart, that are either the same
+// rows or share no byte (slices of one projection lie in each other's gaps).
+int check_overlap(const void *x, const void *y, long long tokens, long long row, long long xs,
+                  long long ys, const char *names) {
+    if (tokens > (1LL << 60) / std::max(xs, ys))
+        return fail(DATTN_ERR_INVALID_ARG, "%s: the strides are too large", names);
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    if (a == b && (xs == ys || tokens == 1)) return DATTN_OK;
+    const uintptr_t ax = static_cast<uintptr_t>((tokens - 1) * xs + row);
+    const uintptr_t by = static_cast<uintptr_t>((tokens - 1) * ys + row);
+    if (a + ax <= b || b + by <= a) return DATTN_OK;
+    const uintptr_t step = static_cast<uintptr_t>(xs), width = static_cast<uintptr_t>(row);
+    const uintptr_t r = (a > b ? a - b : b - a) % step;
+    if (xs == ys && r >= width && step - r >= width) return DATTN_OK;
+    return fail(DATTN_ERR_INVALID_ARG, "%s overlap without being the same tensor", names);
+}
+
 // ------------------------------------------------------------------ rotation
 
 int check_rope(const dattn_rope_params *r, int head_dim) {
@@ -509,6 +526,9 @@ int append(const void *q_new, const void *k_new, const void *v_new, void *q_out,
     if (int st = check_stride(q_stride, static_cast<long long>(n_heads) * head_dim, 2, "q_stride")) return st;
     if (int st = check_stride(k_stride, static_cast<long long>(n_kv_heads) * head_dim, 2, "k_stride")) return st;
     if (int st = check_stride(v_stride, static_cast<long long>(n_kv_heads) * head_dim, 2, "v_stride")) return st;
+    const long long q_row = static_cast<long long>(n_heads) * head_dim;
+    if (int st = check_overlap(q_new, q_out, tokens, q_row * 2, q_stride * 2, q_row * 2, "q_new and q_out"))
+        return st;
     if (int st = check_rope(rope, head_dim)) return st;
     dattn::DeviceFacts df;
     if (int st = dattn::device_facts(&df)) return st;
@@ -572,8 +592,8 @@ int dattn_rope(const void *x, void *out, int dtype, long long tokens, int n_head
         const int elem = dtype == DATTN_F32 ? 4 : 2;
         if (int st = check_stride(x_stride, row, elem, "x_stride")) return st;
         if (int st = check_stride(out_stride, row, elem, "out_stride")) return st;
-        if (x == out && x_stride != out_stride)
-            return fail(DATTN_ERR_INVALID_ARG, "in place, x_stride and out_stride must be equal");
+        if (int st = check_overlap(x, out, tokens, row * elem, x_stride * elem, out_stride * elem, "x and out"))
+            return st;
         if (int st = check_rope(rope, head_dim)) return st;
         dattn::DeviceFacts df;
         if (int st = dattn::device_facts(&df)) return st;

@@ -79,7 +79,7 @@ cudaError_t launch_rope(const RopeArgs &a, int dtype, int sms, cudaStream_t stre
     const long long ctas = std::min(gr.tiles, sms * std::max(1LL, std::min<long long>(in.min_blocks, fit)));
     if (smem > 48 * 1024) {
         const cudaError_t e =
-            cudaFuncSetAttribute(in.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+            cudaFuncSetAttribute(in.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};

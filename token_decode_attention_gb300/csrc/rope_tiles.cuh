@@ -252,6 +252,11 @@ inline bool rope_grid(long long tokens, int H, int D, int rope_dims, int most, i
     return true;
 }
 
+// What a kernel that may need more than the default limit asks for: one value for all
+// its launches, so that threads that launch it at the same time agree.  With the static
+// part (16 KB at most) below the 227 KB of a CTA.
+constexpr int kMaxDynamicSmem = 208 * 1024;
+
 // Shared memory behind a ring of `ring_bytes`: two tables of at most (256 / items + 2)
 // tokens of 8 entries for 16 channels, 36 KB.
 inline size_t rope_smem(const RopeGrid &gr, int rope_dims, int width, int ring_bytes) {
