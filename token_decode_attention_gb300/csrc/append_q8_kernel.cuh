@@ -28,8 +28,12 @@
 // grid cannot know the ragged lengths, so it is cut by tokens: a set looks through a
 // window of the flattened tokens for those that open a block (the first of a sequence,
 // or a position at a multiple of scale_block) and takes their blocks.  K and V go to
-// different CTAs.  q is rotated by further CTAs of the same
-// launch (rope_tiles.cuh), which stream while the others compute.
+// different CTAs.  q is rotated by further CTAs of the same launch (rope_tiles.cuh),
+// which stream while the others compute.
+//
+// Measured (graph replay): 8192 tokens of 32 query and 8 key/value heads of 128, 185 MB,
+// 36.7 us, 5.0 TB/s (k and v alone 22, q alone 29.5); one token each of 256 sequences of
+// 40 heads, 13 MB, 5.9 us; one token of one sequence 2.6 us.
 #pragma once
 
 #include <cuda_fp16.h>

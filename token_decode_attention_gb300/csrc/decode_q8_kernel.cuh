@@ -34,13 +34,20 @@
 // Work split: tiles of 16 positions.  Split plan: as in the f16 decode
 // (streamk.h), the live tiles of all (sequence, head group) units, flattened, are
 // cut into equal ranges, one per CTA, and combine.cu merges the units that span
-// several.  Cluster plan, for batches small enough to be bound by latency: a
-// thread-block cluster takes a unit whole, its CTAs equal runs of its tiles, and
-// they merge through distributed shared memory in the same launch.  In a CTA each
+// several.  Cluster plan: a thread-block cluster takes a unit whole, its CTAs equal
+// runs of its tiles, and they merge through distributed shared memory in the same
+// launch; clusters of several CTAs for batches small enough to be bound by latency,
+// of one, in as many waves as it takes, for many short sequences.  In a CTA each
 // warp owns one head (heads_per_cta of them) and one phase: tiles go to the
 // phases in turn.  Every warp streams its own tiles through a private ring in
 // shared memory with 16-byte cp.async, so the main loop has no CTA-wide barrier;
 // rows past the live length are zero filled and never read from memory.
+//
+// Measured (graph replay, inputs larger than L2 in all): one sequence of 131072
+// positions and 32 heads of 128, 1 GiB, 158 us, 6.8 TB/s, as fast as a copy; 64 ragged
+// ones of up to 2048, 538 MB, 90.7 us, 5.9 TB/s, where the units' beginnings, ends and
+// merge show; one of 4096 positions, 8 key/value heads, 8.4 MB, 8.4 us, bound by latency
+// (launch, position, page, first tiles, exchange).
 #pragma once
 
 #include <cuda_fp16.h>

@@ -1,5 +1,5 @@
 // rope_tiles.cuh -- the rotation of many tokens, by equal runs of tiles per CTA: all of
-// rope.cu, and the queries of append_q8.cu.
+// rope.cu, and the queries of append_q8_kernel.cuh.
 //
 // What bounds it: each element is read once and written once, 3 flops each; the
 // cosines depend on (token, pair) only.  The items of all tokens, flattened, are cut
@@ -7,7 +7,9 @@
 // while it rotates and stores one, the next ones are on their way into a ring in
 // shared memory (each thread copies, waits for and reads its own items), and the
 // cos/sin table of the next one's tokens is built in the other half of a double
-// buffer, from positions fetched one tile earlier still.
+// buffer, from positions fetched one tile earlier still.  Measured (graph replay): 8192
+// tokens of 32 heads of 128 in bf16, 134 MB, 24.2 us, 5.5 TB/s; 4095 of 40 heads in f32,
+// half of each rotated, 168 MB, 29.9 us, 5.6 TB/s (a copy of 4 GB runs at 6.8).
 #pragma once
 
 #include <cuda_runtime.h>
