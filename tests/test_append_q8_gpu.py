@@ -423,3 +423,13 @@ def test_steps_and_a_prompt_in_one_call(counts, last, block):
     s = Step(counts, last, 8, 4, 64, 256, block, "e4m3", ragged=True)
     s.run()
     s.check()
+
+
+@pytest.mark.parametrize("D,rd", [(256, 20), (128, 20), (256, 40), (48, 12), (96, 6), (256, 250)])
+@pytest.mark.parametrize("counts", [[1, 1, 1], [5, 0, 40]])
+@pytest.mark.parametrize("trad", [False, True])
+def test_rotated_parts_that_16_does_not_divide(D, rd, counts, trad):
+    # items of eight, of four (a warp's lanes or too many of them), of single channels
+    s = Step(counts, [50, 7, 44], 6, 3, D, 64, 16, "e4m3", rd=rd, trad=trad)
+    s.run()
+    s.check()

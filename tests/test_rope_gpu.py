@@ -285,3 +285,74 @@ def test_threads_launch_at_the_same_time():
     for t in threads:
         t.join()
     assert not bad, bad[:3]
+
+
+@pytest.mark.parametrize("dtype", list(STEP), ids=["f16", "bf16", "f32"])
+@pytest.mark.parametrize("gradient", [False, True])
+def test_torch_finds_the_gradient(dtype, gradient):
+    g = torch.Generator(device="cuda").manual_seed(11)
+    x = torch.randn((9, 3, 64), generator=g, device="cuda").to(dtype).requires_grad_()
+    w = torch.randn((9, 3, 64), generator=g, device="cuda").to(dtype)
+    p = positions(np.arange(9) * 1000)
+    s = SCALINGS["by_parts"]
+    kw = dict(rope_dims=32, traditional=True, scaling=s)
+    y = dattn.rope(x, p, gradient=gradient, **kw)
+    with torch.no_grad():
+        assert torch.equal(y, dattn.rope(x, p, gradient=gradient, **kw))
+    (y * w).sum().backward()
+    # of y * w the gradient is w itself
+    assert torch.equal(x.grad, dattn.rope(w, p, gradient=not gradient, **kw))
+    x.grad = None
+    dattn.rope(x, p, gradient=gradient, **kw).sum().backward()      # ones of stride 0
+    assert torch.equal(x.grad, dattn.rope(torch.ones_like(w), p, gradient=not gradient, **kw))
+
+
+def test_second_derivatives_and_slices():
+    g = torch.Generator(device="cuda").manual_seed(12)
+    qkv = torch.randn((6, 5 * 32), generator=g, device="cuda", requires_grad=True)
+    p = positions(np.arange(6))
+    y = dattn.rope(qkv[:, 32: 96].view(6, 2, 32), p)
+    d, = torch.autograd.grad((y ** 3).sum(), qkv, create_graph=True)
+    assert torch.count_nonzero(d[:, :32]) == 0 and torch.count_nonzero(d[:, 96:]) == 0
+    v = torch.randn((6, 2, 32), generator=g, device="cuda")
+    hv, = torch.autograd.grad((d[:, 32: 96].view(6, 2, 32) * v).sum(), qkv)
+    # R^T (6 y . (R v))
+    want = dattn.rope(6 * y.detach() * dattn.rope(v, p), p, gradient=True)
+    # products and rotations in fp32: a few roundings of terms of |6 y R v|
+    size = float((6 * y.detach() * dattn.rope(v, p)).abs().max())
+    assert float((hv[:, 32: 96].view(6, 2, 32) - want).abs().max()) <= 16 * 2.0 ** -24 * 2 * size
+
+
+def test_out_and_stream_are_refused_for_a_gradient():
+    x = torch.zeros((2, 1, 64), device="cuda", requires_grad=True)
+    p = positions([0, 1])
+    with pytest.raises(ValueError, match="gradient"):
+        dattn.rope(x, p, out=torch.empty_like(x))
+    with pytest.raises(ValueError, match="gradient"):
+        dattn.rope(x, p, stream=torch.cuda.Stream())
+    with pytest.raises(TypeError, match="float16"):
+        dattn.rope(x.double(), p)
+    with torch.no_grad():
+        assert not dattn.rope(x, p, out=torch.empty_like(x)).requires_grad
+
+
+def test_a_captured_step_takes_its_gradient_by_hand():
+    x = torch.randn((5, 2, 64), device="cuda").requires_grad_()
+    w = torch.randn((5, 2, 64), device="cuda")
+    p = positions(range(5))
+    y = dattn.rope(x, p)   # an eager graph of the same leaf is alive
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        with pytest.raises(ValueError, match="captured"):
+            dattn.rope(x, p)
+        with torch.no_grad():
+            out = dattn.rope(x, p)
+            grad = dattn.rope(w, p, gradient=True)
+    out.zero_()
+    grad.zero_()
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, y)
+    y.backward(w)
+    assert torch.equal(grad, x.grad)

@@ -624,10 +624,43 @@ def dattn_rope(x, out, positions, rope_dims: int = 0, rope_base: float = 10000.0
     _rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
 
 
+class _RopeOfGraph(torch.autograd.Function):
+    """The rotation as a node of torch's graph.  The map is linear: its derivative is the
+    call with the other ``gradient``, which is a node again where torch asks for one."""
+
+    @staticmethod
+    def forward(ctx, x, positions, options):
+        ctx.save_for_backward(positions)
+        ctx.options = options
+        out = _like(x, None)
+        _rope(x, out, positions, *options, None)
+        return out
+
+    @staticmethod
+    def backward(ctx, g):
+        positions, = ctx.saved_tensors
+        *options, gradient = ctx.options
+        if not g.is_contiguous() or g.data_ptr() % 16:  # a broadcast sum's, or a slice
+            g = g.clone(memory_format=torch.contiguous_format)
+        return rope(g, positions, *options, gradient=not gradient), None, None
+
+
 def rope(x, positions, rope_dims: int = 0, rope_base: float = 10000.0, traditional: bool = False,
          scaling=None, gradient: bool = False, out=None, stream=None):
     """Rotate x [tokens, heads, head_dim] (f16, bf16 or f32) at ``positions``; with
-    ``gradient`` the gradient of the rotated tensor into that of the tensor."""
+    ``gradient`` the gradient of the rotated tensor into that of the tensor.  Where x
+    requires a gradient, torch finds it through this call (without ``out`` and
+    ``stream``, and not while a graph is captured)."""
+    if isinstance(x, torch.Tensor) and x.requires_grad and torch.is_grad_enabled():
+        if out is not None or stream is not None:
+            raise ValueError("x requires a gradient: out and stream cannot be given")
+        _not_recorded(stream, "out")
+        if x.is_cuda and torch.cuda.is_current_stream_capturing():
+            # torch's backward of a captured call can end the process where an eager graph of
+            # the same leaves is alive on another stream
+            raise ValueError("x requires a gradient, which a captured call does not follow: capture "
+                             "the call without it and the one with gradient=True")
+        return _RopeOfGraph.apply(x, positions, (rope_dims, rope_base, traditional, scaling, gradient))
     if out is None:
         _not_recorded(stream, "out")
         out = _like(x, stream)
