@@ -389,3 +389,32 @@ def test_every_8_bit_value(kv):
             c.kq[0, p, 0] = np.roll(val, 11 * p + 3)[: c.D]
     c = Case(1, 4, 1, 256, 48, 16, kv, [47], edit=edit, qscale=0.01)
     c.check(c.run())
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("parts", [0, 1, 3])
+def test_zero_scales_over_a_long_stretch(parts, D, kv):
+    # 131072 positions whose V scale is 0, all but the first tile with weights almost as large as
+    # they get before the running maximum moves, then 16 positions that count.  One warp has a
+    # head's positions where a single CTA does the work.
+    S, H = 131072 + 16, 8
+    k = torch.zeros((1, S, H, D), dtype=torch.int8, device="cuda")
+    k[..., 0] = 1
+    v = torch.randint(-100, 100, k.shape, device="cuda").to(torch.int8)
+    v[:, -16:] = 96
+    # the scores, in powers of two, by K's scales
+    s = torch.full((S // 16,), 4.9, dtype=torch.float64)
+    s[0], s[-1] = 0.0, 34.9
+    ks = (s * math.log(2.0) * math.sqrt(D)).float().cuda()[None, :, None].expand(1, S // 16, H).contiguous()
+    vs = torch.zeros_like(ks)
+    vs[:, -1] = 1.0
+    q = torch.zeros((1, H, D), dtype=torch.float16, device="cuda")
+    q[..., 0] = 1.0
+    if kv == "e4m3":
+        k, v = k.float().to(torch.float8_e4m3fn), v.float().to(torch.float8_e4m3fn)
+    plan = dattn.dattn_decode_q8_plan(1, H, H, D, S, 1)
+    assert plan["heads_per_cta"] == 8 and plan["threads_per_cta"] == 256
+    got = dattn.decode_q8(q, k, v, ks, vs, cur_pos_tensor([S - 1]), 16, num_partitions=parts)
+    # 131072 2^4.9 against 16 2^34.9: the zeros weigh 2^-17, 8e-4 of 96, whose step is 2^-4
+    assert torch.equal(got, torch.full_like(got, 96.0))

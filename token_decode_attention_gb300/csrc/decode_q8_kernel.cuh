@@ -72,8 +72,10 @@ constexpr int kMaxCluster = 16;  // CTAs per cluster (8 is the portable limit)
 // precision down to 2^-24 of the largest.
 constexpr float kHeadroom = 10.f, kTrigger = 15.f;
 // log2 of the smallest scale of V that takes part (a scale of 0 stands for
-// values of zero; it is read as 2^-100, which leaves them below any f16).
-constexpr float kMinLogScale = -100.f;
+// values of zero; it is read as 2^-60, which leaves them below any f16).  The sum over
+// such positions holds weights of up to 2^15 times 2^60: below 2^107 for as many as there
+// can be.
+constexpr float kMinLogScale = -60.f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
