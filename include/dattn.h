@@ -466,10 +466,9 @@ int dattn_decode_q8_workspace_bytes(int batch, int n_heads, int n_kv_heads, int 
  * dattn_decode_f16_ex (dattn_decode_paged_f16) on the values the cache stands
  * for, with grouped heads.  Products of f16 and 8-bit values accumulate in fp32;
  * the running maximum and sum are fp32; each position's softmax weight times V's
- * scale is rounded to f16 before it meets V's 8-bit values (relative 2^-11; 2^-35
- * of the largest such product where it is below 2^-24 of that); out is rounded to
- * f16.  Positions past
- * the live length never enter the computation, their rows and scales are not
+ * scale meets V's 8-bit values as the sum of two f16 (relative 2^-22; 2^-35 of the
+ * largest such product where it is below 2^-13 of that); out is rounded to f16.
+ * Positions past the live length never enter the computation, their rows and scales are not
  * read.  A live block-table entry outside [0, num_pages) is not dereferenced:
  * page 0 is read instead and dattn_device_error() reports DATTN_ERR_BAD_PAGE.
  *   Q, out [batch, n_heads, head_dim] f16; workspace and num_partitions as in

@@ -418,3 +418,45 @@ def test_zero_scales_over_a_long_stretch(parts, D, kv):
     got = dattn.decode_q8(q, k, v, ks, vs, cur_pos_tensor([S - 1]), 16, num_partitions=parts)
     # 131072 2^4.9 against 16 2^34.9: the zeros weigh 2^-17, 8e-4 of 96, whose step is 2^-4
     assert torch.equal(got, torch.full_like(got, 96.0))
+
+
+# Weights rounded to f16 would be off by up to 2^-11.  What is left of decode_bound's weight
+# without that rounding: a weight held as the sum of two f16 is off by 2^-21 of itself or, times V's
+# scale, by 2^-35 of the largest of them, whose 8-bit values are at most 448.
+def exact_weight_bound(ref, size, dot, top, L, D, vs):
+    bound = _q8.decode_bound(ref, size, dot, top, L, D, vs) + (2.0 ** -21 - 2.0 ** -11) * size
+    return bound + L * 2.0 ** -35 * 448 * vs.max()
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "int8"])
+@pytest.mark.parametrize("D", [16, 64, 80, 128, 256])
+@pytest.mark.parametrize("H,Hk", [(1, 1), (6, 2), (4, 1), (5, 1), (16, 2), (12, 1), (16, 1), (34, 2)])
+def test_weights_keep_more_bits_than_f16(H, Hk, D, kv):
+    # In every tile one position of weight 1 and value -60, and fifteen of weight
+    # 2^-4 (1 + 0.45 2^-10) and value 64: all but 0.45 2^-10 of it cancels, and that is
+    # what a rounding to 11 bits would drop.
+    S = 144
+
+    def edit(c):
+        at = np.arange(S) % 16 == 0
+        c.q[:] = 0.0
+        c.q[:, :, 0] = -1.0
+        c.kq[:] = 0.0
+        c.kq[:, ~at, :, 0] = 1.0
+        c.ks[:] = (4.0 - math.log2(1 + 0.45 * 2.0 ** -10)) * math.log(2.0) * math.sqrt(D)
+        c.vs[:] = 1.0
+        c.vq[:] = np.where(at, -60.0, 64.0)[None, :, None, None]
+    c = Case(2, H, Hk, D, S, 1, kv, [S - 1, 15], edit=edit)
+    ref, size, dot, top = _q8.decode(c.q, c.kq, c.vq, c.ks, c.vs, c.cp, 1)
+    bound = exact_weight_bound(ref, size, dot, top, S, D, c.vs)
+    assert (bound < 0.6 * np.abs(ref)).all()     # 0.0136: a result of 0 is outside
+    for parts in (0, 1, 9):
+        _q8.check(_q8.f64(c.run(num_partitions=parts)), ref, bound, f"{parts} partitions")
+
+
+@pytest.mark.parametrize("B,H,Hk,D,S,block,page,cp", SHAPES,
+                         ids=[f"B{s[0]}H{s[1]}k{s[2]}D{s[3]}S{s[4]}n{s[5]}p{s[6]}" for s in SHAPES])
+def test_the_bound_without_a_rounding_of_the_weights(B, H, Hk, D, S, block, page, cp):
+    c = Case(B, H, Hk, D, S // page * page if page else S, block, "e4m3", cp, page, seed=3)
+    ref, size, dot, top = _q8.decode(c.q, c.kq, c.vq, c.ks, c.vs, c.cp, block, c.table, page)
+    _q8.check(_q8.f64(c.run()), ref, exact_weight_bound(ref, size, dot, top, max(cp) + 1, D, c.vs), "")

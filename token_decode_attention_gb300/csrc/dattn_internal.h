@@ -207,6 +207,9 @@ __host__ __device__ constexpr int q8_slots(int dp, int nt) {
     return 212 * 1024 / (q8_warps(dp, nt) * q8_ctas_per_sm(dp, nt)) / q8_tile_bytes(dp);
 }
 
+// Whether the eight columns hold each of gq query heads twice.
+__host__ __device__ constexpr bool q8_pair(int gq) { return gq <= 4; }
+
 // Arguments of the decode kernel over an 8-bit cache (decode_q8.cu).  A virtual
 // head is a group of gq query heads of one key/value head (a key/value head has
 // vheads_per_kv of them); units are (sequence, group of heads_per_cta virtual
@@ -240,7 +243,7 @@ struct Q8DecodeArgs {
 };
 cudaError_t decode_q8_configure(int max_smem);
 // Clusters of `cluster` CTAs that can be resident at once.
-cudaError_t decode_q8_max_clusters(int dp, int nt, int smem, int cluster, int *clusters);
+cudaError_t decode_q8_max_clusters(int dp, int nt, bool pair, int smem, int cluster, int *clusters);
 cudaError_t launch_decode_q8(const Q8DecodeArgs &a, int dp, int nt, int kv, int smem,
                              cudaStream_t stream);
 

@@ -5,15 +5,15 @@
 
 namespace dattn {
 
-bool decode_q8_int8_fn(int dp, int nt, const void **split, const void **cluster);
+bool decode_q8_int8_fn(int dp, int nt, bool pair, const void **split, const void **cluster);
 
 namespace {
 
-const void *kernel_of(int dp, int nt, int kv, bool cluster) {
+const void *kernel_of(int dp, int nt, bool pair, int kv, bool cluster) {
     const void *s = nullptr, *c = nullptr;
     if (kv == kKvInt8) {
-        if (!decode_q8_int8_fn(dp, nt, &s, &c)) return nullptr;
-    } else if (const Q8Instance *i = q8_instance<kKvE4m3>(dp, nt)) {
+        if (!decode_q8_int8_fn(dp, nt, pair, &s, &c)) return nullptr;
+    } else if (const Q8Instance *i = q8_instance<kKvE4m3>(dp, nt, pair)) {
         s = i->split;
         c = i->cluster;
     }
@@ -24,10 +24,10 @@ const void *kernel_of(int dp, int nt, int kv, bool cluster) {
 
 cudaError_t decode_q8_configure(int max_smem) {
     for (int dp = 64; dp <= 256; dp *= 2)
-        for (int nt = 1; nt <= 2; ++nt)
+        for (int columns : {4, 8, 16})
             for (int kv : {kKvE4m3, kKvInt8})
                 for (bool cluster : {false, true}) {
-                    const void *fn = kernel_of(dp, nt, kv, cluster);
+                    const void *fn = kernel_of(dp, columns > 8 ? 2 : 1, columns == 4, kv, cluster);
                     cudaFuncAttributes attr{};
                     cudaError_t e = cudaFuncGetAttributes(&attr, fn);
                     if (e != cudaSuccess) return e;
@@ -40,8 +40,8 @@ cudaError_t decode_q8_configure(int max_smem) {
     return cudaSuccess;
 }
 
-cudaError_t decode_q8_max_clusters(int dp, int nt, int smem, int cluster, int *clusters) {
-    const Q8Instance *i = q8_instance<kKvE4m3>(dp, nt);
+cudaError_t decode_q8_max_clusters(int dp, int nt, bool pair, int smem, int cluster, int *clusters) {
+    const Q8Instance *i = q8_instance<kKvE4m3>(dp, nt, pair);
     if (i == nullptr) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(cluster));
@@ -59,8 +59,9 @@ cudaError_t decode_q8_max_clusters(int dp, int nt, int smem, int cluster, int *c
 
 cudaError_t launch_decode_q8(const Q8DecodeArgs &a, int dp, int nt, int kv, int smem,
                              cudaStream_t stream) {
-    const Q8Instance *i = q8_instance<kKvE4m3>(dp, nt);
-    const void *fn = kernel_of(dp, nt, kv, a.cluster > 0);
+    const bool pair = q8_pair(a.gq);
+    const Q8Instance *i = q8_instance<kKvE4m3>(dp, nt, pair);
+    const void *fn = kernel_of(dp, nt, pair, kv, a.cluster > 0);
     if (i == nullptr || fn == nullptr || a.partitions <= 0 || a.cluster > kMaxCluster)
         return cudaErrorInvalidValue;
     void *args[] = {const_cast<Q8DecodeArgs *>(&a)};

@@ -4,8 +4,8 @@
 
 namespace dattn {
 
-bool decode_q8_int8_fn(int dp, int nt, const void **split, const void **cluster) {
-    const Q8Instance *i = q8_instance<kKvInt8>(dp, nt);
+bool decode_q8_int8_fn(int dp, int nt, bool pair, const void **split, const void **cluster) {
+    const Q8Instance *i = q8_instance<kKvInt8>(dp, nt, pair);
     if (i == nullptr) return false;
     *split = i->split;
     *cluster = i->cluster;

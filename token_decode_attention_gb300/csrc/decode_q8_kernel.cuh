@@ -22,14 +22,21 @@
 // memory; a decode has at most 16 query heads to share a fetched key, so
 // the widened cache would have to be written back to shared memory first, which
 // costs more than the products.  8-bit values are exact in f16, Q is f16 already
-// and the products accumulate in fp32; P is rounded to f16 (a relative 2^-11).
+// and the products accumulate in fp32.  P is fp32 and enters as the sum of two f16,
+// the nearest one and what that leaves: a relative 2^-22, where one alone is 2^-11 and
+// left the outputs of 64 ragged sequences 2.4e-4 (rms, relative) from the definition; now
+// 2.1e-4, what their own rounding to f16 makes.  With at most four query heads the second
+// takes the columns that they leave free, at no further product; with more it takes a
+// product of its own per 16 channels.  One and two f16, us: 64 ragged sequences of 32 heads
+// 90.5, 90.8; 32 on 8 heads, 4096 positions 8.4, 8.7; 64 on 8 heads, 32768 positions 18.2,
+// 18.3; 32 on 2 heads (16 columns), 65536 positions 14.6, 15.6.
 //
 // Fragments straight from 16-byte loads: the sum over channels (and over
 // positions) may run in any order, so the channel (position) that a fragment
 // slot stands for is chosen to make each lane's elements contiguous in the
 // cache row, for K one 16-byte chunk per four k-steps, for V two neighbouring
 // positions' words whose bytes are paired with prmt.  P^T is the S^T
-// accumulator rounded to f16 and transposed with movmatrix.
+// accumulator in its two f16, transposed with movmatrix.
 //
 // Work split: tiles of 16 positions.  Split plan: as in the f16 decode
 // (streamk.h), the live tiles of all (sequence, head group) units, flattened, are
@@ -45,8 +52,8 @@
 //
 // Measured (graph replay, inputs larger than L2 in all): one sequence of 131072
 // positions and 32 heads of 128, 1 GiB, 158 us, 6.8 TB/s, as fast as a copy; 64 ragged
-// ones of up to 2048, 538 MB, 90.7 us, 5.9 TB/s, where the units' beginnings, ends and
-// merge show; one of 4096 positions, 8 key/value heads, 8.4 MB, 8.4 us, bound by latency
+// ones of up to 2048, 538 MB, 90.8 us, 5.9 TB/s, where the units' beginnings, ends and
+// merge show; one of 4096 positions, 8 key/value heads, 8.4 MB, 8.7 us, bound by latency
 // (launch, position, page, first tiles, exchange).
 #pragma once
 
@@ -68,8 +75,8 @@ constexpr int kMaxCluster = 16;  // CTAs per cluster (8 is the portable limit)
 
 // The running maximum M is kept kHeadroom (log2) below the largest exponent at
 // the time it was set, and moved only when an exponent exceeds M + kTrigger:
-// weights then lie below 2^15 (f16 holds up to 65504) and keep f16's full
-// precision down to 2^-24 of the largest.
+// weights then lie below 2^15 (f16 holds up to 65504), and their two f16 keep 22 bits
+// down to 2^-13 of the largest, further down 2^-35 of it.
 constexpr float kHeadroom = 10.f, kTrigger = 15.f;
 // log2 of the smallest scale of V that takes part (a scale of 0 stands for
 // values of zero; it is read as 2^-60, which leaves them below any f16).  The sum over
@@ -157,6 +164,11 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
+// What pack2's rounding left of the two.
+__device__ __forceinline__ uint32_t rest2(float lo, float hi, uint32_t packed) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&packed));
+    return pack2(lo - f.x, hi - f.y);
+}
 
 // Shared-memory row of MMA row r (0..7) within a group of 8 tile rows, chosen
 // so that both fragment patterns below are free of bank conflicts under the
@@ -180,7 +192,8 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 
 // DP: head_dim rounded up to 64, 128 or 256 (channels above head_dim are zero
 // filled).  NT: 8-column tiles of query heads.  NW: warps.  NS: ring slots.
-template <int DP, int NT, int KV, int NW, int NS, bool CLUSTER>
+// PAIR (NT = 1): at most four query heads, each in columns h and h + 4.
+template <int DP, int NT, bool PAIR, int KV, int NW, int NS, bool CLUSTER>
 __global__ void __launch_bounds__(NW * 32, q8_ctas_per_sm(DP, NT)) decode_q8_kernel(const Q8DecodeArgs a) {
     constexpr int NJ = DP / 64;           // 64-channel spans of a row
     constexpr int NM = DP / 16;           // 16-channel tiles of the output
@@ -420,12 +433,13 @@ __global__ void __launch_bounds__(NW * 32, q8_ctas_per_sm(DP, NT)) decode_q8_ker
                        : 0;
         };
 
-        // Q^T fragments: column n = query head, channels as in K's chunks.
+        // Q^T fragments: column n = query head (modulo 4 where two columns share one),
+        // channels as in K's chunks.
         uint32_t qf[NT][NJ][4][2];
         if (ntiles > 0) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                const int h = n * 8 + g;
+                const int h = PAIR ? g & 3 : n * 8 + g;
                 const __half *qrow = reinterpret_cast<const __half *>(a.Q) +
                                      (b * a.H + static_cast<long long>(vh) * a.gq + h) * D;
 #pragma unroll
@@ -569,7 +583,9 @@ __global__ void __launch_bounds__(NW * 32, q8_ctas_per_sm(DP, NT)) decode_q8_ker
                         }
                     }
             }
+            // the weights as f16 and, columns 4 to 7 of a pair or pr, what that leaves
             uint32_t pf[NT][2];
+            [[maybe_unused]] uint32_t pr[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const float m0 = M[n][0] == -INFINITY ? 0.f : M[n][0];
@@ -578,8 +594,17 @@ __global__ void __launch_bounds__(NW * 32, q8_ctas_per_sm(DP, NT)) decode_q8_ker
                 const float e2 = ex2(s[n][0][2] - m0), e3 = ex2(s[n][0][3] - m1);
                 l[n][0] = fmaf(e0, iv0, fmaf(e2, iv1, l[n][0]));
                 l[n][1] = fmaf(e1, iv0, fmaf(e3, iv1, l[n][1]));
-                pf[n][0] = transpose8x8(pack2(e0, e1));
-                pf[n][1] = transpose8x8(pack2(e2, e3));
+                const uint32_t h0 = pack2(e0, e1), h1 = pack2(e2, e3);
+                const uint32_t left0 = rest2(e0, e1, h0), left1 = rest2(e2, e3, h1);
+                if constexpr (PAIR) {
+                    pf[n][0] = transpose8x8(t & 2 ? left0 : h0);
+                    pf[n][1] = transpose8x8(t & 2 ? left1 : h1);
+                } else {
+                    pf[n][0] = transpose8x8(h0);
+                    pf[n][1] = transpose8x8(h1);
+                    pr[n][0] = transpose8x8(left0);
+                    pr[n][1] = transpose8x8(left1);
+                }
             }
 
             // out^T += V^T P^T: positions v0, v1 and 8 rows on; channels by lane group
@@ -618,11 +643,21 @@ __global__ void __launch_bounds__(NW * 32, q8_ctas_per_sm(DP, NT)) decode_q8_ker
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         mma16816(acc[n][m], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                    if constexpr (!PAIR) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma16816(acc[n][m], a0, a1, a2, a3, pr[n][0], pr[n][1]);
+                    }
                     widen<KV>(x2, a0, a1);
                     widen<KV>(z2, a2, a3);
 #pragma unroll
                     for (int n = 0; n < NT; ++n)
                         mma16816(acc[n][m + 1], a0, a1, a2, a3, pf[n][0], pf[n][1]);
+                    if constexpr (!PAIR) {
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+                            mma16816(acc[n][m + 1], a0, a1, a2, a3, pr[n][0], pr[n][1]);
+                    }
                 }
             }
         }
@@ -645,7 +680,25 @@ __global__ void __launch_bounds__(NW * 32, q8_ctas_per_sm(DP, NT)) decode_q8_ker
         constexpr int kRow = DP + 4;
         float *const my_rows = reinterpret_cast<float *>(smem + warp * (NS * kTileBytes));
         __syncwarp();  // the last tile has been read
-        if (active) {
+        if constexpr (PAIR) {
+            // The two columns of a query head together: lanes t and t ^ 2 hold the same two
+            // heads and finish one each.
+            const bool second = t & 2;
+            const int h = 2 * (t & 1) + (second ? 1 : 0);
+            float *const row = my_rows + h * kRow + 2 * g;
+            const bool mine = active && h < a.gq;
+            if (mine && g == 0)
+                s_ml[warp][h] = second ? make_float2(M[0][1], l[0][1]) : make_float2(M[0][0], l[0][0]);
+#pragma unroll
+            for (int m = 0; m < NM; ++m) {
+                const float *c = acc[0][m];
+                const float y0 = __shfl_xor_sync(kFull, second ? c[0] : c[1], 2);
+                const float y1 = __shfl_xor_sync(kFull, second ? c[2] : c[3], 2);
+                if (mine)
+                    *reinterpret_cast<float2 *>(row + 16 * m) =
+                        make_float2((second ? c[1] : c[0]) + y0, (second ? c[3] : c[2]) + y1);
+            }
+        } else if (active) {
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -741,7 +794,9 @@ __global__ void __launch_bounds__(NW * 32, q8_ctas_per_sm(DP, NT)) decode_q8_ker
 }
 
 struct Q8Instance {
-    int dp, nt, nw, ns;
+    int dp, nt;
+    bool pair;
+    int nw, ns;
     const void *split, *cluster;
 };
 
@@ -749,18 +804,20 @@ struct Q8Instance {
 // and query fragments leave room for 128 registers, 8 otherwise; ring slots that
 // fill ~200 KB of an SM's shared memory.
 template <int KV>
-const Q8Instance *q8_instance(int dp, int nt) {
-#define DATTN_Q8(DP, NT)                                                                            \
-    {DP, NT, q8_warps(DP, NT), q8_slots(DP, NT),                                                    \
+const Q8Instance *q8_instance(int dp, int nt, bool pair) {
+#define DATTN_Q8(DP, NT, PAIR)                                                                      \
+    {DP, NT, PAIR, q8_warps(DP, NT), q8_slots(DP, NT),                                              \
      reinterpret_cast<const void *>(                                                                \
-         decode_q8_kernel<DP, NT, KV, q8_warps(DP, NT), q8_slots(DP, NT), false>),                  \
+         decode_q8_kernel<DP, NT, PAIR, KV, q8_warps(DP, NT), q8_slots(DP, NT), false>),            \
      reinterpret_cast<const void *>(                                                                \
-         decode_q8_kernel<DP, NT, KV, q8_warps(DP, NT), q8_slots(DP, NT), true>)}
-    static const Q8Instance table[] = {DATTN_Q8(64, 1),  DATTN_Q8(64, 2),  DATTN_Q8(128, 1),
-                                       DATTN_Q8(128, 2), DATTN_Q8(256, 1), DATTN_Q8(256, 2)};
+         decode_q8_kernel<DP, NT, PAIR, KV, q8_warps(DP, NT), q8_slots(DP, NT), true>)}
+    static const Q8Instance table[] = {
+        DATTN_Q8(64, 1, true),  DATTN_Q8(64, 1, false),  DATTN_Q8(64, 2, false),
+        DATTN_Q8(128, 1, true), DATTN_Q8(128, 1, false), DATTN_Q8(128, 2, false),
+        DATTN_Q8(256, 1, true), DATTN_Q8(256, 1, false), DATTN_Q8(256, 2, false)};
 #undef DATTN_Q8
     for (const Q8Instance &i : table)
-        if (i.dp == dp && i.nt == nt) return &i;
+        if (i.dp == dp && i.nt == nt && i.pair == pair) return &i;
     return nullptr;
 }
 

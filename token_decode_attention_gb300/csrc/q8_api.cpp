@@ -23,7 +23,8 @@ constexpr int kMaxHeadDim = 256;
 constexpr int kMaxPartitions = 65535;
 constexpr int kMaxColumns = 16;  // query heads of a key/value head in one CTA
 constexpr int kStaticSmem = 4096;  // the decode kernel's static shared memory at most
-// Tiles of a warp up to which the cluster plan is taken.  Measured (cluster, split):
+// Tiles of a warp up to which the cluster plan is taken.  Measured here and below with one
+// f16 per weight (the second adds 0 to 7 %, under either plan): (cluster, split)
 // one 7B-class step of 8 key/value heads, 2 tiles, 8.4 and 8.7 us; of 32, 4 tiles, 9.9
 // and 12.1; 32 ragged sequences of 8 heads, 8 tiles, 13.6 and 16.0; 37 of 4 heads, 8
 // tiles, 14.7 and 16.2; 64 query on 8 key/value heads over 32768 positions, 16 tiles
@@ -291,8 +292,8 @@ int cluster_plan(int B, int D, long long tiles, const dattn::DeviceFacts &df, Pl
             const long long rec = C > 1 ? (hg * p->gq * (p->dp / 2) + C - 1) / C * C * 16LL : 0;
             if (ring + rec > df.max_smem_optin - kStaticSmem) continue;
             int fit = 0;
-            if (dattn::decode_q8_max_clusters(p->dp, p->nt, static_cast<int>(ring + rec), C, &fit) !=
-                cudaSuccess) {
+            if (dattn::decode_q8_max_clusters(p->dp, p->nt, dattn::q8_pair(p->gq),
+                                              static_cast<int>(ring + rec), C, &fit) != cudaSuccess) {
                 cudaGetLastError();  // this cluster size is not available
                 continue;
             }
