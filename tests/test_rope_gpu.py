@@ -1,6 +1,10 @@
 """Rotary positions of many tokens against a plain form in 64 bits."""
 from __future__ import annotations
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -356,3 +360,22 @@ def test_a_captured_step_takes_its_gradient_by_hand():
     assert torch.equal(out, y)
     y.backward(w)
     assert torch.equal(grad, x.grad)
+
+
+def test_one_head_with_a_part_rotated_launches_in_a_fresh_process():
+    # rings and tables of 46 to 48 KB in all, each launched before anything larger could have
+    # raised its kernel's limit on shared memory
+    code = """
+import torch, token_decode_attention_gb300 as dattn
+p = torch.arange(4096, dtype=torch.int32, device="cuda")
+for dtype in (torch.float16, torch.bfloat16):
+    for d, rd in ((64, 48), (112, 80), (128, 96), (144, 96), (160, 112), (192, 128), (208, 144),
+                  (224, 144), (240, 160), (256, 192)):
+        x = torch.ones((4096, 1, d), dtype=dtype, device="cuda")
+        y = dattn.rope(x, p, rd)
+        assert torch.equal(y[0], x[0]) and torch.equal(y[:, :, rd:], x[:, :, rd:]), (d, rd)
+print("launched")
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
+                       cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+    assert r.returncode == 0 and "launched" in r.stdout, r.stderr[-2000:]

@@ -21,11 +21,13 @@
 namespace dattn {
 namespace {
 
+constexpr size_t kPosBytes = 2 * kRopeThreads * sizeof(uint32_t);
+
 template <typename T, int N, bool FIXED, int HP>
 __global__ void __launch_bounds__(kRopeThreads, (kRopeBlocks<T, N, HP>))
     rope_kernel(const __grid_constant__ RopeArgs a, const RopeGrid gr) {
     extern __shared__ __align__(16) unsigned char smem[];
-    __shared__ uint32_t s_pos[2][kRopeThreads];
+    __shared__ uint32_t s_pos[2][kRopeThreads];  // kPosBytes
     pdl_launch_dependents();
     pdl_wait_primary();
     rope_tiles<T, N, FIXED, HP>(a, a.rope, gr, blockIdx.x, gridDim.x, smem, s_pos);
@@ -77,7 +79,7 @@ cudaError_t launch_rope(const RopeArgs &a, int dtype, int sms, cudaStream_t stre
     // resident CTAs: 228 KB an SM, 2 KB of positions and 1 KB of the system's for each
     const long long fit = 228 * 1024 / (static_cast<long long>(smem) + 3 * 1024);
     const long long ctas = std::min(gr.tiles, sms * std::max(1LL, std::min<long long>(in.min_blocks, fit)));
-    if (smem > 48 * 1024) {
+    if (smem + kPosBytes > 48 * 1024) {  // the default limit holds for both parts together
         const cudaError_t e =
             cudaFuncSetAttribute(in.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxDynamicSmem);
         if (e != cudaSuccess) return e;
