@@ -379,3 +379,17 @@ print("launched")
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300,
                        cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
     assert r.returncode == 0 and "launched" in r.stdout, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("dtype", list(STEP), ids=["f16", "bf16", "f32"])
+def test_forward_mode_rotates_the_tangent(dtype):
+    g = torch.Generator(device="cuda").manual_seed(13)
+    x, t = (torch.randn((9, 3, 64), generator=g, device="cuda").to(dtype) for _ in range(2))
+    p = positions(np.arange(9) * 1000)
+    kw = dict(rope_dims=32, traditional=True, scaling=SCALINGS["by_parts"])
+    fwad = torch.autograd.forward_ad
+    with fwad.dual_level():
+        for tangent in (t, t[:1].expand(9, 3, 64)):
+            y = fwad.unpack_dual(dattn.rope(fwad.make_dual(x, tangent), p, **kw))
+            assert torch.equal(y.primal, dattn.rope(x, p, **kw))
+            assert torch.equal(y.tangent, dattn.rope(tangent.contiguous(), p, **kw))

@@ -624,13 +624,24 @@ def dattn_rope(x, out, positions, rope_dims: int = 0, rope_base: float = 10000.0
     _rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
 
 
+_forward_ad = torch.autograd.forward_ad
+
+
+def _has_tangent(t) -> bool:
+    """Whether forward-mode differentiation follows t (a level is entered before it can)."""
+    return (getattr(_forward_ad, "_current_level", 0) >= 0
+            and _forward_ad.unpack_dual(t).tangent is not None)
+
+
 class _RopeOfGraph(torch.autograd.Function):
-    """The rotation as a node of torch's graph.  The map is linear: its derivative is the
-    call with the other ``gradient``, which is a node again where torch asks for one."""
+    """The rotation as a node of torch's graph.  The map is linear: a tangent is rotated as
+    the tensor is, and the gradient is the call with the other ``gradient``; both are nodes
+    again where torch asks for one."""
 
     @staticmethod
     def forward(ctx, x, positions, options):
         ctx.save_for_backward(positions)
+        ctx.save_for_forward(positions)
         ctx.options = options
         out = _like(x, None)
         _rope(x, out, positions, *options, None)
@@ -640,20 +651,34 @@ class _RopeOfGraph(torch.autograd.Function):
     def backward(ctx, g):
         positions, = ctx.saved_tensors
         *options, gradient = ctx.options
-        if not g.is_contiguous() or g.data_ptr() % 16:  # a broadcast sum's, or a slice
-            g = g.clone(memory_format=torch.contiguous_format)
-        return rope(g, positions, *options, gradient=not gradient), None, None
+        return rope(_dense(g), positions, *options, gradient=not gradient), None, None
+
+    @staticmethod
+    def jvp(ctx, tangent, *_):
+        positions, = ctx.saved_tensors
+        *options, gradient = ctx.options
+        return rope(_dense(tangent), positions, *options, gradient=gradient)
+
+
+def _dense(g):
+    """A derivative as torch hands it over (a broadcast sum's, a slice, zeros that are not
+    stored) as rows that the kernel takes."""
+    at = g.data_ptr()
+    if at == 0 or at % 16 or not g.is_contiguous():
+        return g.clone(memory_format=torch.contiguous_format)
+    return g
 
 
 def rope(x, positions, rope_dims: int = 0, rope_base: float = 10000.0, traditional: bool = False,
          scaling=None, gradient: bool = False, out=None, stream=None):
     """Rotate x [tokens, heads, head_dim] (f16, bf16 or f32) at ``positions``; with
     ``gradient`` the gradient of the rotated tensor into that of the tensor.  Where x
-    requires a gradient, torch finds it through this call (without ``out`` and
-    ``stream``, and not while a graph is captured)."""
-    if isinstance(x, torch.Tensor) and x.requires_grad and torch.is_grad_enabled():
+    requires a gradient or carries a forward-mode tangent, torch follows it through this
+    call (without ``out`` and ``stream``, and not while a graph is captured)."""
+    if isinstance(x, torch.Tensor) and (x.requires_grad and torch.is_grad_enabled()
+                                        or _has_tangent(x)):
         if out is not None or stream is not None:
-            raise ValueError("x requires a gradient: out and stream cannot be given")
+            raise ValueError("x requires a gradient or has a tangent: out and stream cannot be given")
         _not_recorded(stream, "out")
         if x.is_cuda and torch.cuda.is_current_stream_capturing():
             # torch's backward of a captured call can end the process where an eager graph of
