@@ -433,3 +433,26 @@ def test_rotated_parts_that_16_does_not_divide(D, rd, counts, trad):
     s = Step(counts, [50, 7, 44], 6, 3, D, 64, 16, "e4m3", rd=rd, trad=trad)
     s.run()
     s.check()
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_what_an_append_writes_counts_as_changed(page):
+    s = Step([3, 1], [5, 9], 4, 2, 64, 32, 8, "e4m3", page=page)
+    written = (s.qo, s.ck, s.cv, s.sk, s.sv)
+    before = [t._version for t in written]
+    s.run()
+    assert all(t._version > b for t, b in zip(written, before))
+    s.check()
+    with torch.inference_mode():
+        s = Step([3, 1], [5, 9], 4, 2, 64, 32, 8, "e4m3", page=page)
+        s.run()
+    s.check()
+
+
+def test_a_kept_query_that_is_rotated_in_place_is_noticed():
+    s = Step([1, 1], [5, 9], 4, 2, 64, 32, 8, "int8")
+    w = torch.ones_like(s.tq, requires_grad=True)
+    y = (w * s.tq).sum()
+    s.run(q_out=s.tq)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()

@@ -460,3 +460,18 @@ def test_the_bound_without_a_rounding_of_the_weights(B, H, Hk, D, S, block, page
     c = Case(B, H, Hk, D, S // page * page if page else S, block, "e4m3", cp, page, seed=3)
     ref, size, dot, top = _q8.decode(c.q, c.kq, c.vq, c.ks, c.vs, c.cp, block, c.table, page)
     _q8.check(_q8.f64(c.run()), ref, exact_weight_bound(ref, size, dot, top, max(cp) + 1, D, c.vs), "")
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_writing_to_out_counts_as_a_change_in_place(page):
+    c = Case(2, 4, 2, 64, 64, 16, "e4m3", [63, 5], page=page)
+    want, out = c.run(), torch.empty_like(c.tq)
+    before = out._version
+    assert torch.equal(c.run(out=out), want) and out._version > before
+    w = torch.ones_like(c.tq, requires_grad=True)
+    y = (w * c.tq).sum()
+    c.run(out=c.tq)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    with torch.inference_mode():
+        c.run(out=torch.empty_like(c.tq))

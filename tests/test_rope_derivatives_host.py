@@ -21,7 +21,7 @@ def calls(monkeypatch):
         assert not out.requires_grad
         seen.append((gradient, x.is_contiguous(), x.data_ptr() % 16 == 0 and x.data_ptr() != 0))
         y = _q8.rotate(x.detach().numpy(), positions.numpy(), rope_dims, rope_base, traditional, scaling, gradient)
-        out.copy_(torch.from_numpy(y))
+        out.numpy()[...] = y     # as the kernel does, past torch
     monkeypatch.setattr(_native, "_rope", plain)
     return seen
 
@@ -79,3 +79,20 @@ def test_a_tangent_refuses_out_and_stream(calls):
         with pytest.raises(ValueError, match="gradient"):
             dattn.rope(d, P, stream=object())
     assert not calls
+
+
+def test_writing_to_out_counts_as_a_change_in_place(calls):
+    x, w = X.clone(), torch.ones_like(X, requires_grad=True)
+    y = (w * x).sum()            # the graph keeps x for w's gradient
+    before = x._version
+    dattn.rope(x, P, out=x)
+    assert x._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        y.backward()
+    out = torch.empty_like(X)
+    before = out._version
+    dattn.dattn_rope(X, out, P)
+    assert out._version > before
+    with torch.inference_mode():
+        out = torch.empty_like(X)
+        dattn.rope(X, P, out=out)    # such a tensor counts no changes

@@ -550,6 +550,11 @@ def _like(t, stream, shape=None, dtype=None):
     return torch.empty(shape, dtype=dtype, device=t.device)
 
 
+# The kernels write through raw pointers: what a call was given to write counts as changed in
+# place, so that torch notices where a graph keeps the tensor for a gradient.
+_written = torch.autograd.graph.increment_version
+
+
 def _not_recorded(stream, name: str) -> None:
     """A batch that is being recorded on `stream` cannot own a fresh output."""
     if _RECORDING and _current_stream(_device(), stream) in _RECORDING:
@@ -622,6 +627,7 @@ def dattn_rope(x, out, positions, rope_dims: int = 0, rope_base: float = 10000.0
                traditional: bool = False, scaling=None, gradient: bool = False,
                stream=None) -> None:
     _rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
+    _written(out)
 
 
 _forward_ad = torch.autograd.forward_ad
@@ -686,9 +692,11 @@ def rope(x, positions, rope_dims: int = 0, rope_base: float = 10000.0, tradition
             raise ValueError("x requires a gradient, which a captured call does not follow: capture "
                              "the call without it and the one with gradient=True")
         return _RopeOfGraph.apply(x, positions, (rope_dims, rope_base, traditional, scaling, gradient))
-    if out is None:
-        _not_recorded(stream, "out")
-        out = _like(x, stream)
+    if out is not None:
+        dattn_rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
+        return out
+    _not_recorded(stream, "out")
+    out = _like(x, stream)
     _rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
     return out
 
@@ -811,6 +819,7 @@ def dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, 
                                                _current_stream(dev, stream))
         if st != OK:
             _check(st, "dattn_rope_append_paged_q8")
+    _written((q_out, k_cache, v_cache, k_scale, v_scale))
 
 
 def rope_append_q8(q_new, k_new, v_new, k_cache, v_cache, k_scale, v_scale, current_pos,
@@ -918,6 +927,8 @@ def _decode_q8(q, k, v, k_scale, v_scale, block_table, current_pos, scale_block,
                                           current_pos.data_ptr(), wp, wn, num_partitions, handle)
         if st != OK:
             _check(st, "dattn_decode_paged_q8")
+    if not fresh:
+        _written(out)
     return out
 
 
