@@ -456,3 +456,22 @@ def test_a_kept_query_that_is_rotated_in_place_is_noticed():
     s.run(q_out=s.tq)
     with pytest.raises(RuntimeError, match="modified by an inplace operation"):
         y.backward()
+
+
+def test_gradients_that_would_be_lost_are_refused():
+    s = Step([1, 1], [5, 9], 4, 2, 64, 32, 8, "e4m3")
+    for name in ("tq", "tk", "tv", "sk", "qo"):
+        setattr(s, name, getattr(s, name).requires_grad_())
+        with pytest.raises(ValueError, match="gradient"):
+            s.run()
+        setattr(s, name, getattr(s, name).detach())
+    fwad = torch.autograd.forward_ad
+    with fwad.dual_level():
+        keep, s.tk = s.tk, fwad.make_dual(s.tk, torch.ones_like(s.tk))
+        with pytest.raises(ValueError, match="gradient"):
+            s.run()
+        s.tk = keep
+    s.tq.requires_grad_()
+    with torch.no_grad():
+        s.run()
+    s.check()

@@ -475,3 +475,24 @@ def test_writing_to_out_counts_as_a_change_in_place(page):
         y.backward()
     with torch.inference_mode():
         c.run(out=torch.empty_like(c.tq))
+
+
+@pytest.mark.parametrize("page", [0, 16])
+def test_gradients_that_would_be_lost_are_refused(page):
+    c = Case(2, 4, 2, 64, 64, 16, "e4m3", [63, 5], page=page)
+    for name in ("tq", "tks", "tvs"):
+        setattr(c, name, getattr(c, name).requires_grad_())
+        with pytest.raises(ValueError, match="gradient"):
+            c.run()
+        setattr(c, name, getattr(c, name).detach())
+    with pytest.raises(ValueError, match="gradient"):
+        c.run(out=torch.empty_like(c.tq).requires_grad_())
+    fwad = torch.autograd.forward_ad
+    with fwad.dual_level():
+        keep, c.tq = c.tq, fwad.make_dual(c.tq, torch.ones_like(c.tq))
+        with pytest.raises(ValueError, match="gradient"):
+            c.run()
+        c.tq = keep
+    c.tq.requires_grad_()
+    with torch.no_grad():
+        c.check(c.run())

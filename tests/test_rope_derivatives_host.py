@@ -96,3 +96,18 @@ def test_writing_to_out_counts_as_a_change_in_place(calls):
     with torch.inference_mode():
         out = torch.empty_like(X)
         dattn.rope(X, P, out=out)    # such a tensor counts no changes
+
+
+def test_the_call_without_a_graph_refuses_to_lose_a_gradient(calls):
+    x, out = X.clone().requires_grad_(), torch.empty_like(X)
+    with pytest.raises(ValueError, match="gradient"):
+        dattn.dattn_rope(x, out, P)
+    with pytest.raises(ValueError, match="gradient"):
+        dattn.rope(X, P, out=torch.empty_like(X).requires_grad_())
+    with fwad.dual_level():
+        with pytest.raises(ValueError, match="gradient"):
+            dattn.dattn_rope(fwad.make_dual(X, T), out, P)
+    assert not calls
+    with torch.no_grad():
+        dattn.dattn_rope(x, out, P)
+    assert torch.equal(out, rotated(X, P))

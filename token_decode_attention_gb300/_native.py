@@ -550,6 +550,30 @@ def _like(t, stream, shape=None, dtype=None):
     return torch.empty(shape, dtype=dtype, device=t.device)
 
 
+_forward_ad = torch.autograd.forward_ad
+
+
+def _follows_tangents() -> bool:
+    """Whether a level of forward-mode differentiation has been entered."""
+    return getattr(_forward_ad, "_current_level", 0) >= 0
+
+
+def _has_tangent(t) -> bool:
+    return _forward_ad.unpack_dual(t).tangent is not None
+
+
+_grad_enabled = torch.is_grad_enabled
+
+
+def _no_derivative(**named) -> None:
+    """Refuse a tensor whose derivative torch would follow and this call would lose."""
+    grad, dual = _grad_enabled(), _follows_tangents()
+    for name, t in named.items():
+        if isinstance(t, torch.Tensor) and (grad and t.requires_grad or dual and _has_tangent(t)):
+            raise ValueError(f"{name} requires a gradient or has a tangent, which this call does "
+                             "not follow: detach it, or call under torch.no_grad()")
+
+
 # The kernels write through raw pointers: what a call was given to write counts as changed in
 # place, so that torch notices where a graph keeps the tensor for a gradient.
 _written = torch.autograd.graph.increment_version
@@ -626,17 +650,9 @@ def _rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradien
 def dattn_rope(x, out, positions, rope_dims: int = 0, rope_base: float = 10000.0,
                traditional: bool = False, scaling=None, gradient: bool = False,
                stream=None) -> None:
+    _no_derivative(x=x, out=out)
     _rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
     _written(out)
-
-
-_forward_ad = torch.autograd.forward_ad
-
-
-def _has_tangent(t) -> bool:
-    """Whether forward-mode differentiation follows t (a level is entered before it can)."""
-    return (getattr(_forward_ad, "_current_level", 0) >= 0
-            and _forward_ad.unpack_dual(t).tangent is not None)
 
 
 class _RopeOfGraph(torch.autograd.Function):
@@ -682,7 +698,7 @@ def rope(x, positions, rope_dims: int = 0, rope_base: float = 10000.0, tradition
     requires a gradient or carries a forward-mode tangent, torch follows it through this
     call (without ``out`` and ``stream``, and not while a graph is captured)."""
     if isinstance(x, torch.Tensor) and (x.requires_grad and torch.is_grad_enabled()
-                                        or _has_tangent(x)):
+                                        or _follows_tangents() and _has_tangent(x)):
         if out is not None or stream is not None:
             raise ValueError("x requires a gradient or has a tangent: out and stream cannot be given")
         _not_recorded(stream, "out")
@@ -738,7 +754,9 @@ def _q8_ordinary(k, v, k_scale, v_scale, scale_block, block_table, batch, curren
             and k_scale.get_device() == dev == v_scale.get_device()
             and current_pos.dtype in _INDEX and current_pos.shape == (batch,)
             and current_pos.is_contiguous() and current_pos.get_device() == dev
-            and scale_block > 0
+            and scale_block > 0 and not _follows_tangents()
+            and not (_grad_enabled() and (k_scale.requires_grad or v_scale.requires_grad
+                                          or k.requires_grad or v.requires_grad))
             and (lead == batch if block_table is None else
                  (block_table.dtype is torch.int32 and block_table.ndim == 2
                   and block_table.shape[0] == batch and block_table.is_contiguous()
@@ -765,6 +783,8 @@ def dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, 
         qs, ks, vs = h * d, hk * dc, hk * dc
         ordinary = (_q8_ordinary(k_cache, v_cache, k_scale, v_scale, scale_block, block_table,
                                  batch, current_pos, dev)
+                    and not (_grad_enabled() and (q_new.requires_grad or k_new.requires_grad
+                                                  or v_new.requires_grad or q_out.requires_grad))
                     and q_new.dtype is _F16 and k_new.dtype is _F16 and v_new.dtype is _F16
                     and q_out.dtype is _F16 and q_out.shape == shape and d == dc
                     and k_new.shape == new and v_new.shape == new and q_new.is_contiguous()
@@ -779,8 +799,10 @@ def dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, 
     except (AttributeError, TypeError, ValueError, ZeroDivisionError):
         ordinary = False
     if not ordinary:
-        _all_tensors(q_new=q_new, k_new=k_new, v_new=v_new, q_out=q_out, k_cache=k_cache,
-                     v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, current_pos=current_pos)
+        named = {"q_new": q_new, "k_new": k_new, "v_new": v_new, "q_out": q_out,
+                 "k_cache": k_cache, "v_cache": v_cache, "k_scale": k_scale, "v_scale": v_scale}
+        _all_tensors(**named, current_pos=current_pos)
+        _no_derivative(**named)
         batch = current_pos.shape[0] if current_pos.ndim == 1 else -1
         _q8_checks(k_cache, v_cache, k_scale, v_scale, scale_block, block_table, batch, current_pos)
         _tokens(q_new, "q_new", _F16)
@@ -875,14 +897,19 @@ def _decode_q8(q, k, v, k_scale, v_scale, block_table, current_pos, scale_block,
         lead, rows, hk, dc = k.shape
         ordinary = (_q8_ordinary(k, v, k_scale, v_scale, scale_block, block_table, b, current_pos,
                                  dev)
+                    and not (q.requires_grad and _grad_enabled())
                     and q.dtype is _F16 and d == dc and q.is_contiguous() and q.get_device() == dev
                     and (fresh or (out.dtype is _F16 and out.shape == shape
-                                   and out.is_contiguous() and out.get_device() == dev)))
+                                   and out.is_contiguous() and out.get_device() == dev
+                                   and not (out.requires_grad and _grad_enabled()))))
     except (AttributeError, TypeError, ValueError, ZeroDivisionError):
         ordinary = False
     if not ordinary:
-        _all_tensors(Q=q, k_cache=k, v_cache=v, k_scale=k_scale, v_scale=v_scale,
-                     current_pos=current_pos)
+        named = {"Q": q, "k_cache": k, "v_cache": v, "k_scale": k_scale, "v_scale": v_scale}
+        if not fresh:
+            named["out"] = out
+        _all_tensors(**named, current_pos=current_pos)
+        _no_derivative(**named)
         if q.dim() != 3:
             raise ValueError("Q must be [batch, n_heads, head_dim]")
         b, h, d = q.shape
