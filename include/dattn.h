@@ -453,7 +453,8 @@ int dattn_rope_append_paged_q8(const void *q_new, const void *k_new, const void 
 
 /*
  * Plan and workspace of the decode over an 8-bit cache, as dattn_decode_plan and
- * dattn_decode_workspace_bytes; seq_len = page_size * max_pages for a paged cache.
+ * dattn_decode_workspace_bytes; seq_len = page_size * max_pages for a paged cache, whose
+ * pool may be smaller than batch * seq_len.
  * Errors: INVALID_ARG, UNSUPPORTED, CUDA.
  */
 int dattn_decode_q8_plan(int batch, int n_heads, int n_kv_heads, int head_dim, int seq_len,

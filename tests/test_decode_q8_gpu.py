@@ -496,3 +496,20 @@ def test_gradients_that_would_be_lost_are_refused(page):
     c.tq.requires_grad_()
     with torch.no_grad():
         c.check(c.run())
+
+
+def test_a_wide_table_over_a_small_pool():
+    # capacities of 2^20 positions add up to 2^31; the pool holds 8 pages
+    B, page = 2048, 256
+    rng = np.random.default_rng(9)
+    kq, ks = _q8.random_cache(rng, 8, page, 1, 16, 16, "e4m3")
+    vq, vs = _q8.random_cache(rng, 8, page, 1, 16, 16, "e4m3")
+    table = np.full((B, 2 ** 20 // page), -1, np.int32)     # dead entries are not read
+    table[:, :2] = rng.integers(0, 8, (B, 2))
+    cp = rng.integers(0, 2 * page, B)
+    q = rng.standard_normal((B, 2, 16)).astype(np.float16)
+    got = dattn.decode_paged_q8(torch.from_numpy(q).cuda(), _q8.to_cache(kq, "e4m3"), _q8.to_cache(vq, "e4m3"),
+                                torch.from_numpy(ks).cuda(), torch.from_numpy(vs).cuda(),
+                                torch.from_numpy(table).cuda(), cur_pos_tensor(cp), 16)
+    ref, size, dot, top = _q8.decode(q, kq, vq, ks, vs, cp, 16, table, page)
+    _q8.check(_q8.f64(got), ref, _q8.decode_bound(ref, size, dot, top, 2 * page, 16, vs), "wide table")

@@ -182,9 +182,9 @@ struct Cache {
     const int32_t *block_table = nullptr;
 };
 
-int check_cache(int batch, int n_heads, int n_kv_heads, int head_dim, int seq_len, const Cache &c) {
-    if (c.kv_type != DATTN_KV_E4M3 && c.kv_type != DATTN_KV_INT8)
-        return fail(DATTN_ERR_INVALID_ARG, "kv_type=%d is not a dattn_kv_type", c.kv_type);
+// The sizes of a batch.  The queries know no more: what a paged cache's tables can name
+// may be more than its pool holds.
+int check_sizes(int batch, int n_heads, int n_kv_heads, int head_dim, int seq_len) {
     if (batch <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || seq_len <= 0)
         return fail(DATTN_ERR_INVALID_ARG,
                     "sizes must be positive (batch=%d n_heads=%d n_kv_heads=%d head_dim=%d "
@@ -196,15 +196,25 @@ int check_cache(int batch, int n_heads, int n_kv_heads, int head_dim, int seq_le
     if (head_dim % 16 != 0 || head_dim > kMaxHeadDim)
         return fail(DATTN_ERR_UNSUPPORTED, "head_dim=%d: must be a multiple of 16 and <= %d",
                     head_dim, kMaxHeadDim);
+    if (static_cast<double>(n_kv_heads) * head_dim >= 2147483648.0)
+        return fail(DATTN_ERR_UNSUPPORTED, "a position must hold fewer than 2^31 elements");
+    if (static_cast<double>(batch) * n_heads * head_dim > 4.0e18)
+        return fail(DATTN_ERR_INVALID_ARG, "the batch is too large");
+    return DATTN_OK;
+}
+
+int check_cache(int batch, int n_heads, int n_kv_heads, int head_dim, int seq_len, const Cache &c) {
+    if (c.kv_type != DATTN_KV_E4M3 && c.kv_type != DATTN_KV_INT8)
+        return fail(DATTN_ERR_INVALID_ARG, "kv_type=%d is not a dattn_kv_type", c.kv_type);
+    if (int st = check_sizes(batch, n_heads, n_kv_heads, head_dim, seq_len)) return st;
     if (c.scale_block <= 0)
         return fail(DATTN_ERR_INVALID_ARG, "scale_block=%d must be positive", c.scale_block);
     // rows of the cache are counted in 31 bits
     const double lead = c.page_size > 0 ? static_cast<double>(c.num_pages) * c.page_size
                                         : static_cast<double>(batch) * seq_len;
-    if (lead >= 2147483648.0 || static_cast<double>(n_kv_heads) * head_dim >= 2147483648.0)
+    if (lead >= 2147483648.0)
         return fail(DATTN_ERR_UNSUPPORTED, "the cache must hold fewer than 2^31 positions in all");
-    if (lead * n_kv_heads * head_dim > 4.0e18 ||
-        static_cast<double>(batch) * n_heads * head_dim > 4.0e18)
+    if (lead * n_kv_heads * head_dim > 4.0e18)
         return fail(DATTN_ERR_INVALID_ARG, "the cache is too large");
     return DATTN_OK;
 }
@@ -655,8 +665,7 @@ int dattn_decode_q8_plan(int batch, int n_heads, int n_kv_heads, int head_dim, i
                          int num_partitions, dattn_plan *plan) {
     return guarded([&]() -> int {
         if (plan == nullptr) return fail(DATTN_ERR_INVALID_ARG, "plan is NULL");
-        const Cache c{DATTN_KV_E4M3, 1};
-        if (int st = check_cache(batch, n_heads, n_kv_heads, head_dim, seq_len, c)) return st;
+        if (int st = check_sizes(batch, n_heads, n_kv_heads, head_dim, seq_len)) return st;
         Plan p;
         if (int st = make_plan(batch, n_heads, n_kv_heads, head_dim, seq_len, num_partitions, &p)) return st;
         plan->partitions = p.G;
@@ -678,8 +687,7 @@ int dattn_decode_q8_workspace_bytes(int batch, int n_heads, int n_kv_heads, int 
                                     int seq_len, int num_partitions, size_t *bytes) {
     return guarded([&]() -> int {
         if (bytes == nullptr) return fail(DATTN_ERR_INVALID_ARG, "bytes is NULL");
-        const Cache c{DATTN_KV_E4M3, 1};
-        if (int st = check_cache(batch, n_heads, n_kv_heads, head_dim, seq_len, c)) return st;
+        if (int st = check_sizes(batch, n_heads, n_kv_heads, head_dim, seq_len)) return st;
         Plan p;
         if (int st = make_plan(batch, n_heads, n_kv_heads, head_dim, seq_len, num_partitions, &p)) return st;
         *bytes = p.ws_bytes;
