@@ -513,3 +513,21 @@ def test_a_wide_table_over_a_small_pool():
                                 torch.from_numpy(table).cuda(), cur_pos_tensor(cp), 16)
     ref, size, dot, top = _q8.decode(q, kq, vq, ks, vs, cp, 16, table, page)
     _q8.check(_q8.f64(got), ref, _q8.decode_bound(ref, size, dot, top, 2 * page, 16, vs), "wide table")
+
+
+def test_refuses_a_workspace_of_another_device():
+    class Elsewhere(torch.Tensor):
+        def get_device(self):
+            return 1
+    c = Case(1, 8, 2, 128, 40000, 16, "e4m3", [39999])
+    n = dattn.dattn_decode_q8_workspace_bytes(1, 8, 2, 128, 40000)
+    assert n > 0
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    with pytest.raises(ValueError, match="workspace is on cuda:1"):
+        c.run(workspace=ws.as_subclass(Elsewhere))
+    out = torch.empty_like(c.tq)
+    with pytest.raises(ValueError, match="workspace is on cuda:1"):
+        dattn.dattn_decode_q8(c.tq, c.tk, c.tv, c.tks, c.tvs, out, c.tcp, 16, ws.as_subclass(Elsewhere))
+    c.check(c.run(workspace=ws))
+    pinned = torch.empty(n, dtype=torch.uint8, pin_memory=True)
+    c.check(c.run(workspace=pinned))

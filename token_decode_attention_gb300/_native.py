@@ -929,7 +929,8 @@ def _decode_q8(q, k, v, k_scale, v_scale, block_table, current_pos, scale_block,
     handle = _current_stream(dev, stream)
     wp, wn = None, 0
     if workspace is not None:
-        wp = _tensor(workspace, "workspace", None, workspace.dtype)
+        wp = _tensor(workspace, "workspace", None, getattr(workspace, "dtype", None))
+        _on_device((("workspace", workspace),), dev)
         wn = workspace.numel() * workspace.element_size()
     elif allocate:
         wn = _q8_workspace(dev, b, h, hk, d,
