@@ -419,7 +419,8 @@ enum dattn_kv_type { DATTN_KV_E4M3 = 1, DATTN_KV_INT8 = 2 };
  *   q_new  [tokens, n_heads, head_dim], k_new, v_new [tokens, n_kv_heads, head_dim]
  *          f16, tokens q_stride, k_stride, v_stride elements apart (as in dattn_rope)
  *   q_out  [tokens, n_heads, head_dim] f16, dense; may be q_new when that is dense,
- *          otherwise the two must not overlap (INVALID_ARG)
+ *          otherwise the two must not overlap (INVALID_ARG); nor may q_out overlap
+ *          k_new, v_new or the cache, which is not checked
  * q and k are rotated as by dattn_rope.  For each block that receives rows, per
  * key/value head and for K and V apart:
  *   need  = the smallest power of two s >= 2^-32 with |x| <= QMAX s for every

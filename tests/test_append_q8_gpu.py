@@ -475,3 +475,28 @@ def test_gradients_that_would_be_lost_are_refused():
     with torch.no_grad():
         s.run()
     s.check()
+
+
+@pytest.mark.parametrize("ragged", [False, True])
+def test_q_out_on_the_new_keys_or_values_is_refused(ragged):
+    # q is written while k and v are read
+    s = Step([1, 1, 1], [5, 9, 2], 2, 2, 64, 32, 8, "e4m3", ragged=ragged)
+    for name in ("tk", "tv"):
+        with pytest.raises(ValueError, match="q_out"):
+            s.run(q_out=getattr(s, name))
+        room = torch.empty(6 * 128 + 64, dtype=torch.float16, device="cuda")
+        keep = getattr(s, name)
+        setattr(s, name, room[: 3 * 128].view(3, 2, 64).copy_(keep))
+        with pytest.raises(ValueError, match="q_out"):
+            s.run(q_out=room[3 * 128 - 64: 6 * 128 - 64].view(3, 2, 64))
+        s.run(q_out=room[3 * 128: 6 * 128].view(3, 2, 64))            # just behind
+        # between the first and the second token of a wide projection
+        wide = torch.empty((3, 640), dtype=torch.float16, device="cuda")
+        setattr(s, name, wide[:, :128].unflatten(1, (2, 64)).copy_(keep))
+        s.run(q_out=wide.view(-1)[192: 192 + 384].view(3, 2, 64))
+        with pytest.raises(ValueError, match="q_out"):
+            s.run(q_out=wide.view(-1)[384: 384 + 384].view(3, 2, 64))
+        setattr(s, name, keep)
+    s = Step([1, 1, 1], [5, 9, 2], 2, 2, 64, 32, 8, "e4m3", ragged=ragged)
+    s.run()
+    s.check()

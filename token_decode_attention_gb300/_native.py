@@ -769,6 +769,18 @@ def _all_tensors(**named) -> None:
             raise TypeError(f"{name} must be a torch.Tensor")
 
 
+def _meets(dense, t, stride: int) -> bool:
+    """Whether `dense` holds a byte of t's tokens, `stride` elements apart."""
+    n, size = t.shape[0], t.element_size()
+    at, row, step = t.data_ptr(), t.shape[1] * t.shape[2] * size, stride * size
+    lo = dense.data_ptr()
+    hi = lo + dense.numel() * size
+    if hi <= at or lo >= at + (n - 1) * step + row:
+        return False
+    i = max(0, (lo - row - at) // step + 1)   # the first token that ends past lo
+    return i < n and at + i * step < hi
+
+
 def dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, v_scale,
                          current_pos, scale_block: int, token_offsets=None, rope_dims: int = 0,
                          rope_base: float = 10000.0, traditional: bool = False, scaling=None,
@@ -825,6 +837,8 @@ def dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, 
                      ("token_offsets", token_offsets), ("block_table", block_table))
                     if t is not None], dev)
         qs, ks, vs = _token_stride(q_new), _token_stride(k_new), _token_stride(v_new)
+    if _meets(q_out, k_new, ks) or _meets(q_out, v_new, vs):
+        raise ValueError("q_out overlaps k_new or v_new")
     args = (q_new.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(),
             k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             _KV_TYPES[k_cache.dtype], scale_block, batch, n,
