@@ -107,3 +107,25 @@ def test_steps_back_to_back_without_host_sync():
 
     for a, b in zip(go(True), go(False)):
         assert torch.equal(a, b)
+
+
+def test_inputs_in_pinned_memory_without_an_output():
+    # the small inputs of a step may lie in pinned host memory; fresh results are on the device
+    g = torch.Generator().manual_seed(3)
+    q, k, v = (torch.randn((2, h, 64), generator=g).half().pin_memory() for h in (4, 2, 2))
+    cp = torch.tensor([5, 9], dtype=torch.int32).pin_memory()
+    dev = [t.cuda() for t in (q, k, v, cp)]
+    kc, vc = (torch.zeros((2, 32, 2, 64), dtype=torch.int8, device="cuda") for _ in range(2))
+    ks, vs = (torch.zeros((2, 2, 2), device="cuda") for _ in range(2))
+    caches = [t.clone() for t in (kc, vc, ks, vs)]
+    want = dattn.rope_append_q8(*dev[:3], *caches, dev[3], 16)
+    got = dattn.rope_append_q8(q, k, v, kc, vc, ks, vs, cp, 16)
+    assert got.is_cuda and torch.equal(got, want)
+    assert all(torch.equal(a, b) for a, b in zip((kc, vc, ks, vs), caches))
+    assert torch.equal(dattn.decode_q8(q, kc, vc, ks, vs, cp, 16), dattn.decode_q8(dev[0], kc, vc, ks, vs, dev[3], 16))
+    y = dattn.rope(q, cp)
+    assert y.is_cuda and torch.equal(y, dattn.rope(dev[0], dev[3]))
+    s = torch.cuda.Stream()
+    y = dattn.rope(q, cp, stream=s)
+    s.synchronize()
+    assert torch.equal(y, dattn.rope(dev[0], dev[3]))

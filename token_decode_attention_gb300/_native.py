@@ -539,10 +539,12 @@ def _on_device(named, dev: int) -> None:
 
 def _like(t, stream, shape=None, dtype=None):
     """A tensor (as `t`, or of that shape and type) from the pool of the stream that
-    the call goes to."""
+    the call goes to; on the current device where `t` lies in pinned host memory."""
     if stream is not None:
         with torch.cuda.stream(stream):
             return _like(t, None, shape, dtype)
+    if not t.is_cuda and t.is_pinned():
+        return torch.empty(shape or t.shape, dtype=dtype or t.dtype, device="cuda")
     if shape is None:
         if t.is_contiguous():
             return torch.empty_like(t)
@@ -957,7 +959,7 @@ def _decode_q8(q, k, v, k_scale, v_scale, block_table, current_pos, scale_block,
         workspace = _like(k, stream, (wn,), torch.uint8)
         wp = workspace.data_ptr()
     if fresh:
-        out = _like(q, stream) if q.is_cuda else _like(k, stream, q.shape, _F16)
+        out = _like(q, stream)
     args = (q.data_ptr(), k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             out.data_ptr(), _KV_TYPES[k.dtype], scale_block, b, h, hk, d, rows)
     if block_table is None:
