@@ -215,3 +215,14 @@ def test_append_refuses_q_out_inside_q_new(lib):
     assert append(lib, q=A, qo=A + 256, qs=256) == INVALID
     assert append(lib, q=A, qo=A) != INVALID
     assert append(lib, q=A, qo=A + 4 * 256) != INVALID
+
+
+def test_rope_scaling_can_be_copied_and_pickled():
+    # as a part of a model's configuration it is
+    import copy
+    import pickle
+    s = dattn.RopeScaling("by_parts", 8.0, original_len=8192, low_turns=1, high_turns=32, magnitude=1.2)
+    for t in (copy.copy(s), copy.deepcopy({"a": [s]})["a"][0], pickle.loads(pickle.dumps(s))):
+        assert t == s and hash(t) == hash(s) and repr(t) == repr(s)
+        with pytest.raises(AttributeError):
+            t.factor = 3.0

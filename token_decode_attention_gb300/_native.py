@@ -504,6 +504,9 @@ class RopeScaling:
     def __hash__(self):
         return self._hash
 
+    def __reduce__(self):  # how copies and pickles make it
+        return RopeScaling, self._key()
+
     def __repr__(self):
         return "RopeScaling(" + ", ".join(f"{n}={getattr(self, n)!r}" for n in self.__slots__[:-1]) + ")"
 
