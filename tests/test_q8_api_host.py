@@ -20,10 +20,14 @@ STANDINS = r"""
 
 static std::string g_message;
 static int g_launches = 0, g_occupancy = 0;
-static bool g_no_memory = false;
+static bool g_no_memory = false, g_no_message = false;
 
 namespace dattn {
-int set_last_error(int status, const char *m) { g_message = m; return status; }
+int set_last_error(int status, const char *m) {
+    if (g_no_message) throw std::bad_alloc();
+    g_message = m;
+    return status;
+}
 int device_facts(DeviceFacts *out) {
     if (g_no_memory) throw std::bad_alloc();
     static unsigned word;
@@ -87,4 +91,22 @@ def test_queries_take_a_wide_table_over_a_small_pool(run):
     // what no call takes is refused by the queries too
     CHECK(dattn_decode_q8_workspace_bytes(2048, 2, 1, 16, 0, 0, &bytes) == DATTN_ERR_INVALID_ARG);
     CHECK(dattn_decode_q8_workspace_bytes(1, 1 << 30, 1 << 30, 16, 64, 0, &bytes) == DATTN_ERR_UNSUPPORTED);
+""")
+
+
+def test_a_failure_of_the_host_has_its_own_message(run):
+    run("""
+    dattn_rope_params r{64, 0, 10000.0, 0, 1.0, 0.0, 0.0, 0.0, 1.0};
+    g_message = "of an earlier call";
+    g_no_memory = true;
+    CHECK(dattn_rope(A, A, DATTN_F16, 4, 2, 64, 128, 128, (uint32_t *)A, &r, 0, nullptr) == DATTN_ERR_CUDA);
+    CHECK(g_message.find("earlier") == std::string::npos && !g_message.empty());
+    g_message = "of an earlier call";
+    size_t bytes = 0;
+    CHECK(dattn_decode_q8_workspace_bytes(1, 2, 1, 16, 64, 0, &bytes) == DATTN_ERR_CUDA);
+    CHECK(g_message.find("earlier") == std::string::npos && !g_message.empty());
+    CHECK(g_launches == 0);
+    // nor does a failure to keep the message leave the entry
+    g_no_message = true;
+    CHECK(dattn_decode_q8_workspace_bytes(1, 2, 1, 16, 64, 0, &bytes) == DATTN_ERR_CUDA);
 """)

@@ -51,8 +51,12 @@ template <typename F>
 int guarded(F f) noexcept {
     try {
         return f();
-    } catch (const std::exception &) {
-        return DATTN_ERR_CUDA;
+    } catch (const std::exception &e) {
+        try {
+            return fail(DATTN_ERR_CUDA, "on the host: %s", e.what());
+        } catch (const std::exception &) {  // the message's own memory
+            return DATTN_ERR_CUDA;
+        }
     }
 }
 
