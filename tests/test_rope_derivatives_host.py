@@ -111,3 +111,18 @@ def test_the_call_without_a_graph_refuses_to_lose_a_gradient(calls):
     with torch.no_grad():
         dattn.dattn_rope(x, out, P)
     assert torch.equal(out, rotated(X, P))
+
+
+def test_neither_pass_is_captured(calls, monkeypatch):
+    x = X.clone().requires_grad_()
+    y = dattn.rope(x, P)
+    monkeypatch.setattr(_native, "_captured", lambda t: True, raising=False)
+    with pytest.raises(ValueError, match="captured"):
+        dattn.rope(x, P)
+    # the forward pass was an ordinary call, its backward pass is being captured
+    with pytest.raises(ValueError, match="captured"):
+        y.sum().backward()
+    assert x.grad is None
+    with torch.no_grad():
+        dattn.rope(x, P, gradient=True)
+    monkeypatch.undo()

@@ -660,6 +660,18 @@ def dattn_rope(x, out, positions, rope_dims: int = 0, rope_base: float = 10000.0
     _written(out)
 
 
+def _captured(t) -> bool:
+    return t.is_cuda and torch.cuda.is_current_stream_capturing()
+
+
+def _refuse_capture(t) -> None:
+    """Neither pass of torch's graph is captured: a backward pass that is captured while an
+    eager graph of the same leaves lives can end the process."""
+    if _captured(t):
+        raise ValueError("x requires a gradient, which a captured call does not follow: capture "
+                         "the call without it and the one with gradient=True")
+
+
 class _RopeOfGraph(torch.autograd.Function):
     """The rotation as a node of torch's graph.  The map is linear: a tangent is rotated as
     the tensor is, and the gradient is the call with the other ``gradient``; both are nodes
@@ -676,6 +688,7 @@ class _RopeOfGraph(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, g):
+        _refuse_capture(g)
         positions, = ctx.saved_tensors
         *options, gradient = ctx.options
         return rope(_dense(g), positions, *options, gradient=not gradient), None, None
@@ -707,11 +720,7 @@ def rope(x, positions, rope_dims: int = 0, rope_base: float = 10000.0, tradition
         if out is not None or stream is not None:
             raise ValueError("x requires a gradient or has a tangent: out and stream cannot be given")
         _not_recorded(stream, "out")
-        if x.is_cuda and torch.cuda.is_current_stream_capturing():
-            # torch's backward of a captured call can end the process where an eager graph of
-            # the same leaves is alive on another stream
-            raise ValueError("x requires a gradient, which a captured call does not follow: capture "
-                             "the call without it and the one with gradient=True")
+        _refuse_capture(x)
         return _RopeOfGraph.apply(x, positions, (rope_dims, rope_base, traditional, scaling, gradient))
     if out is not None:
         dattn_rope(x, out, positions, rope_dims, rope_base, traditional, scaling, gradient, stream)
