@@ -51,6 +51,16 @@ cudaError_t cudaGetLastError() { return cudaSuccess; }
 const char *cudaGetErrorName(cudaError_t) { return ""; }
 const char *cudaGetErrorString(cudaError_t) { return ""; }
 }
+// allocations that are alive
+static long long g_alive = 0;
+void *operator new(size_t n) {
+    void *p = std::malloc(n);
+    if (!p) throw std::bad_alloc();
+    ++g_alive;
+    return p;
+}
+void operator delete(void *p) noexcept { if (p) --g_alive, std::free(p); }
+void operator delete(void *p, size_t) noexcept { operator delete(p); }
 static char *const A = reinterpret_cast<char *>(0x10000);
 #define CHECK(x) do { if (!(x)) { std::printf("line %d: %s (%s)\n", __LINE__, #x, g_message.c_str()); return 1; } } while (0)
 """
@@ -109,4 +119,24 @@ def test_a_failure_of_the_host_has_its_own_message(run):
     // nor does a failure to keep the message leave the entry
     g_no_message = true;
     CHECK(dattn_decode_q8_workspace_bytes(1, 2, 1, 16, 64, 0, &bytes) == DATTN_ERR_CUDA);
+""")
+
+
+def test_plans_are_kept_for_a_bounded_number_of_shapes(run):
+    # a process that sees a new capacity at every step keeps no more than some of them
+    run("""
+    dattn_plan first, again;
+    CHECK(dattn_decode_q8_plan(1, 8, 8, 64, 500, 0, &first) == DATTN_OK);
+    const long long before = g_alive;
+    for (int s = 1; s <= 20000; ++s) {
+        dattn_plan p;
+        CHECK(dattn_decode_q8_plan(2, 8, 2, 128, s, 0, &p) == DATTN_OK);
+    }
+    CHECK(g_alive - before < 2000);
+    const int asked = g_occupancy;
+    CHECK(dattn_decode_q8_plan(2, 8, 2, 128, 20000, 0, &again) == DATTN_OK);
+    CHECK(g_occupancy == asked);   // the latest is kept
+    CHECK(dattn_decode_q8_plan(1, 8, 8, 64, 500, 0, &again) == DATTN_OK);
+    CHECK(first.partitions == again.partitions && first.cluster_size == again.cluster_size &&
+          first.workspace_bytes == again.workspace_bytes && first.heads_per_cta == again.heads_per_cta);
 """)

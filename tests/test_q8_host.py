@@ -226,3 +226,22 @@ def test_rope_scaling_can_be_copied_and_pickled():
         assert t == s and hash(t) == hash(s) and repr(t) == repr(s)
         with pytest.raises(AttributeError):
             t.factor = 3.0
+
+
+def test_workspace_sizes_are_kept_for_a_bounded_number_of_shapes(monkeypatch):
+    class Lib:
+        asked = 0
+
+        def dattn_decode_q8_workspace_bytes(self, b, h, hk, d, s, parts, out):
+            self.asked += 1
+            out._obj.value = 16 * s
+            return 0
+    lib = Lib()
+    monkeypatch.setattr(_native, "load", lambda: lib)
+    monkeypatch.setattr(_native, "_Q8_WORKSPACE", {})
+    for s in range(1, 20001):
+        assert dattn.dattn_decode_q8_workspace_bytes(1, 8, 8, 64, s) == 16 * s
+    assert len(_native._Q8_WORKSPACE) < 2000
+    lib.asked = 0
+    assert dattn.dattn_decode_q8_workspace_bytes(1, 8, 8, 64, 20000) == 16 * 20000 and lib.asked == 0
+    assert dattn.dattn_decode_q8_workspace_bytes(1, 8, 8, 64, 1) == 16 and lib.asked == 1

@@ -906,6 +906,8 @@ def _q8_workspace(*key) -> int:
         size = ctypes.c_size_t(0)
         _check(load().dattn_decode_q8_workspace_bytes(*key[1:], ctypes.byref(size)),
                "dattn_decode_q8_workspace_bytes")
+        if len(_Q8_WORKSPACE) >= 1024:  # a program that never repeats a shape
+            _Q8_WORKSPACE.clear()
         n = _Q8_WORKSPACE[key] = int(size.value)
     return n
 

@@ -32,6 +32,7 @@ constexpr int kStaticSmem = 4096;  // the decode kernel's static shared memory a
 constexpr long long kClusterTiles = 8;
 constexpr long long kUnitTiles = 16;  // the same with a CTA for each unit
 constexpr long long kShortUnitTiles = 10;
+constexpr size_t kKeptPlans = 1024;  // a program that never repeats a shape starts anew
 
 int fail(int status, const char *fmt, ...) {
     char buf[512];
@@ -420,6 +421,7 @@ int make_plan(int B, int H, int Hk, int D, int S, int num_partitions, Plan *out)
         if (static_cast<double>(B) * H * ((D + p.combine_chunk - 1) / p.combine_chunk) > 2147483647.0)
             return fail(DATTN_ERR_UNSUPPORTED, "batch x n_heads is too large");
     }
+    if (plans.size() >= kKeptPlans) plans.clear();
     plans[key] = p;
     *out = p;
     return DATTN_OK;
