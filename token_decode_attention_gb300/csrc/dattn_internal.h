@@ -195,16 +195,10 @@ __host__ __device__ constexpr int q8_tile_bytes(int dp) { return 32 * dp + 128; 
 
 // Warps of a decode CTA, CTAs of an SM and ring slots of a warp, by the row size and
 // the 8-column tiles of query heads.
-#ifndef Q8_SMALL_WARPS
-#define Q8_SMALL_WARPS 8
-#endif
-__host__ __device__ constexpr bool q8_small(int dp, int nt) { return dp * nt <= 128; }
-__host__ __device__ constexpr int q8_warps(int dp, int nt) { return q8_small(dp, nt) ? Q8_SMALL_WARPS : 8; }
-__host__ __device__ constexpr int q8_ctas_per_sm(int dp, int nt) {
-    return q8_small(dp, nt) ? 16 / Q8_SMALL_WARPS : 1;
-}
+constexpr int kQ8Warps = 8;
+__host__ __device__ constexpr int q8_ctas_per_sm(int dp, int nt) { return dp * nt <= 128 ? 2 : 1; }
 __host__ __device__ constexpr int q8_slots(int dp, int nt) {
-    return 212 * 1024 / (q8_warps(dp, nt) * q8_ctas_per_sm(dp, nt)) / q8_tile_bytes(dp);
+    return 212 * 1024 / (kQ8Warps * q8_ctas_per_sm(dp, nt)) / q8_tile_bytes(dp);
 }
 
 // Whether the eight columns hold each of gq query heads twice.

@@ -45,7 +45,7 @@ cudaError_t decode_q8_max_clusters(int dp, int nt, bool pair, int smem, int clus
     if (i == nullptr) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(cluster));
-    cfg.blockDim = dim3(i->nw * 32);
+    cfg.blockDim = dim3(kQ8Warps * 32);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -59,15 +59,13 @@ cudaError_t decode_q8_max_clusters(int dp, int nt, bool pair, int smem, int clus
 
 cudaError_t launch_decode_q8(const Q8DecodeArgs &a, int dp, int nt, int kv, int smem,
                              cudaStream_t stream) {
-    const bool pair = q8_pair(a.gq);
-    const Q8Instance *i = q8_instance<kKvE4m3>(dp, nt, pair);
-    const void *fn = kernel_of(dp, nt, pair, kv, a.cluster > 0);
-    if (i == nullptr || fn == nullptr || a.partitions <= 0 || a.cluster > kMaxCluster)
+    const void *fn = kernel_of(dp, nt, q8_pair(a.gq), kv, a.cluster > 0);
+    if (fn == nullptr || a.partitions <= 0 || a.cluster > kMaxCluster)
         return cudaErrorInvalidValue;
     void *args[] = {const_cast<Q8DecodeArgs *>(&a)};
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(a.partitions));
-    cfg.blockDim = dim3(i->nw * 32);
+    cfg.blockDim = dim3(kQ8Warps * 32);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];

@@ -191,13 +191,13 @@ __device__ __forceinline__ uint32_t chunk_at(int r, int c) {
 }
 
 // DP: head_dim rounded up to 64, 128 or 256 (channels above head_dim are zero
-// filled).  NT: 8-column tiles of query heads.  NW: warps.  NS: ring slots.
+// filled).  NT: 8-column tiles of query heads.  NS: ring slots.
 // PAIR (NT = 1): at most four query heads, each in columns h and h + 4.
-template <int DP, int NT, bool PAIR, int KV, int NW, int NS, bool CLUSTER>
-__global__ void __launch_bounds__(NW * 32, q8_ctas_per_sm(DP, NT)) decode_q8_kernel(const Q8DecodeArgs a) {
+template <int DP, int NT, bool PAIR, int KV, int NS, bool CLUSTER>
+__global__ void __launch_bounds__(kQ8Warps * 32, q8_ctas_per_sm(DP, NT)) decode_q8_kernel(const Q8DecodeArgs a) {
     constexpr int NJ = DP / 64;           // 64-channel spans of a row
     constexpr int NM = DP / 16;           // 16-channel tiles of the output
-    constexpr int kThreads = NW * 32;
+    constexpr int NW = kQ8Warps, kThreads = NW * 32;
     constexpr int kTileBytes = q8_tile_bytes(DP);
     constexpr int CPR = DP / 16;          // 16-byte chunks per row
     constexpr int RPI = 32 / CPR;         // rows per warp-wide copy
@@ -796,21 +796,19 @@ __global__ void __launch_bounds__(NW * 32, q8_ctas_per_sm(DP, NT)) decode_q8_ker
 struct Q8Instance {
     int dp, nt;
     bool pair;
-    int nw, ns;
     const void *split, *cluster;
 };
 
 // The instances of one 8-bit type: 16 warps on an SM where a thread's accumulators
 // and query fragments leave room for 128 registers, 8 otherwise; ring slots that
-// fill ~200 KB of an SM's shared memory.
+// fill ~200 KB of an SM's shared memory.  256 channels with 9 to 16 query heads need
+// more than the 255 registers that there are and spill 32 to 84 bytes; no other does.
 template <int KV>
 const Q8Instance *q8_instance(int dp, int nt, bool pair) {
 #define DATTN_Q8(DP, NT, PAIR)                                                                      \
-    {DP, NT, PAIR, q8_warps(DP, NT), q8_slots(DP, NT),                                              \
-     reinterpret_cast<const void *>(                                                                \
-         decode_q8_kernel<DP, NT, PAIR, KV, q8_warps(DP, NT), q8_slots(DP, NT), false>),            \
-     reinterpret_cast<const void *>(                                                                \
-         decode_q8_kernel<DP, NT, PAIR, KV, q8_warps(DP, NT), q8_slots(DP, NT), true>)}
+    {DP, NT, PAIR,                                                                                  \
+     reinterpret_cast<const void *>(decode_q8_kernel<DP, NT, PAIR, KV, q8_slots(DP, NT), false>),   \
+     reinterpret_cast<const void *>(decode_q8_kernel<DP, NT, PAIR, KV, q8_slots(DP, NT), true>)}
     static const Q8Instance table[] = {
         DATTN_Q8(64, 1, true),  DATTN_Q8(64, 1, false),  DATTN_Q8(64, 2, false),
         DATTN_Q8(128, 1, true), DATTN_Q8(128, 1, false), DATTN_Q8(128, 2, false),

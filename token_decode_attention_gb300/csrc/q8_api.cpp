@@ -361,7 +361,7 @@ int make_plan(int B, int H, int Hk, int D, int S, int num_partitions, Plan *out)
     p.vheads = Hk * p.vheads_per_kv;
     p.nt = p.gq > 8 ? 2 : 1;
     p.dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-    p.warps = dattn::q8_warps(p.dp, p.nt);
+    p.warps = dattn::kQ8Warps;
     p.slots = dattn::q8_slots(p.dp, p.nt);
     p.ctas_per_sm = dattn::q8_ctas_per_sm(p.dp, p.nt);
     // Heads per CTA, of those that keep the most warps busy.  More heads make longer
