@@ -756,11 +756,11 @@ def _q8_checks(k, v, k_scale, v_scale, scale_block, block_table, batch, current_
     _index32(current_pos, "current_pos", (batch,))
 
 
-def _q8_ordinary(k, v, k_scale, v_scale, scale_block, block_table, batch, current_pos, dev) -> bool:
-    """Whether the cache and its companions are what an ordinary call brings."""
+def _q8_ordinary(k, v, k_scale, v_scale, scale_block, block_table, batch, current_pos, dev, shape) -> bool:
+    """Whether the cache, of that shape, and its companions are what an ordinary call brings."""
     dtype = k.dtype
-    lead, rows, hk, _ = shape = k.shape
-    scales = (lead, -(-rows // scale_block), hk)
+    lead = shape[0]
+    scales = (lead, -(-shape[1] // scale_block), shape[2])
     return (dtype in _KV_TYPES and v.dtype is dtype and v.shape == shape and k_scale.dtype is _F32
             and v_scale.dtype is _F32 and k_scale.shape == scales and v_scale.shape == scales
             and k.is_contiguous() and v.is_contiguous() and k_scale.is_contiguous()
@@ -768,9 +768,7 @@ def _q8_ordinary(k, v, k_scale, v_scale, scale_block, block_table, batch, curren
             and k_scale.get_device() == dev == v_scale.get_device()
             and current_pos.dtype in _INDEX and current_pos.shape == (batch,)
             and current_pos.is_contiguous() and current_pos.get_device() == dev
-            and scale_block > 0 and not _follows_tangents()
-            and not (_grad_enabled() and (k_scale.requires_grad or v_scale.requires_grad
-                                          or k.requires_grad or v.requires_grad))
+            and scale_block > 0
             and (lead == batch if block_table is None else
                  (block_table.dtype is torch.int32 and block_table.ndim == 2
                   and block_table.shape[0] == batch and block_table.is_contiguous()
@@ -783,14 +781,8 @@ def _all_tensors(**named) -> None:
             raise TypeError(f"{name} must be a torch.Tensor")
 
 
-def _meets(dense, t, stride: int) -> bool:
-    """Whether `dense` holds a byte of t's tokens, `stride` elements apart."""
-    n, size = t.shape[0], t.element_size()
-    at, row, step = t.data_ptr(), t.shape[1] * t.shape[2] * size, stride * size
-    lo = dense.data_ptr()
-    hi = lo + dense.numel() * size
-    if hi <= at or lo >= at + (n - 1) * step + row:
-        return False
+def _meets(lo: int, hi: int, at: int, n: int, step: int, row: int) -> bool:
+    """Whether the bytes [lo, hi) hold one of n tokens of `row` bytes, `step` apart from `at`."""
     i = max(0, (lo - row - at) // step + 1)   # the first token that ends past lo
     return i < n and at + i * step < hi
 
@@ -804,13 +796,18 @@ def dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, 
     try:
         batch, = current_pos.shape
         n, h, d = shape = q_new.shape
-        lead, rows, hk, dc = k_cache.shape
+        lead, rows, hk, dc = cache = k_cache.shape
         new = (n, hk, dc)
-        qs, ks, vs = h * d, hk * dc, hk * dc
+        qs = h * d
+        ks = vs = hk * dc
         ordinary = (_q8_ordinary(k_cache, v_cache, k_scale, v_scale, scale_block, block_table,
-                                 batch, current_pos, dev)
-                    and not (_grad_enabled() and (q_new.requires_grad or k_new.requires_grad
-                                                  or v_new.requires_grad or q_out.requires_grad))
+                                 batch, current_pos, dev, cache)
+                    and not (_grad_enabled()
+                             and (q_new.requires_grad or k_new.requires_grad or v_new.requires_grad
+                                  or q_out.requires_grad or k_cache.requires_grad
+                                  or v_cache.requires_grad or k_scale.requires_grad
+                                  or v_scale.requires_grad))
+                    and getattr(_forward_ad, "_current_level", 0) < 0
                     and q_new.dtype is _F16 and k_new.dtype is _F16 and v_new.dtype is _F16
                     and q_out.dtype is _F16 and q_out.shape == shape and d == dc
                     and k_new.shape == new and v_new.shape == new and q_new.is_contiguous()
@@ -851,9 +848,12 @@ def dattn_rope_append_q8(q_new, k_new, v_new, q_out, k_cache, v_cache, k_scale, 
                      ("token_offsets", token_offsets), ("block_table", block_table))
                     if t is not None], dev)
         qs, ks, vs = _token_stride(q_new), _token_stride(k_new), _token_stride(v_new)
-    if _meets(q_out, k_new, ks) or _meets(q_out, v_new, vs):
+    kp, vp, qo = k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr()
+    end, row = qo + 2 * n * h * d, 2 * hk * d
+    if (qo < kp + 2 * n * ks and kp < end and _meets(qo, end, kp, n, 2 * ks, row)
+            or qo < vp + 2 * n * vs and vp < end and _meets(qo, end, vp, n, 2 * vs, row)):
         raise ValueError("q_out overlaps k_new or v_new")
-    args = (q_new.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), q_out.data_ptr(),
+    args = (q_new.data_ptr(), kp, vp, qo,
             k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
             _KV_TYPES[k_cache.dtype], scale_block, batch, n,
             None if token_offsets is None else token_offsets.data_ptr(), qs, ks, vs, h, hk, d, rows)
@@ -924,14 +924,17 @@ def _decode_q8(q, k, v, k_scale, v_scale, block_table, current_pos, scale_block,
     fresh = out is None and allocate
     try:
         b, h, d = shape = q.shape
-        lead, rows, hk, dc = k.shape
+        lead, rows, hk, dc = cache = k.shape
         ordinary = (_q8_ordinary(k, v, k_scale, v_scale, scale_block, block_table, b, current_pos,
-                                 dev)
-                    and not (q.requires_grad and _grad_enabled())
+                                 dev, cache)
+                    and not (_grad_enabled()
+                             and (q.requires_grad or k.requires_grad or v.requires_grad
+                                  or k_scale.requires_grad or v_scale.requires_grad
+                                  or not fresh and out.requires_grad))
+                    and getattr(_forward_ad, "_current_level", 0) < 0
                     and q.dtype is _F16 and d == dc and q.is_contiguous() and q.get_device() == dev
                     and (fresh or (out.dtype is _F16 and out.shape == shape
-                                   and out.is_contiguous() and out.get_device() == dev
-                                   and not (out.requires_grad and _grad_enabled()))))
+                                   and out.is_contiguous() and out.get_device() == dev)))
     except (AttributeError, TypeError, ValueError, ZeroDivisionError):
         ordinary = False
     if not ordinary:
