@@ -74,11 +74,11 @@ cudaError_t launch_append_q8(const Q8AppendArgs &a, int kv, int sms, cudaStream_
     while (gr.set < kWarps && kHeads * gr.groups_per_warp * (gr.set / gr.warps) < a.kv_heads) gr.set *= 2;
     gr.heads_per_set = kHeads * gr.groups_per_warp * (gr.set / gr.warps);
     gr.head_chunks = (a.kv_heads + gr.heads_per_set - 1) / gr.heads_per_set;
-    // about two blocks per window when sequences are long, one token when short; smaller
-    // where that leaves warps idle, since a set takes its blocks one after another (301
-    // tokens of 13 sequences, 8 heads: 12.5 us with windows of 16 tokens, 8.8 with 1).
-    // Windows of one block at most, and twice as many of them: 7050 tokens of 8 heads in
-    // blocks of eight 21.5 us against 15.4; 8192 of 32 on 8 heads 36.7 against 36.4.
+    // Two blocks per window at most, one token per window when sequences are short; smaller
+    // where two blocks would leave warps idle, since a set takes its blocks one after another
+    // (301 tokens of 13 sequences, 8 heads: 12.5 us with windows of 16 tokens, 8.8 with 1).
+    // Two blocks, as taken, and one, with twice as many windows: 7050 tokens of 8 heads in
+    // blocks of eight 15.4 and 21.5 us; 8192 of 32 on 8 heads 36.4 and 36.7.
     const int sets = kWarps / gr.set;
     const long long mean = std::max(1LL, a.tokens / a.B);
     gr.window = static_cast<int>(std::min<long long>(mean, 2LL * a.scale_block));

@@ -32,8 +32,9 @@
 // which stream while the others compute.
 //
 // Measured (graph replay): 8192 tokens of 32 query and 8 key/value heads of 128, 185 MB,
-// 36.7 us, 5.0 TB/s (k and v alone 22, q alone 29.5); one token each of 256 sequences of
-// 40 heads, 13 MB, 5.9 us; one token of one sequence 2.6 us.
+// 36.4 us, 5.1 TB/s (k and v alone 22, q alone 29.5); one token each of 256 sequences of
+// 40 heads, 13 MB, 5.9 us; one token of one sequence 2.6 us.  The instances that read
+// element by element (a rotated part that four do not divide) spill 220 bytes.
 #pragma once
 
 #include <cuda_fp16.h>
