@@ -22,6 +22,12 @@ def cuda_available():
 def pytest_collection_modifyitems(config, items):
     import torch
     if torch.cuda.is_available():
+        # These hand made-up addresses to the library.  Some calls pass its checks and then
+        # end for want of a device; with one they would be launched and fault.
+        skip = pytest.mark.skip(reason="made-up addresses: only where there is no CUDA device")
+        for item in items:
+            if item.path.name == "test_q8_host.py" and "lib" in item.fixturenames:
+                item.add_marker(skip)
         return
     skip = pytest.mark.skip(reason="no CUDA device")
     for item in items:

@@ -140,3 +140,31 @@ def test_plans_are_kept_for_a_bounded_number_of_shapes(run):
     CHECK(first.partitions == again.partitions && first.cluster_size == again.cluster_size &&
           first.workspace_bytes == again.workspace_bytes && first.heads_per_cta == again.heads_per_cta);
 """)
+
+
+def test_overlapping_tensors_are_refused_and_neighbours_launched(run):
+    # rows of 2 x 64 f16
+    run("""
+    dattn_rope_params r{8, 0, 10000.0, 0, 1.0, 0.0, 0.0, 0.0, 1.0};
+    auto rope = [&](char *x, long long xs, char *out, long long os, long long T) {
+        return dattn_rope(x, out, DATTN_F16, T, 2, 64, xs, os, (uint32_t *)A, &r, 0, nullptr);
+    };
+    CHECK(rope(A, 256, A + 256, 256, 4) == DATTN_OK);
+    CHECK(rope(A + 256, 256, A, 256, 4) == DATTN_OK);
+    CHECK(rope(A, 136, A, 128, 1) == DATTN_OK);
+    CHECK(rope(A, 128, A + 1024, 128, 4) == DATTN_OK);
+    CHECK(rope(A, 128, A, 128, 4) == DATTN_OK);
+    CHECK(g_launches == 5);
+    CHECK(rope(A, 128, A + 16, 128, 4) == DATTN_ERR_INVALID_ARG);
+    CHECK(rope(A, 256, A + 240, 256, 4) == DATTN_ERR_INVALID_ARG);
+    CHECK(rope(A, 136, A, 128, 4) == DATTN_ERR_INVALID_ARG);
+    auto append = [&](char *q, long long qs, char *qo) {
+        return dattn_rope_append_q8(q, A, A, qo, A, A, (float *)A, (float *)A, DATTN_KV_E4M3, 16, 4, 4, nullptr, qs, 64, 64,
+                                    2, 1, 64, 64, &r, (uint32_t *)A, nullptr);
+    };
+    CHECK(append(A, 128, A) == DATTN_OK && append(A, 128, A + 1024) == DATTN_OK);
+    CHECK(g_launches == 7);
+    CHECK(append(A, 128, A + 16) == DATTN_ERR_INVALID_ARG);
+    CHECK(append(A, 256, A) == DATTN_ERR_INVALID_ARG && append(A, 256, A + 256) == DATTN_ERR_INVALID_ARG);
+    CHECK(g_launches == 7);
+""")
