@@ -401,8 +401,8 @@ int dattn_rope(const void *x, void *out, int dtype, long long tokens, int n_head
  *           block_table       [batch, max_pages] int32, as in dattn_decode_paged_f16;
  *           page_size is a multiple of scale_block
  * head_dim is a multiple of 16, at most 256; a cache holds fewer than 2^31 positions
- * in all.  Scales are not negative and
- * at most 2^60; 0 stands for a block of zeros.
+ * in all.  Scales are finite and not negative, V's at most 2^60; 0 stands for a
+ * block of zeros.
  */
 enum dattn_kv_type { DATTN_KV_E4M3 = 1, DATTN_KV_INT8 = 2 };
 
