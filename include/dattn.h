@@ -73,7 +73,7 @@ enum dattn_status {
     DATTN_ERR_CUDA = -5,        /* a CUDA runtime call or kernel launch failed      */
     DATTN_ERR_TIMEOUT = -6,     /* a kernel gave up waiting on its own pipeline     */
     DATTN_ERR_BAD_PAGE = -7,    /* a live position's block-table entry was invalid  */
-    DATTN_ERR_BAD_POSITION = -8 /* an append position was outside the cache         */
+    DATTN_ERR_BAD_POSITION = -8 /* a new token's position was outside the cache     */
 };
 
 /* Library version: major*10000 + minor*100 + patch. */
@@ -490,6 +490,83 @@ int dattn_decode_paged_q8(const void *Q, const void *K_pages, const void *V_page
                           size_t workspace_bytes, int num_partitions, dattn_stream_t stream);
 
 /*
+ * Attention over a 16-bit cache (f16 or bf16) with grouped heads, for one token per
+ * sequence or a ragged batch of them (a prompt, chunks of prompts, a mixed step), with
+ * all positions visible or a sliding window and a few first tokens that stay visible.
+ *   Q    [tokens, n_heads, head_dim] of `dtype` (DATTN_F16 or DATTN_BF16), tokens
+ *        q_stride elements apart (as in dattn_rope)
+ *   K_cache, V_cache  [batch, seq_len, n_kv_heads, head_dim], or pages [num_pages,
+ *        page_size, n_kv_heads, head_dim] with block_table as in dattn_decode_paged_f16
+ *        (seq_len = page_size * max_pages); the new tokens' rows are there already
+ *   out  [tokens, n_heads, head_dim], dense; shares no byte with the inputs (INVALID_ARG)
+ * token_offsets and current_pos are those of dattn_rope_append_q8: sequence b brings
+ * tokens token_offsets[b] .. token_offsets[b+1]-1, the last at position
+ * min(current_pos[b], seq_len-1) and the ones before it at the positions before;
+ * token_offsets NULL: one token per sequence.  Rows from token_offsets[batch] on are
+ * padding, their rows of `out` are left as they were.  A token at position p sees, of
+ * 0 .. p, the last `window` positions (0: all) and the first `sinks` ones:
+ *   out[t,h,:] = sum_j softmax_j(Q[t,h,:] . K[j,e,:] / sqrt(head_dim)) V[j,e,:]
+ * over the positions j it sees and e = h / (n_heads / n_kv_heads).  Products accumulate
+ * in fp32, the running maximum and sum are fp32, out is rounded once.  Positions a token
+ * does not see never enter its row, whatever their contents (NaN included).  A token
+ * whose position would be negative sees nothing: its row is zeros and
+ * dattn_device_error() reports DATTN_ERR_BAD_POSITION.  Table entries are used only for
+ * pages with a position that some token of the call sees, so those that a window has
+ * left behind may be freed; an invalid one is reported as DATTN_ERR_BAD_PAGE, as in
+ * dattn_decode_paged_f16.
+ * workspace: device scratch, 16-byte aligned, of dattn_attend_workspace_bytes (`ragged`
+ * non-zero where token_offsets is given; NULL where that is 0); calls on different
+ * streams need different ones.  head_dim: a multiple of 8, at most 256; tokens x n_heads
+ * below 2^31.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
+ */
+int dattn_attend_workspace_bytes(int batch, int tokens, int ragged, int n_heads, int n_kv_heads,
+                                 int head_dim, int seq_len, int window, int sinks, size_t *bytes);
+int dattn_attend(const void *Q, const void *K_cache, const void *V_cache, void *out, int dtype,
+                 int batch, int tokens, const int32_t *token_offsets, long long q_stride,
+                 int n_heads, int n_kv_heads, int head_dim, int seq_len, int window, int sinks,
+                 const uint32_t *current_pos, void *workspace, size_t workspace_bytes,
+                 dattn_stream_t stream);
+int dattn_attend_paged(const void *Q, const void *K_pages, const void *V_pages, void *out, int dtype,
+                       int batch, int tokens, const int32_t *token_offsets, long long q_stride,
+                       int n_heads, int n_kv_heads, int head_dim, int page_size, int max_pages,
+                       long long num_pages, const int32_t *block_table, int window, int sinks,
+                       const uint32_t *current_pos, void *workspace, size_t workspace_bytes,
+                       dattn_stream_t stream);
+
+/*
+ * Decode attention of a batch whose sequences share their first `shared_len` positions
+ * (a system prompt, samples of one prompt): the shared keys and values are read once
+ * for all sequences.  One token per sequence, types, heads and q_stride as in
+ * dattn_attend, every position up to the token's own visible.
+ *   dattn_decode_shared        K_prefix, V_prefix [shared_len, n_kv_heads, head_dim] and
+ *       a cache [batch, seq_len, n_kv_heads, head_dim] of what follows them;
+ *       current_pos[b] counts in that cache: the token is at row
+ *       min(current_pos[b], seq_len-1) of it and sees the whole prefix
+ *   dattn_decode_shared_paged  one pool of pages: the first shared_len positions are
+ *       those of the first sequence's pages (its row of block_table; entries of the other
+ *       rows for pages that hold shared positions only are not used), the others each
+ *       sequence's own.  current_pos[b] counts from the first shared position; a token
+ *       inside them sees the shared positions up to its own
+ * workspace as in dattn_attend, of dattn_decode_shared_workspace_bytes: own_len is
+ * seq_len, or page_size * max_pages.
+ * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
+ */
+int dattn_decode_shared_workspace_bytes(int batch, int n_heads, int n_kv_heads, int head_dim,
+                                        int shared_len, int own_len, size_t *bytes);
+int dattn_decode_shared(const void *Q, const void *K_prefix, const void *V_prefix,
+                        const void *K_cache, const void *V_cache, void *out, int dtype, int batch,
+                        long long q_stride, int n_heads, int n_kv_heads, int head_dim,
+                        int shared_len, int seq_len, const uint32_t *current_pos, void *workspace,
+                        size_t workspace_bytes, dattn_stream_t stream);
+int dattn_decode_shared_paged(const void *Q, const void *K_pages, const void *V_pages, void *out,
+                              int dtype, int batch, long long q_stride, int n_heads, int n_kv_heads,
+                              int head_dim, int page_size, int max_pages, long long num_pages,
+                              const int32_t *block_table, int shared_len,
+                              const uint32_t *current_pos, void *workspace, size_t workspace_bytes,
+                              dattn_stream_t stream);
+
+/*
  * Submission batching: the analogue of the fm_batch_begin / fm_batch_end pair
  * of the C API in Foundry's docs/metal.md (section "Command Batching"), which
  * accumulates operations into one GPU submission.  Here the calls issued on a
@@ -504,8 +581,9 @@ int dattn_decode_paged_q8(const void *Q, const void *K_pages, const void *V_page
  * Calls that may be recorded: dattn_decode_f16_ex, dattn_decode_paged_f16,
  * dattn_decode_f16_noalloc after its first call on the device, dattn_qk_f16,
  * dattn_pv_f16, dattn_rope_append_f16, dattn_rope_append_paged_f16,
- * dattn_softmax_f32, dattn_rope, the q8 calls, and dattn_decode_f16 once its
- * workspace is large enough (a recorded call must not allocate).  Copies the caller issues on the same
+ * dattn_softmax_f32, dattn_rope, the q8 calls, dattn_attend, dattn_decode_shared and
+ * their paged forms, and dattn_decode_f16 once its workspace is large enough (a recorded
+ * call must not allocate).  Copies the caller issues on the same
  * stream meanwhile (cudaMemcpyAsync from pinned host memory, for example) are
  * recorded too.  The shape's plan is made when a call is
  * recorded; make one ordinary call per shape first if its set-up should not
@@ -528,7 +606,7 @@ int dattn_batch_destroy(dattn_batch *batch);
  * here too.  This call synchronises the device and returns DATTN_OK if no
  * kernel has recorded anything since the last clear, DATTN_ERR_TIMEOUT if a
  * wait ran out, DATTN_ERR_BAD_PAGE if a block-table entry was invalid,
- * DATTN_ERR_BAD_POSITION if an append position was outside the cache; it
+ * DATTN_ERR_BAD_POSITION if a new token's position was outside the cache; it
  * resets the word when `clear` is non-zero.
  * Errors: TIMEOUT, BAD_PAGE, BAD_POSITION, CUDA.
  */

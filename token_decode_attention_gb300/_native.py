@@ -92,6 +92,14 @@ _SIGNATURES = {
     "dattn_decode_q8_workspace_bytes": ([_I] * 6 + [ctypes.POINTER(ctypes.c_size_t)], _I),
     "dattn_decode_q8": ([_P] * 6 + [_I] * 7 + [_P, _P, ctypes.c_size_t, _I, _P], _I),
     "dattn_decode_paged_q8": ([_P] * 6 + [_I] * 8 + [_L, _P, _P, _P, ctypes.c_size_t, _I, _P], _I),
+    "dattn_attend_workspace_bytes": ([_I] * 9 + [ctypes.POINTER(ctypes.c_size_t)], _I),
+    "dattn_attend": ([_P] * 4 + [_I, _I, _I, _P, _L] + [_I] * 6 + [_P, _P, ctypes.c_size_t, _P], _I),
+    "dattn_attend_paged": ([_P] * 4 + [_I, _I, _I, _P, _L] + [_I] * 5
+                           + [_L, _P, _I, _I, _P, _P, ctypes.c_size_t, _P], _I),
+    "dattn_decode_shared_workspace_bytes": ([_I] * 6 + [ctypes.POINTER(ctypes.c_size_t)], _I),
+    "dattn_decode_shared": ([_P] * 6 + [_I, _I, _L] + [_I] * 5 + [_P, _P, ctypes.c_size_t, _P], _I),
+    "dattn_decode_shared_paged": ([_P] * 4 + [_I, _I, _L] + [_I] * 5
+                                  + [_L, _P, _I, _P, _P, ctypes.c_size_t, _P], _I),
     "dattn_batch_begin": ([_P], _I),
     "dattn_batch_end": ([_P, ctypes.POINTER(ctypes.c_void_p)], _I),
     "dattn_batch_launch": ([_P, _P], _I),
@@ -1016,3 +1024,233 @@ def decode_paged_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, current_
     head_dim] with scales [num_pages, page_size / scale_block, n_kv_heads]."""
     return _decode_q8(q, k_pages, v_pages, k_scale, v_scale, block_table, current_pos, scale_block,
                       num_partitions, out, workspace, stream, True)
+
+
+# ------------------------------------------- attention over a 16-bit cache
+#
+# As above: an ordinary call is recognised by attribute reads alone.
+
+_BF16 = torch.bfloat16
+
+
+_ATTEND_WORKSPACE: dict[tuple, int] = {}  # the size depends on the shape and the device only
+
+
+def _attend_workspace(query: str, dev: int, *key) -> int:
+    n = _ATTEND_WORKSPACE.get((query, dev, key))
+    if n is None:
+        size = ctypes.c_size_t(0)
+        _check(getattr(load(), query)(*key, ctypes.byref(size)), query)
+        if len(_ATTEND_WORKSPACE) >= 1024:  # a program that never repeats a shape
+            _ATTEND_WORKSPACE.clear()
+        n = _ATTEND_WORKSPACE[query, dev, key] = int(size.value)
+    return n
+
+
+def dattn_attend_workspace_bytes(batch: int, tokens: int, ragged: bool, n_heads: int, n_kv_heads: int,
+                                 head_dim: int, seq_len: int, window: int = 0, sinks: int = 0) -> int:
+    return _attend_workspace("dattn_attend_workspace_bytes", _device(), batch, tokens,
+                             1 if ragged else 0, n_heads, n_kv_heads, head_dim, seq_len, window, sinks)
+
+
+def dattn_decode_shared_workspace_bytes(batch: int, n_heads: int, n_kv_heads: int, head_dim: int,
+                                        shared_len: int, own_len: int) -> int:
+    return _attend_workspace("dattn_decode_shared_workspace_bytes", _device(), batch, n_heads,
+                             n_kv_heads, head_dim, shared_len, own_len)
+
+
+def _attend(name, q, prefix, k, v, block_table, current_pos, token_offsets, shared_len, window, sinks,
+            out, workspace, stream, allocate):
+    """Checks and marshalling of dattn_attend and dattn_decode_shared (`prefix`: a pair of
+    tensors, or `shared_len` positions of the first sequence's pages)."""
+    dev = _device()
+    fresh = out is None and allocate
+    kp, vp = prefix or (None, None)
+    shared = prefix is not None or shared_len is not None
+    try:
+        batch, = current_pos.shape
+        n, h, d = shape = q.shape
+        lead, rows, hk, dc = cache = k.shape
+        dtype = q.dtype
+        qs = h * d
+        ordinary = ((dtype is _F16 or dtype is _BF16) and k.dtype is dtype and v.dtype is dtype
+                    and v.shape == cache and d == dc and q.is_contiguous() and k.is_contiguous()
+                    and v.is_contiguous() and q.get_device() == dev == k.get_device()
+                    and v.get_device() == dev
+                    and not (_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad
+                                                  or not fresh and out.requires_grad
+                                                  or kp is not None and (kp.requires_grad or vp.requires_grad)))
+                    and getattr(_forward_ad, "_current_level", 0) < 0
+                    and (fresh or (out.dtype is dtype and out.shape == shape and out.is_contiguous()
+                                   and out.get_device() == dev))
+                    and current_pos.dtype in _INDEX and current_pos.is_contiguous()
+                    and current_pos.get_device() == dev
+                    and (n == batch if token_offsets is None else
+                         (token_offsets.dtype is torch.int32 and token_offsets.shape == (batch + 1,)
+                          and token_offsets.is_contiguous() and token_offsets.get_device() == dev))
+                    and (lead == batch if block_table is None else
+                         (block_table.dtype is torch.int32 and block_table.ndim == 2
+                          and block_table.shape[0] == batch and block_table.is_contiguous()
+                          and block_table.get_device() == dev))
+                    and (prefix is None or
+                         (kp.dtype is dtype and vp.dtype is dtype and kp.shape == vp.shape
+                          and kp.ndim == 3 and kp.shape[1:] == cache[2:] and kp.is_contiguous()
+                          and vp.is_contiguous() and kp.get_device() == dev == vp.get_device())))
+    except (AttributeError, TypeError, ValueError):
+        ordinary = False
+    if not ordinary:
+        named = {"Q": q, "k_cache": k, "v_cache": v}
+        if prefix is not None:
+            named.update(k_prefix=kp, v_prefix=vp)
+        if not fresh:
+            named["out"] = out
+        _all_tensors(**named, current_pos=current_pos)
+        _no_derivative(**named)
+        dtype = q.dtype
+        if dtype not in (_F16, _BF16):
+            raise TypeError(f"Q must be float16 or bfloat16, got {dtype}")
+        _tokens(q, "Q", dtype)
+        n, h, d = q.shape
+        if k.dim() != 4:
+            raise ValueError("the cache must be [batch, seq_len, n_kv_heads, head_dim] or [num_pages, "
+                             "page_size, n_kv_heads, head_dim]")
+        lead, rows, hk, dc = k.shape
+        if d != dc:
+            raise ValueError(f"Q has head_dim {d}, the cache {dc}")
+        _tensor(k, "K cache", None, dtype)
+        _tensor(v, "V cache", k.shape, dtype)
+        batch = current_pos.shape[0] if current_pos.ndim == 1 else -1
+        _index32(current_pos, "current_pos", (batch,))
+        if block_table is None and lead != batch:
+            raise ValueError(f"the cache holds {lead} sequences, the batch {batch}")
+        named = [("Q", q), ("K cache", k), ("V cache", v), ("current_pos", current_pos)]
+        if token_offsets is not None:
+            _tensor(token_offsets, "token_offsets", (batch + 1,), torch.int32)
+            named.append(("token_offsets", token_offsets))
+        elif n != batch:
+            raise ValueError(f"without token_offsets each sequence brings one token: {n} tokens, "
+                             f"{batch} sequences")
+        if block_table is not None:
+            if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+                raise ValueError("block_table must be [batch, max_pages]")
+            _tensor(block_table, "block_table", (batch, block_table.shape[1]), torch.int32)
+            named.append(("block_table", block_table))
+        if prefix is not None:
+            if kp.dim() != 3:
+                raise ValueError("the prefix must be [shared_len, n_kv_heads, head_dim]")
+            _tensor(kp, "k_prefix", (kp.shape[0], hk, d), dtype)
+            _tensor(vp, "v_prefix", kp.shape, dtype)
+            named += [("k_prefix", kp), ("v_prefix", vp)]
+        if not fresh:
+            _tensor(out, "out", q.shape, dtype)
+            named.append(("out", out))
+        _on_device(named, dev)
+        qs = _token_stride(q)
+    handle = _current_stream(dev, stream)
+    if prefix is not None:
+        shared_len = kp.shape[0]
+    table_pages = 0 if block_table is None else block_table.shape[1]
+    wp, wn = None, 0
+    if workspace is not None:
+        wp = _tensor(workspace, "workspace", None, getattr(workspace, "dtype", None))
+        _on_device((("workspace", workspace),), dev)
+        wn = workspace.numel() * workspace.element_size()
+    elif allocate:
+        capacity = rows * table_pages if table_pages else rows
+        if shared:
+            wn = _attend_workspace("dattn_decode_shared_workspace_bytes", dev, batch, h, hk, d,
+                                   shared_len, capacity)
+        else:
+            wn = _attend_workspace("dattn_attend_workspace_bytes", dev, batch, n,
+                                   0 if token_offsets is None else 1, h, hk, d, capacity, window, sinks)
+    if _RECORDING and handle in _RECORDING and (fresh or (wn and wp is None)) and allocate:
+        raise ValueError(f"a recorded call needs buffers that outlive the batch: pass out and "
+                         f"workspace (dattn_{name}_workspace_bytes)")
+    if wn and wp is None:
+        workspace = _like(k, stream, (wn,), torch.uint8)
+        wp = workspace.data_ptr()
+    if fresh:
+        out = _like(q, stream)
+    kind = 1 if dtype is _F16 else 2
+    lib = load()
+    if shared:
+        if block_table is None:
+            st = lib.dattn_decode_shared(q.data_ptr(), kp.data_ptr(), vp.data_ptr(), k.data_ptr(),
+                                         v.data_ptr(), out.data_ptr(), kind, batch, qs, h, hk, d,
+                                         shared_len, rows, current_pos.data_ptr(), wp, wn, handle)
+        else:
+            st = lib.dattn_decode_shared_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                               kind, batch, qs, h, hk, d, rows, table_pages, lead,
+                                               block_table.data_ptr(), shared_len,
+                                               current_pos.data_ptr(), wp, wn, handle)
+    else:
+        at = None if token_offsets is None else token_offsets.data_ptr()
+        if block_table is None:
+            st = lib.dattn_attend(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), kind, batch,
+                                  n, at, qs, h, hk, d, rows, window, sinks, current_pos.data_ptr(), wp,
+                                  wn, handle)
+        else:
+            st = lib.dattn_attend_paged(q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), kind,
+                                        batch, n, at, qs, h, hk, d, rows, table_pages, lead,
+                                        block_table.data_ptr(), window, sinks, current_pos.data_ptr(),
+                                        wp, wn, handle)
+    if st != OK:
+        _check(st, f"dattn_{name}" if block_table is None else f"dattn_{name}_paged")
+    if not fresh:
+        _written(out)
+    return out
+
+
+def dattn_attend(q, k_cache, v_cache, out, current_pos, window: int = 0, sinks: int = 0,
+                 token_offsets=None, block_table=None, workspace=None, stream=None) -> None:
+    """The dense call, or the paged one when ``block_table`` is given."""
+    _attend("attend", q, None, k_cache, v_cache, block_table, current_pos, token_offsets, None, window,
+            sinks, out, workspace, stream, False)
+
+
+def attend(q, k_cache, v_cache, current_pos, window: int = 0, sinks: int = 0, token_offsets=None,
+           block_table=None, out=None, workspace=None, stream=None):
+    """Attention of q [tokens, n_heads, head_dim] (f16 or bf16) over a cache [batch,
+    seq_len, n_kv_heads, head_dim] of that type (paged when ``block_table`` is given):
+    one token per sequence, or the ragged ``token_offsets`` [batch + 1] of a prompt or a
+    mixed step.  A token sees the positions up to its own, with ``window`` the last
+    ``window`` of them and the first ``sinks``.  ``current_pos`` holds the position of
+    each sequence's last new token, whose row is in the cache already.  Allocates ``out``
+    and the workspace if not given."""
+    return _attend("attend", q, None, k_cache, v_cache, block_table, current_pos, token_offsets, None,
+                   window, sinks, out, workspace, stream, True)
+
+
+def dattn_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, out, current_pos, workspace=None,
+                        stream=None) -> None:
+    _attend("decode_shared", q, (k_prefix, v_prefix), k_cache, v_cache, None, current_pos, None, None, 0,
+            0, out, workspace, stream, False)
+
+
+def dattn_decode_shared_paged(q, k_pages, v_pages, out, block_table, current_pos, shared_len: int,
+                              workspace=None, stream=None) -> None:
+    _attend("decode_shared", q, None, k_pages, v_pages, _table(block_table), current_pos, None, shared_len,
+            0, 0, out, workspace, stream, False)
+
+
+def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, current_pos, out=None, workspace=None,
+                  stream=None):
+    """Decode attention of a batch that shares a prefix [shared_len, n_kv_heads, head_dim],
+    read once for all sequences; the cache [batch, seq_len, n_kv_heads, head_dim] and
+    ``current_pos`` count what follows it.  Allocates ``out`` and the workspace if not given."""
+    return _attend("decode_shared", q, (k_prefix, v_prefix), k_cache, v_cache, None, current_pos, None,
+                   None, 0, 0, out, workspace, stream, True)
+
+
+def decode_shared_paged(q, k_pages, v_pages, block_table, current_pos, shared_len: int, out=None,
+                        workspace=None, stream=None):
+    """Decode attention over a paged cache whose sequences share their first ``shared_len``
+    positions, which are read once, through the first sequence's row of ``block_table``."""
+    return _attend("decode_shared", q, None, k_pages, v_pages, _table(block_table), current_pos, None,
+                   shared_len, 0, 0, out, workspace, stream, True)
+
+
+def _table(block_table):
+    if block_table is None:
+        raise TypeError("block_table must be a torch.Tensor")
+    return block_table

@@ -1,0 +1,163 @@
+// attend_rows.cuh -- what the kernels of attention over a 16-bit cache share: which
+// positions a token sees, where their rows lie, and one query head's attention by a warp.
+//
+// A token at position p sees [0, first) and [lo, p]: lo = max(0, p - window + 1) (0
+// without a window) and first = min(sinks, lo).  The n = first + p + 1 - lo positions it
+// sees are counted through: the i-th is i below `first` and i - first + lo from there on,
+// so the kernels walk what is seen and nothing else.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "dattn_internal.h"
+#include "ptx.cuh"
+
+namespace dattn {
+namespace attend {
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16-bit types: two values of a word to fp32, two fp32 to a word (to nearest).
+template <typename T>
+struct Pair;
+template <>
+struct Pair<__half> {
+    static __device__ __forceinline__ float2 wide(uint32_t w) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+    }
+    static __device__ __forceinline__ uint32_t narrow(float x, float y) {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+template <>
+struct Pair<__nv_bfloat16> {
+    static __device__ __forceinline__ float2 wide(uint32_t w) {
+        return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    }
+    static __device__ __forceinline__ uint32_t narrow(float x, float y) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+
+struct Seen {
+    int first, lo, end;  // [0, first) and [lo, end)
+    __device__ __forceinline__ int count() const { return first + end - lo; }
+    __device__ __forceinline__ int at(int i) const { return i < first ? i : i - first + lo; }
+};
+
+// Positions of sequence b: its last token's, plus one.
+__device__ __forceinline__ int live_end(const AttendArgs &a, int b) {
+    const uint32_t c = __ldg(a.cur_pos + b), top = static_cast<uint32_t>(a.S - a.own_base - 1);
+    return a.own_base + static_cast<int>(c < top ? c : top) + 1;
+}
+
+// What a token at position p sees (nothing at a position before the first).
+__device__ __forceinline__ Seen seen_by(const AttendArgs &a, int p) {
+    Seen v;
+    v.end = max(p + 1, 0);
+    v.lo = a.window > 0 ? max(0, v.end - a.window) : 0;
+    v.first = min(a.sinks, v.lo);
+    return v;
+}
+
+// Row of position pos of sequence b in the cache (or in the tensor of the shared
+// positions, where they have one), in rows of Hk x D elements.  A page outside the pool
+// is recorded and page 0 read in its place.
+__device__ __forceinline__ long long row_of(const AttendArgs &a, int b, int pos) {
+    if (a.block_table == nullptr)
+        return pos < a.own_base ? pos : static_cast<long long>(b) * (a.S - a.own_base) + (pos - a.own_base);
+    const int pi = fast_div(pos, a.div_page);
+    const int owner = pos < a.shared ? 0 : b;
+    int page = __ldg(a.block_table + static_cast<long long>(owner) * a.max_pages + pi);
+    if (page < 0 || page >= a.num_pages) {
+        atomicOr(a.err, kErrPageIndex);
+        page = 0;
+    }
+    return static_cast<long long>(page) * a.page_size + (pos - pi * a.page_size);
+}
+
+// Attention of query head h of token t, of sequence b, over the positions in `v`, by one
+// warp: 32 positions at a time, a lane each for the scores, channel pairs of V over the
+// lanes.  A token that sees nothing gets zeros.
+template <typename T>
+__device__ void attend_row(const AttendArgs &a, int b, long long t, int h, Seen v, int lane) {
+    constexpr unsigned kAll = 0xffffffffu;
+    const T *q = static_cast<const T *>(a.Q) + t * a.q_stride + static_cast<long long>(h) * a.D;
+    T *out = static_cast<T *>(a.out) + (t * a.H + h) * a.D;
+    const long long head = static_cast<long long>(h / a.group) * a.D;
+    const long long row_elems = static_cast<long long>(a.Hk) * a.D;
+    float acc[4][2] = {};
+    float M = -INFINITY, l = 0.f;
+    const int n = v.count();
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        const int i = i0 + lane;
+        float s = -INFINITY;
+        long long at = 0;
+        int apart = 0;
+        if (i < n) {
+            const int pos = v.at(i);
+            apart = a.Kp != nullptr && pos < a.own_base;
+            at = row_of(a, b, pos) * row_elems + head;
+            const T *k = static_cast<const T *>(apart ? a.Kp : a.K) + at;
+            float dot = 0.f;
+            for (int c = 0; c < a.D; c += 8) {
+                const uint4 kw = __ldg(reinterpret_cast<const uint4 *>(k + c));
+                const uint4 qw = __ldg(reinterpret_cast<const uint4 *>(q + c));
+                const uint32_t ks[4] = {kw.x, kw.y, kw.z, kw.w}, qs[4] = {qw.x, qw.y, qw.z, qw.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 x = Pair<T>::wide(ks[e]), y = Pair<T>::wide(qs[e]);
+                    dot = fmaf(x.x, y.x, dot);
+                    dot = fmaf(x.y, y.y, dot);
+                }
+            }
+            s = dot * a.qscale;
+        }
+        float top = s;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
+        const float nm = fmaxf(M, top), ref = nm == -INFINITY ? 0.f : nm;
+        const float f = ex2(M - ref);  // 0 before the first
+        const float p = i < n ? ex2(s - ref) : 0.f;
+        M = nm;
+        l = fmaf(l, f, p);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) acc[c][0] *= f, acc[c][1] *= f;
+        for (int j = 0; j < min(32, n - i0); ++j) {
+            const float w = __shfl_sync(kAll, p, j);
+            const long long row = __shfl_sync(kAll, at, j);
+            const int there = __shfl_sync(kAll, apart, j);
+            const T *vr = static_cast<const T *>(there ? a.Vp : a.V) + row;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const int ch = 2 * (lane + 32 * c);
+                if (ch >= a.D) continue;
+                const float2 x = Pair<T>::wide(__ldg(reinterpret_cast<const uint32_t *>(vr + ch)));
+                acc[c][0] = fmaf(w, x.x, acc[c][0]);
+                acc[c][1] = fmaf(w, x.y, acc[c][1]);
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
+    const float inv = n > 0 ? 1.f / l : 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int ch = 2 * (lane + 32 * c);
+        if (ch < a.D)
+            *reinterpret_cast<uint32_t *>(out + ch) = Pair<T>::narrow(acc[c][0] * inv, acc[c][1] * inv);
+    }
+}
+
+}  // namespace attend
+}  // namespace dattn

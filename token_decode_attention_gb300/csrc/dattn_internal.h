@@ -313,4 +313,30 @@ struct Q8AppendArgs {
 };
 cudaError_t launch_append_q8(const Q8AppendArgs &a, int kv, int sms, cudaStream_t stream);
 
+// Arguments of attention over a 16-bit cache (attend_*.cu).  Positions 0 .. S-1 of a
+// sequence; the `shared` first ones are the same for every sequence, in a tensor of their
+// own (Kp, Vp; the cache then begins at position `own_base` = shared) or through the
+// first sequence's pages (own_base = 0).
+struct AttendArgs {
+    const void *Q;               // [tokens,H,D], tokens q_stride elements apart
+    const void *K, *V;           // [B,S - own_base,Hk,D], or pages [num_pages,page_size,Hk,D]
+    const void *Kp, *Vp;         // [shared,Hk,D] or nullptr
+    void *out;                   // [tokens,H,D]
+    const int *block_table;      // nullptr: dense cache
+    long long num_pages;
+    int page_size, max_pages;
+    FastDiv div_page;
+    const int *offsets;          // [B+1], or nullptr: one token per sequence
+    const uint32_t *cur_pos;     // [B] cache row of each sequence's last token
+    unsigned *err;
+    long long q_stride;
+    int tokens, B, H, Hk, D, S;
+    int group;                   // query heads of a key/value head
+    int shared, own_base;
+    int window;                  // positions that a token sees up to its own; 0: all
+    int sinks;                   // first positions that stay visible
+    float qscale;                // log2(e) / sqrt(D)
+};
+cudaError_t launch_attend(const AttendArgs &a, int dtype, cudaStream_t stream);
+
 }  // namespace dattn
