@@ -6,6 +6,9 @@
 
 #include <algorithm>
 #include <cmath>
+#include <map>
+#include <mutex>
+#include <tuple>
 
 #include "api_checks.h"
 #include "dattn_internal.h"
@@ -47,8 +50,8 @@ int check_shape(const Shape &s) {
         return fail(DATTN_ERR_INVALID_ARG, "window=%d and sinks=%d must not be negative", s.window, s.sinks);
     if (static_cast<double>(s.tokens) * s.n_heads >= 2147483648.0)
         return fail(DATTN_ERR_UNSUPPORTED, "tokens x n_heads must stay below 2^31");
-    if (static_cast<double>(s.n_kv_heads) * s.head_dim >= 2147483648.0)
-        return fail(DATTN_ERR_UNSUPPORTED, "a position must hold fewer than 2^31 elements");
+    if (static_cast<double>(s.n_kv_heads) * s.head_dim >= 1073741824.0)
+        return fail(DATTN_ERR_UNSUPPORTED, "a position must hold fewer than 2^30 elements");
     if (static_cast<double>(s.rows) + (s.apart ? s.shared : 0) >= 2147483648.0 - 1024)
         return fail(DATTN_ERR_UNSUPPORTED, "a sequence must hold fewer than 2^31 - 1024 positions");
     return DATTN_OK;
@@ -76,6 +79,138 @@ int check_apart(const void *out, double out_bytes, const void *p, double bytes, 
     return DATTN_OK;
 }
 
+// ------------------------------------------------------------------- plans
+
+size_t round_up(size_t x, size_t m) { return (x + m - 1) / m * m; }
+
+struct Plan {
+    int dp = 0, slots = 0, smem = 0;
+    dattn::TokenArgs w{};
+    size_t acc_bytes = 0, ws_bytes = 0;
+};
+
+constexpr int kMaxColumns = 16;  // query heads of a key/value head in one CTA
+constexpr int kStaticSmem = 1024;  // the kernel's static shared memory at most
+constexpr size_t kKeptPlans = 1024;  // a program that never repeats a shape starts anew
+
+// One token per sequence, `cap` positions seen at most.  Measured (graph replay, inputs
+// larger than L2 in all), us:
+//  - Key/value heads of a CTA: the fewest of 1, 2, 4 with which all units are resident at
+//    once, as each further wave of CTAs costs its start.  64 sequences of 8 heads, window
+//    4096: 1, 2 heads 128, 119; 222 of 2, 240 positions, 15.7, 14.2; 168 of 16, 128
+//    positions: 1, 2, 4 heads 34.9, 26.8, 23.2.
+//  - Where that leaves most SMs idle, clusters of CTAs share a unit, as many as leave a warp
+//    3/2 tiles on average: one sequence of 8 heads, window 1024 (65 tiles): 4, 8, 16 CTAs
+//    5.9, 5.5, 5.7; 7 sequences of 32 heads, 8 tiles, D = 64: 1, 2 CTAs 3.9, 4.4.
+//  - Up to kClusterTiles tiles a warp the merge in the same launch wins; beyond, chunks that
+//    a second kernel merges: 3/2 as many as are resident for a batch, whose lengths differ
+//    (19 sequences of 4 heads, 295 tiles: clusters of 4 19.5, 6 chunks 18.1), 3/4 for one
+//    sequence (8 heads, 131072 positions: clusters of 16 91.6, chunks for 1/2, 3/4, 1 of
+//    the slots 84.8, 83.0, 86.6).
+constexpr long long kClusterTiles = 16;
+
+int token_plan(const Shape &s, int cap, const dattn::DeviceFacts &df, Plan *p) {
+    dattn::TokenArgs &w = p->w;
+    const int group = s.n_heads / s.n_kv_heads;
+    w.vheads_per_kv = (group + kMaxColumns - 1) / kMaxColumns;
+    while (group % w.vheads_per_kv != 0) ++w.vheads_per_kv;
+    w.gq = group / w.vheads_per_kv;
+    w.div_gq = dattn::fast_div_of(w.gq);
+    w.vheads = s.n_kv_heads * w.vheads_per_kv;
+    w.own_only = s.shared > 0 ? 1 : 0;
+    p->dp = s.head_dim <= 64 ? 64 : s.head_dim <= 128 ? 128 : 256;
+    const long long slots = static_cast<long long>(df.sms) * dattn::token_ctas_per_sm(p->dp);
+    const long long tiles = (static_cast<long long>(cap) + dattn::kTokenTile - 1) / dattn::kTokenTile;
+    int hg = 1;
+    auto units_of = [&](int heads) {
+        return static_cast<long long>(s.batch) * ((w.vheads + heads - 1) / heads);
+    };
+    while (hg < dattn::kTokenWarps && 2 * hg <= w.vheads && units_of(hg) > slots) hg *= 2;
+    const long long units = units_of(hg);
+    w.heads_per_cta = hg;
+    w.head_groups = (w.vheads + hg - 1) / hg;
+    w.phases = dattn::kTokenWarps / hg;
+    auto per_warp = [&](long long C) { return ((tiles + C - 1) / C + w.phases - 1) / w.phases; };
+    long long C = 1;
+    while (C < 16 && units * C * 2 <= slots && 2 * tiles >= 3 * w.phases * C * 2) C *= 2;
+    if (w.own_only && per_warp(1) <= kClusterTiles) C = 1;  // its states are merged in any case
+    const bool chunked = per_warp(C) > kClusterTiles || (w.own_only && C > 1);
+    if (chunked) {
+        C = std::max(1LL, s.batch == 1 ? slots * 3 / 4 / units : slots * 3 / 2 / units);
+        w.chunk_tiles = static_cast<int>(std::max<long long>(4 * w.phases, (tiles + C - 1) / C));
+        C = (tiles + w.chunk_tiles - 1) / w.chunk_tiles;
+    }
+    p->slots = dattn::kTokenSlots;  // a chunk has tiles for all of them
+    p->smem = dattn::token_smem(p->dp, p->slots, w.gq);
+    if (!chunked) {
+        const int nt = w.gq > 8 ? 2 : 1;
+        for (; C > 1; C /= 2) {
+            p->slots = static_cast<int>(std::min<long long>(dattn::kTokenSlots, per_warp(C)));
+            const long long rec = (hg * w.gq * (p->dp / 2) + C - 1) / C * C * 16LL;
+            const long long smem = dattn::token_smem(p->dp, p->slots, w.gq) + rec;
+            if (smem > df.max_smem_optin - kStaticSmem) continue;
+            int fit = 0;
+            if (dattn::attend_token_max_clusters(p->dp, nt, w.gq <= 4, static_cast<int>(smem), static_cast<int>(C),
+                                                 &fit) != cudaSuccess) {
+                cudaGetLastError();  // this cluster size is not available
+                continue;
+            }
+            if (fit < units) continue;
+            p->smem = static_cast<int>(smem);
+            w.cluster = 1;
+            break;
+        }
+        if (C == 1) {
+            p->slots = static_cast<int>(std::min<long long>(dattn::kTokenSlots, per_warp(1)));
+            p->smem = dattn::token_smem(p->dp, p->slots, w.gq);
+        }
+        w.chunk_tiles = static_cast<int>(tiles);
+    }
+    w.ring_bytes = dattn::token_ring_bytes(p->dp, p->slots, w.gq);
+    w.chunks = static_cast<int>(C);
+    if (!w.cluster && (w.chunks > 1 || w.own_only)) {
+        const size_t states = static_cast<size_t>(s.batch) * s.n_heads * w.chunks;
+        p->acc_bytes = round_up(states * s.head_dim * sizeof(float), 256);
+        p->ws_bytes = p->acc_bytes + states * sizeof(float2);
+    }
+    if (units * C > 0x7fffffffLL) return fail(DATTN_ERR_UNSUPPORTED, "batch x n_kv_heads is too large");
+    return DATTN_OK;
+}
+
+int make_plan(const Shape &s, Plan *out) {
+    dattn::DeviceFacts df;
+    if (int st = dattn::device_facts(&df)) return st;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return fail_cuda(e, "cudaGetDevice");
+    const int cap = s.window > 0 && s.window < s.rows
+                        ? static_cast<int>(std::min<long long>(s.rows, static_cast<long long>(s.window) + s.sinks))
+                        : s.rows;
+    using Key = std::tuple<int, int, int, int, int, int, int, int, int>;
+    static std::mutex mutex;
+    static std::map<Key, Plan> plans;
+    static std::map<int, bool> configured;
+    const Key key{dev, s.batch, s.tokens, s.ragged, s.n_heads, s.n_kv_heads, s.head_dim, cap, s.shared};
+    std::lock_guard<std::mutex> lock(mutex);
+    const auto it = plans.find(key);
+    if (it != plans.end()) {
+        *out = it->second;
+        return DATTN_OK;
+    }
+    if (!configured[dev]) {
+        e = dattn::attend_token_configure(df.max_smem_optin);
+        if (e != cudaSuccess) return fail_cuda(e, "cudaFuncSetAttribute(attention kernel)");
+        configured[dev] = true;
+    }
+    Plan p;
+    if (!s.ragged && s.shared == 0)
+        if (int st = token_plan(s, cap, df, &p)) return st;
+    if (plans.size() >= kKeptPlans) plans.clear();
+    plans[key] = p;
+    *out = p;
+    return DATTN_OK;
+}
+
 int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const void *V, void *out, int dtype,
            const Shape &s, long long q_stride, const int32_t *token_offsets, const uint32_t *current_pos,
            void *workspace, size_t workspace_bytes, cudaStream_t stream) {
@@ -98,6 +233,8 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
     if (int st = check_stride(q_stride, q_row, 2, "q_stride")) return st;
     const double rows = s.page_size > 0 ? static_cast<double>(s.num_pages) * s.page_size
                                         : static_cast<double>(s.batch) * s.rows;
+    if (rows >= 2147483648.0)
+        return fail(DATTN_ERR_UNSUPPORTED, "the cache must hold fewer than 2^31 positions in all");
     if (rows * kv_row > 4.0e18 || static_cast<double>(s.tokens) * q_stride > 4.0e18)
         return fail(DATTN_ERR_INVALID_ARG, "the tensors are too large");
     const double out_bytes = 2.0 * s.tokens * q_row, kv_bytes = 2.0 * rows * kv_row;
@@ -108,8 +245,17 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
         if (int st = check_apart(out, out_bytes, Kp, 2.0 * s.shared * kv_row, "K_prefix")) return st;
         if (int st = check_apart(out, out_bytes, Vp, 2.0 * s.shared * kv_row, "V_prefix")) return st;
     }
-    (void)workspace;
-    (void)workspace_bytes;
+    Plan p;
+    if (int st = make_plan(s, &p)) return st;
+    if (p.ws_bytes > 0) {
+        if (workspace == nullptr)
+            return fail(DATTN_ERR_WORKSPACE, "workspace of %zu bytes required, got NULL", p.ws_bytes);
+        if (reinterpret_cast<uintptr_t>(workspace) & 15u)
+            return fail(DATTN_ERR_WORKSPACE, "workspace is not 16-byte aligned");
+        if (workspace_bytes < p.ws_bytes)
+            return fail(DATTN_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu", p.ws_bytes,
+                        workspace_bytes);
+    }
     dattn::DeviceFacts df;
     if (int st = dattn::device_facts(&df)) return st;
     dattn::AttendArgs a{};
@@ -140,14 +286,28 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
     a.window = s.window;
     a.sinks = s.sinks;
     a.qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(s.head_dim)));
-    const cudaError_t e = dattn::launch_attend(a, dtype, stream);
-    return e == cudaSuccess ? DATTN_OK : fail_cuda(e, "attention kernel launch");
+    if (s.ragged || s.shared > 0) {
+        const cudaError_t e = dattn::launch_attend(a, dtype, stream);
+        return e == cudaSuccess ? DATTN_OK : fail_cuda(e, "attention kernel launch");
+    }
+    dattn::TokenArgs w = p.w;
+    w.ws_acc = static_cast<float *>(workspace);
+    w.ws_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p.acc_bytes);
+    cudaError_t e = dattn::launch_attend_token(a, w, dtype, p.dp, p.smem, stream);
+    if (e != cudaSuccess) return fail_cuda(e, "attention kernel launch");
+    if (p.ws_bytes > 0) {
+        e = dattn::launch_attend_merge(a, w, dtype, stream);
+        if (e != cudaSuccess) return fail_cuda(e, "merge kernel launch");
+    }
+    return DATTN_OK;
 }
 
 int workspace_of(const Shape &s, size_t *bytes) {
     if (bytes == nullptr) return fail(DATTN_ERR_INVALID_ARG, "bytes is NULL");
     if (int st = check_shape(s)) return st;
-    *bytes = 0;
+    Plan p;
+    if (int st = make_plan(s, &p)) return st;
+    *bytes = p.ws_bytes;
     return DATTN_OK;
 }
 

@@ -339,4 +339,40 @@ struct AttendArgs {
 };
 cudaError_t launch_attend(const AttendArgs &a, int dtype, cudaStream_t stream);
 
+// One token per sequence (attend_token.cu): warps of a CTA, ring slots of a warp at most
+// (a slot holds K and V of a tile), CTAs of an SM by the row size.  A warp's ring holds no
+// more slots than it has tiles, and the states of its query heads at the end.
+constexpr int kTokenTile = 16;  // positions
+constexpr int kTokenWarps = 4, kTokenSlots = 3;
+__host__ __device__ constexpr int token_ctas_per_sm(int dp) { return 256 / dp; }
+__host__ __device__ constexpr int token_ring_bytes(int dp, int slots, int gq) {
+    const int ring = slots * 2 * kTokenTile * dp * 2, states = (gq * (dp + 4) * 4 + 127) / 128 * 128;
+    return ring > states ? ring : states;
+}
+__host__ __device__ constexpr int token_smem(int dp, int slots, int gq) {
+    return kTokenWarps * token_ring_bytes(dp, slots, gq);
+}
+// A virtual head is a group of gq query heads of one key/value head (a key/value head has
+// vheads_per_kv of them); units are (sequence, heads_per_cta virtual heads).
+struct TokenArgs {
+    float *ws_acc;      // [B,H,chunks,D] states of the chunks of units of several
+    float2 *ws_ml;      // [B,H,chunks]   (running max, log2 units; sum)
+    int gq, vheads, vheads_per_kv;
+    FastDiv div_gq;
+    int heads_per_cta;
+    int head_groups;
+    int phases;         // warps that share a virtual head
+    int chunks;         // CTAs of a unit
+    int chunk_tiles;    // tiles of a chunk (not of a cluster's: equal runs of what is seen)
+    int cluster;        // the chunks of a unit are a cluster and merge in shared memory
+    int ring_bytes;     // a warp's ring
+    int own_only;       // the shared positions are left out and every chunk leaves its state
+};
+cudaError_t attend_token_configure(int max_smem);
+cudaError_t attend_token_max_clusters(int dp, int nt, bool pair, int smem, int cluster, int *clusters);
+cudaError_t launch_attend_token(const AttendArgs &a, const TokenArgs &w, int dtype, int dp, int smem,
+                                cudaStream_t stream);
+// Merge of the chunks' states into `out`.
+cudaError_t launch_attend_merge(const AttendArgs &a, const TokenArgs &w, int dtype, cudaStream_t stream);
+
 }  // namespace dattn
