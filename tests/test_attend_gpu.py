@@ -327,12 +327,11 @@ def test_captured_and_recorded_calls(i):
     assert torch.equal(out.cpu(), first)
 
     stream = torch.cuda.Stream()
+    ws = torch.empty(max(workspace_bytes(c), 16), dtype=torch.uint8, device="cuda")
     dattn.dattn_batch_begin(stream)
     try:
         with pytest.raises(ValueError, match="outlive"):
             c.call(d, stream=stream)
-        n = workspace_bytes(c)
-        ws = torch.empty(max(n, 16), dtype=torch.uint8, device="cuda")
         c.call(d, out=out, workspace=ws, stream=stream)
     finally:
         batch = dattn.dattn_batch_end(stream)

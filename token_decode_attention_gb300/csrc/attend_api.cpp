@@ -9,6 +9,7 @@
 #include <map>
 #include <mutex>
 #include <tuple>
+#include <type_traits>
 
 #include "api_checks.h"
 #include "dattn_internal.h"
@@ -85,8 +86,19 @@ size_t round_up(size_t x, size_t m) { return (x + m - 1) / m * m; }
 
 struct Plan {
     int dp = 0, slots = 0, smem = 0;
+    bool tiles = false, token = false;  // which kernels run
     dattn::TokenArgs w{};
-    size_t acc_bytes = 0, ws_bytes = 0;
+    dattn::TileArgs t{};
+    size_t ws_bytes = 0;
+    // where the parts of the workspace begin
+    size_t ws_acc = 0, ws_ml = 0, t_plan = 0, t_items = 0, t_before = 0, t_seq = 0, t_acc = 0, t_ml = 0,
+           t_whole_acc = 0, t_whole_ml = 0;
+
+    size_t take(size_t bytes) {
+        const size_t at = ws_bytes;
+        ws_bytes = at + round_up(bytes, 256);
+        return at;
+    }
 };
 
 constexpr int kMaxColumns = 16;  // query heads of a key/value head in one CTA
@@ -118,7 +130,7 @@ int token_plan(const Shape &s, int cap, const dattn::DeviceFacts &df, Plan *p) {
     w.div_gq = dattn::fast_div_of(w.gq);
     w.vheads = s.n_kv_heads * w.vheads_per_kv;
     w.own_only = s.shared > 0 ? 1 : 0;
-    p->dp = s.head_dim <= 64 ? 64 : s.head_dim <= 128 ? 128 : 256;
+    p->token = true;
     const long long slots = static_cast<long long>(df.sms) * dattn::token_ctas_per_sm(p->dp);
     const long long tiles = (static_cast<long long>(cap) + dattn::kTokenTile - 1) / dattn::kTokenTile;
     int hg = 1;
@@ -170,10 +182,41 @@ int token_plan(const Shape &s, int cap, const dattn::DeviceFacts &df, Plan *p) {
     w.chunks = static_cast<int>(C);
     if (!w.cluster && (w.chunks > 1 || w.own_only)) {
         const size_t states = static_cast<size_t>(s.batch) * s.n_heads * w.chunks;
-        p->acc_bytes = round_up(states * s.head_dim * sizeof(float), 256);
-        p->ws_bytes = p->acc_bytes + states * sizeof(float2);
+        p->ws_acc = p->take(states * s.head_dim * sizeof(float));
+        p->ws_ml = p->take(states * sizeof(float2));
     }
     if (units * C > 0x7fffffffLL) return fail(DATTN_ERR_UNSUPPORTED, "batch x n_kv_heads is too large");
+    return DATTN_OK;
+}
+
+// Many tokens (or the shared positions), `cap` positions seen at most by one token.
+int tiles_plan(const Shape &s, int cap, const dattn::DeviceFacts &df, Plan *p) {
+    dattn::TileArgs &t = p->t;
+    const int group = s.n_heads / s.n_kv_heads, rows = dattn::tile_rows(p->dp), keys = dattn::tile_keys(p->dp);
+    const long long all_rows = static_cast<long long>(s.tokens) * group;
+    p->tiles = true;
+    t.div_group = dattn::fast_div_of(group);
+    t.bound_ends = s.shared > 0 && !s.apart ? 1 : 0;
+    const long long items = (all_rows + rows - 1) / rows + (s.ragged ? s.batch : 0);
+    if (items > 0x7fffff00LL) return fail(DATTN_ERR_UNSUPPORTED, "the batch is too large");
+    t.max_items = static_cast<int>(items);
+    // key tiles of an item at most: what its first token sees and the tokens behind it
+    const long long seen = s.shared > 0 ? s.shared : std::min<long long>(s.rows, static_cast<long long>(cap) + rows);
+    const double units = static_cast<double>(items) * s.n_kv_heads * ((seen + keys - 1) / keys + 1);
+    if (units * 1024.0 > 4.0e18) return fail(DATTN_ERR_UNSUPPORTED, "the batch is too large");
+    t.ctas = static_cast<int>(std::max(1.0, std::min<double>(df.sms, units / dattn::kTileMinUnits)));
+    if (s.ragged) {
+        p->t_plan = p->take(sizeof(dattn::TilePlan));
+        p->t_items = p->take(sizeof(dattn::TileItem) * items);
+        p->t_before = p->take(sizeof(long long) * (items + 1));
+        p->t_seq = p->take(sizeof(int) * (static_cast<size_t>(s.batch) + 1));
+    } else {
+        const size_t states = static_cast<size_t>(s.batch) * s.n_heads;
+        p->t_whole_acc = p->take(states * s.head_dim * sizeof(float));
+        p->t_whole_ml = p->take(states * sizeof(float2));
+    }
+    p->t_acc = p->take(2 * static_cast<size_t>(t.ctas) * rows * s.head_dim * sizeof(float));
+    p->t_ml = p->take(2 * static_cast<size_t>(t.ctas) * rows * sizeof(float2));
     return DATTN_OK;
 }
 
@@ -186,11 +229,12 @@ int make_plan(const Shape &s, Plan *out) {
     const int cap = s.window > 0 && s.window < s.rows
                         ? static_cast<int>(std::min<long long>(s.rows, static_cast<long long>(s.window) + s.sinks))
                         : s.rows;
-    using Key = std::tuple<int, int, int, int, int, int, int, int, int>;
+    using Key = std::tuple<int, int, int, bool, int, int, int, int, int, bool>;
     static std::mutex mutex;
     static std::map<Key, Plan> plans;
     static std::map<int, bool> configured;
-    const Key key{dev, s.batch, s.tokens, s.ragged, s.n_heads, s.n_kv_heads, s.head_dim, cap, s.shared};
+    const Key key{dev, s.batch, s.tokens, s.ragged, s.n_heads, s.n_kv_heads, s.head_dim, cap,
+                  s.shared, s.apart};
     std::lock_guard<std::mutex> lock(mutex);
     const auto it = plans.find(key);
     if (it != plans.end()) {
@@ -199,11 +243,15 @@ int make_plan(const Shape &s, Plan *out) {
     }
     if (!configured[dev]) {
         e = dattn::attend_token_configure(df.max_smem_optin);
+        if (e == cudaSuccess) e = dattn::attend_tiles_configure(df.max_smem_optin);
         if (e != cudaSuccess) return fail_cuda(e, "cudaFuncSetAttribute(attention kernel)");
         configured[dev] = true;
     }
     Plan p;
-    if (!s.ragged && s.shared == 0)
+    p.dp = s.head_dim <= 64 ? 64 : s.head_dim <= 128 ? 128 : 256;
+    if (s.ragged || s.shared > 0)
+        if (int st = tiles_plan(s, cap, df, &p)) return st;
+    if (!s.ragged)
         if (int st = token_plan(s, cap, df, &p)) return st;
     if (plans.size() >= kKeptPlans) plans.clear();
     plans[key] = p;
@@ -286,18 +334,40 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
     a.window = s.window;
     a.sinks = s.sinks;
     a.qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(s.head_dim)));
-    if (s.ragged || s.shared > 0) {
-        const cudaError_t e = dattn::launch_attend(a, dtype, stream);
-        return e == cudaSuccess ? DATTN_OK : fail_cuda(e, "attention kernel launch");
-    }
+    char *const ws = static_cast<char *>(workspace);
+    auto at = [&](size_t offset, auto *&part) {
+        part = reinterpret_cast<std::remove_reference_t<decltype(part)>>(ws + offset);
+    };
     dattn::TokenArgs w = p.w;
-    w.ws_acc = static_cast<float *>(workspace);
-    w.ws_ml = reinterpret_cast<float2 *>(static_cast<char *>(workspace) + p.acc_bytes);
-    cudaError_t e = dattn::launch_attend_token(a, w, dtype, p.dp, p.smem, stream);
-    if (e != cudaSuccess) return fail_cuda(e, "attention kernel launch");
-    if (p.ws_bytes > 0) {
-        e = dattn::launch_attend_merge(a, w, dtype, stream);
-        if (e != cudaSuccess) return fail_cuda(e, "merge kernel launch");
+    dattn::TileArgs t = p.t;
+    cudaError_t e = cudaSuccess;
+    if (p.tiles) {
+        if (s.ragged) {
+            at(p.t_plan, t.plan);
+            at(p.t_items, t.items);
+            at(p.t_before, t.before);
+            at(p.t_seq, t.seq_items);
+        } else {
+            at(p.t_whole_acc, t.whole_acc);
+            at(p.t_whole_ml, t.whole_ml);
+        }
+        at(p.t_acc, t.acc);
+        at(p.t_ml, t.ml);
+        e = dattn::launch_attend_tiles(a, t, dtype, p.dp, stream);
+        if (e != cudaSuccess) return fail_cuda(e, "attention kernel launch");
+    }
+    if (p.token) {
+        const bool states = !w.cluster && (w.chunks > 1 || w.own_only);
+        if (states) {
+            at(p.ws_acc, w.ws_acc);
+            at(p.ws_ml, w.ws_ml);
+        }
+        e = dattn::launch_attend_token(a, w, dtype, p.dp, p.smem, stream);
+        if (e != cudaSuccess) return fail_cuda(e, "attention kernel launch");
+        if (states) {
+            e = dattn::launch_attend_merge(a, w, p.tiles ? &t : nullptr, dtype, p.dp, stream);
+            if (e != cudaSuccess) return fail_cuda(e, "merge kernel launch");
+        }
     }
     return DATTN_OK;
 }

@@ -1,9 +1,10 @@
 // attend_merge.cu -- the states of a query head's chunks into its output:
 //   out = sum_j 2^(m_j - M) acc_j / sum_j 2^(m_j - M) l_j,   M = max_j m_j,
 // m_j the chunk's running maximum (log2 units), l_j and acc_j its sums, in the chunks'
-// order.  One warp a query head, or four that take the chunks in turn where there are
+// order, after those of the shared positions where there are such (attend_tiles.cuh; a
+// piece or several).  One warp a query head, or four that take the chunks in turn where there are
 // many; lanes hold four channels each.
-#include "attend_rows.cuh"
+#include "attend_tiles.cuh"
 
 namespace dattn {
 namespace {
@@ -15,7 +16,8 @@ constexpr unsigned kFull = 0xffffffffu;
 constexpr int kWarps = 4;
 
 template <typename T, int WPR>
-__global__ void __launch_bounds__(kWarps * 32) merge_kernel(const AttendArgs a, const TokenArgs w) {
+__global__ void __launch_bounds__(kWarps * 32) merge_kernel(const AttendArgs a, const TokenArgs w,
+                                                           const TileArgs t, int dp) {
     __shared__ float4 s_acc[WPR > 1 ? kWarps : 1][64];
     __shared__ float s_l[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % WPR;
@@ -28,24 +30,52 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const AttendArgs a, 
     if (w.own_only) v.lo = min(a.shared, v.end);
     const int tiles = (v.count() + kTokenTile - 1) / kTokenTile;
     const int n = max(1, (tiles + w.chunk_tiles - 1) / w.chunk_tiles);
+    // state q: of the shared positions for q < pieces, then of the sequence's own
     const float2 *ml = w.ws_ml + row * w.chunks;
     const float *acc = w.ws_acc + row * w.chunks * a.D;
+    int pieces = 0, c0 = 0, r = 0;
+    bool whole = false;
+    if (w.own_only) {
+        const attend::Shares s = attend::shares_of(a, t, dp);
+        const int h = static_cast<int>(row - static_cast<long long>(b) * a.H);
+        const int kvh = fast_div(h, t.div_group);
+        const int rr = b * a.group + (h - kvh * a.group), item = rr / tile_rows(dp);
+        r = rr - item * tile_rows(dp);
+        const int2 who = attend::holders(s, kvh, attend::units_before(t, s, item),
+                                         attend::units_before(t, s, item + 1));
+        c0 = who.x;
+        pieces = who.y - who.x + 1;
+        whole = pieces == 1;
+    }
+    auto slot = [&](int q) {
+        return static_cast<long long>(2 * (c0 + q) + (q == 0 ? 1 : 0)) * tile_rows(dp) + r;
+    };
+    auto ml_of = [&](int q) {
+        if (q >= pieces) return ml[q - pieces];
+        return whole ? t.whole_ml[row] : t.ml[slot(q)];
+    };
+    auto acc_of = [&](int q) -> const float * {
+        if (q >= pieces) return acc + static_cast<long long>(q - pieces) * a.D;
+        return whole ? t.whole_acc + row * a.D : t.acc + slot(q) * a.D;
+    };
+    const int states = pieces + n;
     float top = -INFINITY;
-    for (int q = lane; q < n; q += 32) top = fmaxf(top, ml[q].x);
+    for (int q = lane; q < states; q += 32) top = fmaxf(top, ml_of(q).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFull, top, o));
     float4 y[2] = {};
     float l = 0.f;
 #pragma unroll 4
-    for (int q = sub; q < n; q += WPR) {
-        const float2 x = ml[q];
+    for (int q = sub; q < states; q += WPR) {
+        const float2 x = ml_of(q);
+        const float *from = acc_of(q);
         const float f = x.x == -INFINITY ? 0.f : ex2(x.x - top);
         l = fmaf(f, x.y, l);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
             const int ch = 4 * lane + 128 * j;
             if (ch >= a.D) continue;
-            const float4 z = *reinterpret_cast<const float4 *>(acc + static_cast<long long>(q) * a.D + ch);
+            const float4 z = *reinterpret_cast<const float4 *>(from + ch);
             y[j].x = fmaf(f, z.x, y[j].x);
             y[j].y = fmaf(f, z.y, y[j].y);
             y[j].z = fmaf(f, z.z, y[j].z);
@@ -79,9 +109,9 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const AttendArgs a, 
 }
 
 template <typename T>
-cudaError_t launch(const AttendArgs &a, const TokenArgs &w, cudaStream_t stream) {
+cudaError_t launch(const AttendArgs &a, const TokenArgs &w, const TileArgs &t, int dp, cudaStream_t stream) {
     const long long rows = static_cast<long long>(a.B) * a.H;
-    const bool many = w.chunks > 8;
+    const bool many = w.chunks > 8 || (w.own_only && t.ctas > 8);
     const long long blocks = many ? rows : (rows + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};
@@ -93,14 +123,17 @@ cudaError_t launch(const AttendArgs &a, const TokenArgs &w, cudaStream_t stream)
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return many ? cudaLaunchKernelEx(&cfg, merge_kernel<T, kWarps>, a, w)
-                : cudaLaunchKernelEx(&cfg, merge_kernel<T, 1>, a, w);
+    return many ? cudaLaunchKernelEx(&cfg, merge_kernel<T, kWarps>, a, w, t, dp)
+                : cudaLaunchKernelEx(&cfg, merge_kernel<T, 1>, a, w, t, dp);
 }
 
 }  // namespace
 
-cudaError_t launch_attend_merge(const AttendArgs &a, const TokenArgs &w, int dtype, cudaStream_t stream) {
-    return dtype == kDtypeF16 ? launch<__half>(a, w, stream) : launch<__nv_bfloat16>(a, w, stream);
+cudaError_t launch_attend_merge(const AttendArgs &a, const TokenArgs &w, const TileArgs *t, int dtype, int dp,
+                                cudaStream_t stream) {
+    const TileArgs tiles = t != nullptr ? *t : TileArgs{};
+    return dtype == kDtypeF16 ? launch<__half>(a, w, tiles, dp, stream)
+                              : launch<__nv_bfloat16>(a, w, tiles, dp, stream);
 }
 
 }  // namespace dattn

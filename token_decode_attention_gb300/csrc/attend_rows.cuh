@@ -86,26 +86,31 @@ __device__ __forceinline__ long long row_of(const AttendArgs &a, int b, int pos)
     return static_cast<long long>(page) * a.page_size + (pos - pi * a.page_size);
 }
 
-// Attention of query head h of token t, of sequence b, over the positions in `v`, by one
-// warp: 32 positions at a time, a lane each for the scores, channel pairs of V over the
-// lanes.  A token that sees nothing gets zeros.
+// State of one query head over the positions counted i0 .. i1-1 of `v` (those of a group
+// of tokens) that its own token, which sees [0, sinks) and [lo, end), sees too: running
+// maximum (log2 units), sum of weights and weighted values of channels 2 (lane + 32 c), by
+// one warp, 32 positions at a time: a lane each for the scores, channels over the lanes for V.
+struct RowState {
+    float M, l, acc[4][2];
+};
 template <typename T>
-__device__ void attend_row(const AttendArgs &a, int b, long long t, int h, Seen v, int lane) {
+__device__ void row_state(const AttendArgs &a, int b, int kvh, const T *q, Seen v, int i0, int i1, int lo, int end,
+                          int lane, RowState &r) {
     constexpr unsigned kAll = 0xffffffffu;
-    const T *q = static_cast<const T *>(a.Q) + t * a.q_stride + static_cast<long long>(h) * a.D;
-    T *out = static_cast<T *>(a.out) + (t * a.H + h) * a.D;
-    const long long head = static_cast<long long>(h / a.group) * a.D;
+    const long long head = static_cast<long long>(kvh) * a.D;
     const long long row_elems = static_cast<long long>(a.Hk) * a.D;
-    float acc[4][2] = {};
-    float M = -INFINITY, l = 0.f;
-    const int n = v.count();
-    for (int i0 = 0; i0 < n; i0 += 32) {
+    r.M = -INFINITY;
+    r.l = 0.f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) r.acc[c][0] = r.acc[c][1] = 0.f;
+    for (; i0 < i1; i0 += 32) {
         const int i = i0 + lane;
+        const int pos = v.at(i);
+        const bool sees = i < i1 && pos < end && (pos >= lo || pos < a.sinks);
         float s = -INFINITY;
         long long at = 0;
         int apart = 0;
-        if (i < n) {
-            const int pos = v.at(i);
+        if (sees) {
             apart = a.Kp != nullptr && pos < a.own_base;
             at = row_of(a, b, pos) * row_elems + head;
             const T *k = static_cast<const T *>(apart ? a.Kp : a.K) + at;
@@ -123,17 +128,19 @@ __device__ void attend_row(const AttendArgs &a, int b, long long t, int h, Seen 
             }
             s = dot * a.qscale;
         }
+        const unsigned who = __ballot_sync(kAll, sees);
         float top = s;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kAll, top, o));
-        const float nm = fmaxf(M, top), ref = nm == -INFINITY ? 0.f : nm;
-        const float f = ex2(M - ref);  // 0 before the first
-        const float p = i < n ? ex2(s - ref) : 0.f;
-        M = nm;
-        l = fmaf(l, f, p);
+        const float nm = fmaxf(r.M, top), ref = nm == -INFINITY ? 0.f : nm;
+        const float f = ex2(r.M - ref);  // 0 before the first
+        const float p = sees ? ex2(s - ref) : 0.f;
+        r.M = nm;
+        r.l = fmaf(r.l, f, p);
 #pragma unroll
-        for (int c = 0; c < 4; ++c) acc[c][0] *= f, acc[c][1] *= f;
-        for (int j = 0; j < min(32, n - i0); ++j) {
+        for (int c = 0; c < 4; ++c) r.acc[c][0] *= f, r.acc[c][1] *= f;
+        for (unsigned left = who; left != 0; left &= left - 1) {
+            const int j = __ffs(left) - 1;
             const float w = __shfl_sync(kAll, p, j);
             const long long row = __shfl_sync(kAll, at, j);
             const int there = __shfl_sync(kAll, apart, j);
@@ -143,20 +150,13 @@ __device__ void attend_row(const AttendArgs &a, int b, long long t, int h, Seen 
                 const int ch = 2 * (lane + 32 * c);
                 if (ch >= a.D) continue;
                 const float2 x = Pair<T>::wide(__ldg(reinterpret_cast<const uint32_t *>(vr + ch)));
-                acc[c][0] = fmaf(w, x.x, acc[c][0]);
-                acc[c][1] = fmaf(w, x.y, acc[c][1]);
+                r.acc[c][0] = fmaf(w, x.x, r.acc[c][0]);
+                r.acc[c][1] = fmaf(w, x.y, r.acc[c][1]);
             }
         }
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(kAll, l, o);
-    const float inv = n > 0 ? 1.f / l : 0.f;
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int ch = 2 * (lane + 32 * c);
-        if (ch < a.D)
-            *reinterpret_cast<uint32_t *>(out + ch) = Pair<T>::narrow(acc[c][0] * inv, acc[c][1] * inv);
-    }
+    for (int o = 16; o > 0; o >>= 1) r.l += __shfl_xor_sync(kAll, r.l, o);
 }
 
 }  // namespace attend

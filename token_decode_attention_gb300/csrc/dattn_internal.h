@@ -337,8 +337,6 @@ struct AttendArgs {
     int sinks;                   // first positions that stay visible
     float qscale;                // log2(e) / sqrt(D)
 };
-cudaError_t launch_attend(const AttendArgs &a, int dtype, cudaStream_t stream);
-
 // One token per sequence (attend_token.cu): warps of a CTA, ring slots of a warp at most
 // (a slot holds K and V of a tile), CTAs of an SM by the row size.  A warp's ring holds no
 // more slots than it has tiles, and the states of its query heads at the end.
@@ -372,7 +370,48 @@ cudaError_t attend_token_configure(int max_smem);
 cudaError_t attend_token_max_clusters(int dp, int nt, bool pair, int smem, int cluster, int *clusters);
 cudaError_t launch_attend_token(const AttendArgs &a, const TokenArgs &w, int dtype, int dp, int smem,
                                 cudaStream_t stream);
-// Merge of the chunks' states into `out`.
-cudaError_t launch_attend_merge(const AttendArgs &a, const TokenArgs &w, int dtype, cudaStream_t stream);
+
+// Many tokens at a time (attend_tiles.cu): query rows are a sequence's tokens times the
+// query heads of a key/value head, cut into items of tile_rows(dp), each over the
+// key tiles that one of its tokens sees.
+__host__ __device__ constexpr int tile_stacks(int dp) { return dp <= 128 ? 2 : 1; }  // of 128 rows
+__host__ __device__ constexpr int tile_rows(int dp) { return 128 * tile_stacks(dp); }
+__host__ __device__ constexpr int tile_keys(int dp) { return dp <= 128 ? 128 : 64; }
+constexpr int kTileMinUnits = 4;  // key tiles (and what an item adds) of a CTA, of which there are
+                                  // fewer for less work
+// Items of one key/value head (the same for each).
+struct TileItem {
+    int b, token;     // sequence, first row's token
+    int head, rows;   // first row's query head within the group, rows
+    int p0;           // first token's position
+    int lo, first;    // positions that some row sees: [0, first) and [lo, first + ...), n in all
+    int n;
+};
+// What the planning kernel leaves ahead of the items.
+struct TilePlan {
+    long long total;  // key tiles of the items of one key/value head, and what an item adds
+    int items;
+    int ctas;         // CTAs that share them
+};
+struct TileArgs {
+    TilePlan *plan;          // nullptr: rows of all sequences over the shared positions
+    TileItem *items;
+    long long *before;       // [items + 1] tiles (and what an item adds) ahead of each item
+    int *seq_items;          // [B + 1] items ahead of each sequence
+    int max_items;
+    float *acc;              // [2 ctas, tile_rows, D] states of pieces of items
+    float2 *ml;              // [2 ctas, tile_rows]
+    float *whole_acc;        // shared: [B,H,D] states of items that one CTA held
+    float2 *whole_ml;        // shared: [B,H]
+    FastDiv div_group;
+    int ctas;                // CTAs at most
+    int bound_ends;          // shared: a token may lie inside the shared positions
+};
+cudaError_t attend_tiles_configure(int max_smem);
+cudaError_t launch_attend_tiles(const AttendArgs &a, const TileArgs &t, int dtype, int dp, cudaStream_t stream);
+
+// Merge of the chunks' states into `out`, with those of the shared positions where `t` is given.
+cudaError_t launch_attend_merge(const AttendArgs &a, const TokenArgs &w, const TileArgs *t, int dtype, int dp,
+                                cudaStream_t stream);
 
 }  // namespace dattn
