@@ -41,6 +41,7 @@ using attend::Seen;
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kSoftmaxThreads = 128;  // of a stack
 constexpr int kLoadWarps = 3, kThreads = 384;
+constexpr unsigned kNoRow = 0xffffffffu;  // zeros (a cache has fewer than 2^31 rows)
 // The running maximum M is kept kHeadroom (log2) below the largest exponent when it was set
 // and moved when one exceeds M + kTrigger: weights lie below 2^12 (f16 holds up to 65504)
 // and the largest is at least 2^4, which keeps f16 weights normal down to 2^-18 of it.
@@ -61,6 +62,41 @@ struct TileShape {
 // Byte offset of 16-byte chunk c of row r in a tile of blocks of `rows` rows.
 __device__ __forceinline__ uint32_t swizzled(int rows, int r, int c) {
     return (c >> 3) * (rows * 128) + r * 128 + (((c ^ r) & 7) << 4);
+}
+
+// Pairs of fp32 in one instruction; the largest of three (NaN left aside).
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    unsigned long long x, y, z, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(z) : "f"(c.x), "f"(c.y));
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(x), "l"(y), "l"(z));
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(r));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    unsigned long long x, y, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(x) : "f"(a.x), "f"(a.y));
+    asm("mov.b64 %0, {%1, %2};" : "=l"(y) : "f"(b.x), "f"(b.y));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(y));
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(r));
+    return d;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
 }
 
 // Whether a word holds a 16-bit value whose exponent is all ones.
@@ -121,10 +157,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
     if (warp == 11) tc::alloc(&s_tmem);
     if (tid == 0) {
         for (int i = 0; i < Z::kSlots; ++i) {
-            mbar_init(kv_full + i, kLoadWarps);
+            mbar_init(kv_full + i, kLoadWarps * 32);
             mbar_init(kv_free + i, 1);
         }
-        mbar_init(q_full, kLoadWarps);
+        mbar_init(q_full, kLoadWarps * 32);
         mbar_init(q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_two + i, 1);
@@ -172,6 +208,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
         return x1 > all.end || (x0 < all.lo && x1 > all.sinks);
     };
 
+    // A softmax thread holds a row's scores of a tile; the registers come from the others:
+    // 256 x 200 + 128 x 104 = 384 x 168, what the launch gave.
+    if (warp < 8)
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    else
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
     if (warp < 8) {
         // ------------------------------------------------------------ softmax
         const int stack = warp >> 2, row = tid & 127;
@@ -218,8 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                 }
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int c = 0; c < kKeys; ++c) m4[c & 3] = fmaxf(m4[c & 3], __uint_as_float(sv[c]));
-                const float top = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * a.qscale;
+                for (int c = 0; c < kKeys; c += 2)
+                    m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
+                const float top = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * a.qscale;
                 // With one stack the last product with V may still run, with two it is done:
                 // this S was issued behind it.
                 bool running = stacks == 1 && n > 0;
@@ -251,16 +294,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     }
                 }
                 const float ref = M == -INFINITY ? 0.f : M;
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                const float2 scale2 = make_float2(a.qscale, a.qscale), ref2 = make_float2(-ref, -ref);
+                float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int c = 0; c < kKeys; c += 2) {
-                    const float p0 = ex2(fmaf(__uint_as_float(sv[c]), a.qscale, -ref));
-                    const float p1 = ex2(fmaf(__uint_as_float(sv[c + 1]), a.qscale, -ref));
-                    l4[c & 2] += p0;
-                    l4[(c & 2) + 1] += p1;
-                    sv[c / 2] = Pair<T>::narrow(p0, p1);
+                    float2 p = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), scale2, ref2);
+                    p.x = ex2(p.x);
+                    p.y = ex2(p.y);
+                    l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], p);
+                    sv[c / 2] = Pair<T>::narrow(p.x, p.y);
                 }
-                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                l2[0] = add2(l2[0], l2[1]);
+                l += l2[0].x + l2[0].y;
 #pragma unroll
                 for (int c = 0; c < kKeys / 2; c += 32) tc::st32(col_s + c, sv + c);
                 tc::wait_st();
@@ -359,12 +404,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
         constexpr int CPR = DP / 8;              // of a full row
         constexpr int kLanesRow = CPR < 32 ? CPR : 32, kRowsCopy = 32 / kLanesRow;
         const int crow = lane / kLanesRow, cc = lane % kLanesRow;
-        // Groups of copies under way, oldest first: the barrier of each, and the slot of a V
-        // tile to look through (-1: none).
-        constexpr int kLag = 2;
-        uint64_t *pend_bar[kLag + 1];
-        int pend_look[kLag + 1];
-        int pending = 0, number = 0;
+        int number = 0;
+        bool ok = true;
+        // Whether this lane's own copies of a tile hold a value that is not finite.
         auto look_through = [&](int slot) {
             const uint32_t base = ring + slot * Z::kSlotBytes;
             uint32_t any = 0;
@@ -372,78 +414,33 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
 #pragma unroll 4
                 for (int i = 0; i < 16 / kRowsCopy; ++i) {
                     if (cc >= chunks) continue;
-                    const uint32_t at = base + swizzled(kKeys, g * 16 + i * kRowsCopy + crow, cc);
-                    uint32_t w0, w1, w2, w3;
-                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(w0), "=r"(w1), "=r"(w2), "=r"(w3) : "r"(at) : "memory");
-                    any |= not_finite<T>(w0) | not_finite<T>(w1) | not_finite<T>(w2) | not_finite<T>(w3);
+                    const uint4 w = lds128(base + swizzled(kKeys, g * 16 + i * kRowsCopy + crow, cc));
+                    any |= not_finite<T>(w.x) | not_finite<T>(w.y) | not_finite<T>(w.z) | not_finite<T>(w.w);
                 }
             return any != 0;
         };
-        int bad_number = 0;
-        auto hand_over = [&]() {  // the oldest group, whose copies are done
-            if (pend_look[0] >= 0 && look_through(pend_look[0])) {
-                *const_cast<volatile int *>(&s_bad[bad_number & 3]) = bad_number;
-                __threadfence_block();
-            }
-            tc::fence_async();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(pend_bar[0]);
-#pragma unroll
-            for (int i = 0; i < kLag; ++i) {
-                pend_bar[i] = pend_bar[i + 1];
-                pend_look[i] = pend_look[i + 1];
-            }
-            --pending;
-        };
-        auto flush = [&]() {
-            cp_async_wait<0>();
-            while (pending > 0) hand_over();
-        };
-        auto push = [&](uint64_t *bar, int look) {
-            cp_async_commit();
-#pragma unroll
-            for (int i = 0; i <= kLag; ++i)
-                if (i == pending) {
-                    pend_bar[i] = bar;
-                    pend_look[i] = look;
-                }
-            if (++pending > kLag) {
-                cp_async_wait<kLag>();
-                hand_over();
-            }
-        };
-        // 16 rows: lane l (and l + 16) knows row l's address, or nullptr for zeros
+        constexpr int kCopies = 16 / kRowsCopy;  // warp-wide copies of 16 rows
+        const bool in_row = cc < chunks, in_head = cc * 8 < a.D;
+        // 16 rows from r0 on; lane l (and l + 16) knows row l's address, or nullptr for zeros
         auto copy16 = [&](uint32_t tile, int rows, int r0, const unsigned char *row) {
+            unsigned long long p[kCopies];
 #pragma unroll
-            for (int i = 0; i < 16 / kRowsCopy; ++i) {
-                const int r = i * kRowsCopy + crow;
-                const unsigned long long p =
-                    __shfl_sync(kFull, reinterpret_cast<unsigned long long>(row), r);
-                if (cc >= chunks) continue;
-                const bool there = p != 0 && cc * 8 < a.D;
-                const void *src = there ? reinterpret_cast<const void *>(p + cc * 16) : a.Q;
-                cp_async16(tile + swizzled(rows, r0 + r, cc), src, there ? 16 : 0);
+            for (int i = 0; i < kCopies; ++i)
+                p[i] = __shfl_sync(kFull, reinterpret_cast<unsigned long long>(row), i * kRowsCopy + crow);
+            if (!in_row) return;
+#pragma unroll
+            for (int i = 0; i < kCopies; ++i) {
+                const bool there = p[i] != 0 && in_head;
+                const void *src = there ? reinterpret_cast<const void *>(p[i] + cc * 16) : a.Q;
+                cp_async16(tile + swizzled(rows, r0 + i * kRowsCopy + crow, cc), src, there ? 16 : 0);
             }
         };
         uint32_t used = 0;  // slots handed out
-        bool ok = true;
-        auto claim = [&](uint64_t *bar, uint32_t parity) {
-            // what is under way may be what the products wait for
-            if (!__all_sync(kFull, mbar_test_wait(bar, parity))) {
-                flush();
-                ok = wait_warp(bar, parity, kErrProducerWait);
-            }
-            return ok;
-        };
         while (ok && some && walk.next(t, shares)) {
             const int my_number = number++;
             const TileItem it = attend::item_of(a, t, shares, tile_rows(DP), walk.item);
             const int stacks = stacks_of(it);
-            if (my_number > 0) {
-                if (!claim(q_free, (my_number - 1) & 1)) break;
-                flush();  // pieces of the last item are looked through under its number
-            }
-            bad_number = my_number;
+            if (my_number > 0 && !(ok = wait_warp(q_free, (my_number - 1) & 1, kErrProducerWait))) break;
             for (int g = lw; g < stacks * 8; g += kLoadWarps) {
                 const int r = g * 16 + (lane & 15);
                 const unsigned char *row = nullptr;
@@ -455,7 +452,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                 }
                 copy16(q_smem + (g >> 3) * Z::kQBytes, 128, (g & 7) * 16, row);
             }
-            push(q_full, -1);
+            cp_async_arrive(q_full);
             int min_end = a.shared;
             if (uniform && t.bound_ends) {
                 const int toks = fast_div(it.head + it.rows - 1, t.div_group) + 1;
@@ -465,23 +462,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
             const Seen counted{it.first, it.lo, it.lo + it.n - it.first};
             const Edges all = seen_by_all(it, 0, it.rows, min_end);
             const unsigned row_bytes = static_cast<unsigned>(a.Hk) * a.D * 2;
-            const size_t head_at = static_cast<size_t>(walk.kvh) * a.D * 2;
+            const size_t col = (static_cast<size_t>(walk.kvh) * a.D + (in_head ? cc * 8 : 0)) * 2;
+            const unsigned char *const from_k = static_cast<const unsigned char *>(a.Kp ? a.Kp : a.K) + col;
+            const unsigned char *const from_v = static_cast<const unsigned char *>(a.Kp ? a.Vp : a.V) + col;
             for (int j = walk.j0; j < walk.j1 && ok; ++j) {
+                // the rows that this lane copies from, of each of the warp's groups of 16
                 constexpr int kGroups = (kKeys / 16 + kLoadWarps - 1) / kLoadWarps;
-                const unsigned char *rows_k[kGroups];
-                size_t off[kGroups];
-                bool there[kGroups], apart[kGroups];
+                unsigned at[kGroups][kCopies];
 #pragma unroll
                 for (int i = 0; i < kGroups; ++i) {
                     const int g = lw + i * kLoadWarps;
                     const int x = j * kKeys + g * 16 + (lane & 15);
-                    there[i] = g < kKeys / 16 && x < it.n;
-                    off[i] = 0;
-                    apart[i] = false;
-                    if (there[i]) {
-                        const int pos = counted.at(x);
-                        apart[i] = a.Kp != nullptr && pos < a.own_base;
-                        off[i] = static_cast<size_t>(attend::row_of(a, it.b, pos)) * row_bytes + head_at;
+                    unsigned row = kNoRow;
+                    if (g < kKeys / 16 && x < it.n) row = static_cast<unsigned>(attend::row_of(a, it.b, counted.at(x)));
+#pragma unroll
+                    for (int c = 0; c < kCopies; ++c) {
+                        at[i][c] = __shfl_sync(kFull, row, c * kRowsCopy + crow);
+                        if (!in_head) at[i][c] = kNoRow;
                     }
                 }
 #pragma unroll
@@ -489,26 +486,42 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     const int slot = used % Z::kSlots;
                     const uint32_t round = used / Z::kSlots;
                     ++used;
-                    if (round > 0 && !claim(kv_free + slot, (round - 1) & 1)) break;
+                    if (round > 0 && !(ok = wait_warp(kv_free + slot, (round - 1) & 1, kErrProducerWait))) break;
+                    const unsigned char *const from = kv == 0 ? from_k : from_v;
+                    const uint32_t tile = ring + slot * Z::kSlotBytes;
 #pragma unroll
                     for (int i = 0; i < kGroups; ++i) {
                         const int g = lw + i * kLoadWarps;
-                        if (g >= kKeys / 16) break;
-                        const void *base = kv == 0 ? (apart[i] ? a.Kp : a.K) : (apart[i] ? a.Vp : a.V);
-                        rows_k[i] = there[i] ? static_cast<const unsigned char *>(base) + off[i] : nullptr;
-                        copy16(ring + slot * Z::kSlotBytes, kKeys, g * 16, rows_k[i]);
+                        if (g >= kKeys / 16 || !in_row) break;
+#pragma unroll
+                        for (int c = 0; c < kCopies; ++c) {
+                            const bool there = at[i][c] != kNoRow;
+                            const unsigned row = there ? at[i][c] : 0u;
+                            cp_async16(tile + swizzled(kKeys, g * 16 + c * kRowsCopy + crow, cc),
+                                       from + static_cast<size_t>(row) * row_bytes, there ? 16 : 0);
+                        }
                     }
-                    push(kv_full + slot, kv == 1 && in_part(all, j * kKeys, min(it.n, (j + 1) * kKeys)) ? slot : -1);
+                    if (kv == 1 && in_part(all, j * kKeys, min(it.n, (j + 1) * kKeys))) {
+                        cp_async_commit();
+                        cp_async_wait<0>();
+                        if (look_through(slot)) *const_cast<volatile int *>(&s_bad[my_number & 3]) = my_number;
+                        mbar_arrive(kv_full + slot);
+                    } else {
+                        cp_async_arrive(kv_full + slot);
+                    }
                 }
             }
         }
-        flush();
+        cp_async_commit();
+        cp_async_wait<0>();
     } else {
         // ---------------------------------------------------------- products
-        if (lane == 0) {
+        if (tc::elect_one()) {
             constexpr uint32_t kIdescS = tc::instr_desc(128, kKeys, kBf16, false);
             const uint32_t idesc_o = tc::instr_desc(128, (a.D + 15) / 16 * 16, kBf16, true);
             const int ksteps = (a.D + 15) / 16;
+            const uint64_t q_desc = tc::smem_desc(q_smem, 0), k_desc = tc::smem_desc(ring, 0);
+            const uint64_t v_desc = tc::smem_desc(ring, kKeys * 128);
             uint32_t used = 0, n_p[2] = {0, 0};
             int number = 0;
             bool ok = true;
@@ -521,12 +534,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     const uint32_t u = used + 2 * j;
                     const int slot = u % Z::kSlots;
                     if (stack == 0 && !wait(kv_full + slot, (u / Z::kSlots) & 1, kErrConsumerWait)) return false;
+                    tc::fence_async();  // what the copies wrote is visible to the tensor cores
                     tc::fence_after();
-                    const uint32_t qa = q_smem + stack * Z::kQBytes, ka = ring + slot * Z::kSlotBytes;
-                    for (int k = 0; k < ksteps; ++k)
-                        tc::mma(tmem + Z::kColS + buf * kKeys,
-                                tc::smem_desc(qa + (k >> 2) * (128 * 128) + (k & 3) * 32, 0),
-                                tc::smem_desc(ka + (k >> 2) * (kKeys * 128) + (k & 3) * 32, 0), kIdescS, k > 0);
+                    const uint64_t qd = q_desc + stack * (Z::kQBytes >> 4), kd = k_desc + slot * (Z::kSlotBytes >> 4);
+                    const uint32_t to = tmem + Z::kColS + buf * kKeys;
+#pragma unroll
+                    for (int k = 0; k < DP / 16; ++k) {
+                        if (k >= ksteps) break;
+                        tc::mma(to, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
+                                kd + (((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4), kIdescS, k > 0);
+                    }
                     tc::commit((stacks == 2 ? s_two : s_one) + buf);
                     if (stack == stacks - 1) tc::commit(kv_free + slot);
                     if (n == steps - 1) tc::commit(q_free);
@@ -539,11 +556,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     if (stack == 0 && !wait(kv_full + slot, (u / Z::kSlots) & 1, kErrConsumerWait)) return false;
                     if (!wait(p_full + buf, n_p[buf] & 1, kErrConsumerWait)) return false;
                     ++n_p[buf];
+                    tc::fence_async();
                     tc::fence_after();
-                    const uint32_t va = ring + slot * Z::kSlotBytes;
+                    const uint64_t vd = v_desc + slot * (Z::kSlotBytes >> 4);
+                    const uint32_t to = tmem + Z::kColO + stack * DP, from = tmem + Z::kColS + buf * kKeys;
+#pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k)
-                        tc::mma_tmem(tmem + Z::kColO + stack * DP, tmem + Z::kColS + buf * kKeys + k * 8,
-                                     tc::smem_desc(va + k * 2048, kKeys * 128), idesc_o, j > 0 || k > 0);
+                        tc::mma_tmem(to, from + k * 8, vd + k * (2048 >> 4), idesc_o, j > 0 || k > 0);
                     tc::commit(o_done + stack);
                     if (stack == stacks - 1) tc::commit(kv_free + slot);
                     return true;

@@ -169,6 +169,12 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// One arrival of the calling thread on `bar` when its copies so far are done (one of the
+// arrivals that the barrier was set up for).
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
 // Thread-block clusters: rank of this CTA in its cluster, the address of the
 // same shared-memory location in another CTA of the cluster, a load from it,
 // and the cluster-wide barrier (every thread of every CTA of the cluster

@@ -27,6 +27,13 @@ __host__ __device__ constexpr uint32_t instr_desc(int m, int n, bool bf16, bool 
            (static_cast<uint32_t>(n >> 3) << 17) | (static_cast<uint32_t>(m >> 4) << 24);
 }
 
+// One thread of the warp, which the compiler knows to be one.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // All columns of the SM's tensor memory, by one warp; the address goes to *where.
 __device__ __forceinline__ void alloc(uint32_t *where) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(where))
