@@ -10,6 +10,7 @@
 #include <mutex>
 #include <tuple>
 #include <type_traits>
+#include <utility>
 
 #include "api_checks.h"
 #include "dattn_internal.h"
@@ -101,6 +102,7 @@ struct Plan {
     }
 };
 
+constexpr int kBoxRows = 8;  // fewest rows of a page's box
 constexpr int kMaxColumns = 16;  // query heads of a key/value head in one CTA
 constexpr int kStaticSmem = 1024;  // the kernel's static shared memory at most
 constexpr size_t kKeptPlans = 1024;  // a program that never repeats a shape starts anew
@@ -351,9 +353,22 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
             at(p.t_whole_acc, t.whole_acc);
             at(p.t_whole_ml, t.whole_ml);
         }
+        // A dense cache's tiles are one box each; a paged one's as many rows as divide a page.
+        dattn::TileMaps m{};
+        m.box_rows = dattn::tile_keys(p.dp);
+        if (s.page_size > 0)
+            while (s.page_size % m.box_rows != 0) m.box_rows /= 2;
+        if (m.box_rows < kBoxRows) m.box_rows = 0;
+        t.align = s.page_size > 0 && m.box_rows > 0 ? m.box_rows : 1;
+        if (m.box_rows > 0) {
+            const long long map_rows = s.apart ? s.shared : static_cast<long long>(rows);
+            for (auto &[map, base] : {std::pair{&m.k, s.apart ? Kp : K}, std::pair{&m.v, s.apart ? Vp : V}})
+                if (int st = dattn::encode_head_rows(map, base, map_rows, s.n_kv_heads, s.head_dim, m.box_rows, dtype))
+                    return st;
+        }
         at(p.t_acc, t.acc);
         at(p.t_ml, t.ml);
-        e = dattn::launch_attend_tiles(a, t, dtype, p.dp, stream);
+        e = dattn::launch_attend_tiles(a, t, m, dtype, p.dp, stream);
         if (e != cudaSuccess) return fail_cuda(e, "attention kernel launch");
     }
     if (p.token) {

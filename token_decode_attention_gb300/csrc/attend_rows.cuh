@@ -86,15 +86,22 @@ __device__ __forceinline__ long long row_of(const AttendArgs &a, int b, int pos)
     return static_cast<long long>(page) * a.page_size + (pos - pi * a.page_size);
 }
 
-// State of one query head over the positions counted i0 .. i1-1 of `v` (those of a group
-// of tokens) that its own token, which sees [0, sinks) and [lo, end), sees too: running
+// The positions that some token of a group sees, counted: `window` from lo on, then the
+// sinks from 0 on.
+struct Counted {
+    int lo, window;
+    __device__ __forceinline__ int at(int i) const { return i < window ? lo + i : i - window; }
+};
+
+// State of one query head over the positions counted i0 .. i1-1 of `v` that its own token,
+// which sees [0, sinks) and [lo, end), sees too: running
 // maximum (log2 units), sum of weights and weighted values of channels 2 (lane + 32 c), by
 // one warp, 32 positions at a time: a lane each for the scores, channels over the lanes for V.
 struct RowState {
     float M, l, acc[4][2];
 };
 template <typename T>
-__device__ void row_state(const AttendArgs &a, int b, int kvh, const T *q, Seen v, int i0, int i1, int lo, int end,
+__device__ void row_state(const AttendArgs &a, int b, int kvh, const T *q, Counted v, int i0, int i1, int lo, int end,
                           int lane, RowState &r) {
     constexpr unsigned kAll = 0xffffffffu;
     const long long head = static_cast<long long>(kvh) * a.D;

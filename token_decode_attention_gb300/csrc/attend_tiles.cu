@@ -83,10 +83,9 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttendArgs a, 
             it.rows = min(rows, all - row);
             const int last = fast_div(row + it.rows - 1, t.div_group);
             it.p0 = attend::live_end(a, lo) - (own.y - own.x) + tok;
-            const attend::Seen v = attend::seen_by(a, it.p0);
-            it.lo = v.lo;
-            it.first = v.first;
-            it.n = max(it.p0 + (last - tok) + 1, 0) - v.lo + v.first;
+            it.lo = attend::seen_by(a, it.p0).lo & ~(t.align - 1);
+            it.first = min(a.sinks, it.lo);
+            it.n = max(it.p0 + (last - tok) + 1, 0) - it.lo + it.first;
             int4 *at = reinterpret_cast<int4 *>(t.items + s);
             at[0] = make_int4(it.b, it.token, it.head, it.rows);
             at[1] = make_int4(it.p0, it.lo, it.first, it.n);
@@ -185,7 +184,8 @@ cudaError_t attend_tiles_configure(int max_smem) {
     return cudaSuccess;
 }
 
-cudaError_t launch_attend_tiles(const AttendArgs &a, const TileArgs &t, int dtype, int dp, cudaStream_t stream) {
+cudaError_t launch_attend_tiles(const AttendArgs &a, const TileArgs &t, const TileMaps &m, int dtype, int dp,
+                                cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -199,7 +199,7 @@ cudaError_t launch_attend_tiles(const AttendArgs &a, const TileArgs &t, int dtyp
         const cudaError_t e = cudaLaunchKernelEx(&cfg, plan_kernel, a, t, tile_rows(dp), tile_keys(dp));
         if (e != cudaSuccess) return e;
     }
-    void *args[] = {const_cast<AttendArgs *>(&a), const_cast<TileArgs *>(&t)};
+    void *args[] = {const_cast<AttendArgs *>(&a), const_cast<TileArgs *>(&t), const_cast<TileMaps *>(&m)};
     cfg.gridDim = dim3(static_cast<unsigned>(t.ctas));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = static_cast<size_t>(smem_of(dp));

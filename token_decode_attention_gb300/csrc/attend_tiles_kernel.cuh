@@ -12,16 +12,16 @@
 //             from tensor memory, P goes back there in 16 bits over S; O stays there too
 //             and is rescaled only when a maximum grows by more than 2^kTrigger, so most
 //             tiles never touch it.
-//   8-10      loads: cp.async of 16 bytes into swizzled tiles, a ring of slots for K and V.
-//             Row addresses may be any (pages, sinks ahead of a window), positions that no
-//             row sees are not read and zero.
+//   8-10      loads: K and V tiles into a ring of slots, Q once an item.  Tiles inside the
+//             window are boxes of TMA (a whole tile of a dense cache, of a paged one as many
+//             rows as divide a page); others, 16-byte cp.async of any rows (sinks, the
+//             item's end, odd pages): positions that no row sees are not read and zero.
 //   11        issues the products: S of the next tile while softmax works on the last one.
 // While one stack's softmax runs, the tensor cores work for the other.
 //
-// A hidden position gets weight zero; 0 times a V that is not finite would still reach the
-// row.  The loading warps look for such values in tiles that some row sees in part (no
-// other tile can hold a hidden one); where there are any, the piece's rows are computed
-// again position by position (attend::row_state), which touches what they see only.
+// A hidden position gets weight zero; 0 times a V that is not finite still makes the row's
+// O a NaN.  Rows with a NaN in a piece with hidden positions are computed again position
+// by position (attend::row_state), which touches what they see only.
 //
 // Work split: attend_tiles.cuh.  Pieces of items leave their states to the merge kernels.
 #pragma once
@@ -39,7 +39,6 @@ using attend::Pair;
 using attend::Seen;
 
 constexpr unsigned kFull = 0xffffffffu;
-constexpr int kSoftmaxThreads = 128;  // of a stack
 constexpr int kLoadWarps = 3, kThreads = 384;
 constexpr unsigned kNoRow = 0xffffffffu;  // zeros (a cache has fewer than 2^31 rows)
 // The running maximum M is kept kHeadroom (log2) below the largest exponent when it was set
@@ -55,7 +54,8 @@ struct TileShape {
     static constexpr int kSlotBytes = kKeys * DP * 2;  // K or V of a tile
     static constexpr int kSlots = DP == 64 ? 8 : DP == 128 ? 5 : 5;
     static constexpr int kColS = 0, kColO = 2 * kKeys;  // tensor memory columns
-    static constexpr int kBars = 2 * kSlots + 16;
+    static constexpr int kParts = 4;  // of a tile's keys, whose P is handed over by itself
+    static constexpr int kBars = 2 * kSlots + 9 + 2 * kParts;
     static constexpr int kSmem = kStacks * kQBytes + kSlots * kSlotBytes + 1024;
 };
 
@@ -90,65 +90,59 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-__device__ __forceinline__ uint4 lds128(uint32_t addr) {
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
-    return v;
-}
-
-// Whether a word holds a 16-bit value whose exponent is all ones.
-template <typename T>
-__device__ __forceinline__ uint32_t not_finite(uint32_t w) {
-    if constexpr (std::is_same<T, __half>::value) return ((w & 0x7c007c00u) + 0x04000400u) & 0x80008000u;
-    return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
-}
-
-// Hidden positions of an item's rows, in the item's count: a row sees i < end that is at
-// least `lo` or below `sinks`.
+// What a row sees of an item's positions, in the item's count: of the `window` ones from
+// the item's `lo` on those in [lo, end) and below `sinks`; the sinks behind them, up to n, all.
 struct Edges {
-    int lo, end, sinks;
-    __device__ __forceinline__ bool hides(int i) const { return i >= end || (i < lo && i >= sinks); }
+    int lo, end, sinks, window, n;
+    // The hidden ones of positions x0 .. x0 + 31, a bit each.
+    __device__ __forceinline__ uint32_t hidden32(int x0) const {
+        return range32(end - x0, window - x0) | range32(sinks - x0, min(lo, window) - x0) | ~below32(n - x0);
+    }
+    static __device__ __forceinline__ uint32_t below32(int k) { return k >= 32 ? ~0u : k <= 0 ? 0u : (1u << k) - 1u; }
+    static __device__ __forceinline__ uint32_t range32(int k0, int k1) { return below32(k1) & ~below32(k0); }
+    // Whether rows that all see this much see [x0, x1) in part.
+    __device__ __forceinline__ bool cuts(int x0, int x1) const {
+        const int w1 = min(x1, window);
+        return w1 > max(end, x0) || (x0 < lo && min(w1, lo) > max(sinks, x0)) || x1 > n;
+    }
 };
 
-// A row of token `tok` rows behind the item's first one.
+// The row of the item's token `tok`.
 __device__ __forceinline__ Edges edges_of(const AttendArgs &a, const TileArgs &t, const TileItem &it, int tok,
                                           bool uniform) {
     Edges e;
+    e.window = it.n - it.first;
+    e.n = it.n;
     if (uniform) {
         e.lo = 0;
         e.sinks = 0;
         e.end = t.bound_ends ? min(a.shared, attend::live_end(a, it.token + tok)) : a.shared;
         return e;
     }
-    const int shift = it.first - it.lo;  // position to count, from `lo` on
     const Seen v = attend::seen_by(a, it.p0 + tok);
-    e.lo = v.lo + shift;
-    e.end = v.end + shift;
-    // sinks past the item's `lo` are seen by rows whose window has moved past them
-    e.sinks = a.sinks > it.lo ? a.sinks + shift : it.first;
+    e.lo = v.lo - it.lo;
+    e.end = v.end - it.lo;
+    e.sinks = max(a.sinks - it.lo, 0);
     return e;
 }
 
 template <typename T, int DP>
-__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendArgs a, const TileArgs t) {
+__global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendArgs a, const TileArgs t,
+                                                                  const __grid_constant__ TileMaps maps) {
     using Z = TileShape<DP>;
     constexpr int kKeys = Z::kKeys;
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t bars[Z::kBars];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_bad[4];  // number of the last item (modulo 4) with values that are not finite
 
     uint64_t *const kv_full = bars, *const kv_free = bars + Z::kSlots;
     uint64_t *const q_full = bars + 2 * Z::kSlots, *const q_free = q_full + 1;
     uint64_t *const s_two = q_full + 2;   // [2] S of a stack is there (items of two stacks)
     uint64_t *const s_one = q_full + 4;   // [2] S of a buffer is there (items of one)
-    uint64_t *const p_full = q_full + 6;  // [2] P of a buffer is there
-    uint64_t *const o_done = q_full + 8;  // [2] O of a stack has its last tile
-    uint64_t *const drained = q_full + 10;
+    uint64_t *const o_done = q_full + 6;  // [2] O of a stack has its last tile
+    uint64_t *const drained = q_full + 8;
+    uint64_t *const p_full = q_full + 9;  // [2][kParts] a part of P of a buffer is there
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t q_smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -157,20 +151,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
     if (warp == 11) tc::alloc(&s_tmem);
     if (tid == 0) {
         for (int i = 0; i < Z::kSlots; ++i) {
-            mbar_init(kv_full + i, kLoadWarps * 32);
+            mbar_init(kv_full + i, kLoadWarps);
             mbar_init(kv_free + i, 1);
         }
-        mbar_init(q_full, kLoadWarps * 32);
+        mbar_init(q_full, kLoadWarps);
         mbar_init(q_free, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_two + i, 1);
             mbar_init(s_one + i, 1);
-            mbar_init(p_full + i, kSoftmaxThreads);
             mbar_init(o_done + i, 1);
         }
+        for (int i = 0; i < 2 * Z::kParts; ++i) mbar_init(p_full + i, 4);  // the stack's warps
         mbar_init(drained, 1);
         fence_barrier_init();
-        s_bad[0] = s_bad[1] = s_bad[2] = s_bad[3] = -1;
     }
     tc::fence_before();
     __syncthreads();
@@ -196,16 +189,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
         return __all_sync(kFull, wait(bar, parity, code)) != 0;
     };
     auto stacks_of = [&](const TileItem &it) { return Z::kStacks == 2 && it.rows > 128 ? 2 : 1; };
-    // What rows [r0, r1) of the item all see; a tile that goes past it is hidden in part.
+    // What rows [r0, r1) of the item all see.
     auto seen_by_all = [&](const TileItem &it, int r0, int r1, int min_end) {
-        if (uniform) return Edges{0, min_end, 0};
-        const Edges first = edges_of(a, t, it, fast_div(it.head + r0, t.div_group), false);
-        Edges last = edges_of(a, t, it, fast_div(it.head + r1 - 1, t.div_group), false);
-        last.end = first.end;
+        const Edges first = edges_of(a, t, it, fast_div(it.head + r0, t.div_group), uniform);
+        Edges last = edges_of(a, t, it, fast_div(it.head + r1 - 1, t.div_group), uniform);
+        last.end = uniform ? min_end : first.end;
         return last;
-    };
-    auto in_part = [&](const Edges &all, int x0, int x1) {
-        return x1 > all.end || (x0 < all.lo && x1 > all.sinks);
     };
 
     // A softmax thread holds a row's scores of a tile; the registers come from the others:
@@ -220,17 +209,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4)
         const uint32_t col_o = tmem + lanes + Z::kColO + stack * DP;
         uint32_t n_two = 0, n_one[2] = {0, 0}, n_o = 0;
-        int number = 0;
         bool ok = true;
         while (ok && some && walk.next(t, shares)) {
-            const int my_number = number++;
             const TileItem it = attend::item_of(a, t, shares, tile_rows(DP), walk.item);
             const int stacks = stacks_of(it);
             if (stack >= stacks) continue;
             const int r0 = stack * 128, r1 = min(it.rows, r0 + 128);
             const int tok = fast_div(it.head + r0 + row, t.div_group);
             const bool mine = r0 + row < it.rows;
-            Edges e{0, 0, 0};
+            Edges e{0, 0, 0, it.n, it.n};
             if (mine) e = edges_of(a, t, it, tok, uniform);
             int min_end = a.shared;
             if (uniform && t.bound_ends) {
@@ -239,6 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
             }
             const Edges all = seen_by_all(it, r0, r1, min_end);
             float M = -INFINITY, l = 0.f;
+            bool hidden = false;  // some row of the warp does not see some position
             for (int j = walk.j0; j < walk.j1; ++j) {
                 const int n = j - walk.j0;
                 const int buf = stacks == 2 ? stack : n & 1;
@@ -253,10 +241,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                 for (int c = 0; c < kKeys; c += 32) tc::ld32(sv + c, col_s + c);
                 tc::wait_ld();
                 const int x0 = j * kKeys;
-                if (in_part(all, x0, x0 + kKeys)) {
+                if (all.cuts(x0, x0 + kKeys)) {
+                    hidden = true;
 #pragma unroll
-                    for (int c = 0; c < kKeys; ++c)
-                        if (e.hides(x0 + c)) sv[c] = 0xff800000u;  // -infinity
+                    for (int c = 0; c < kKeys; c += 32) {
+                        const uint32_t h = e.hidden32(x0 + c);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k)
+                            if (h >> k & 1) sv[c + k] = 0xff800000u;  // -infinity
+                    }
                 }
                 float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -296,22 +289,29 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                 const float ref = M == -INFINITY ? 0.f : M;
                 const float2 scale2 = make_float2(a.qscale, a.qscale), ref2 = make_float2(-ref, -ref);
                 float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                constexpr int kPart = kKeys / Z::kParts;
 #pragma unroll
-                for (int c = 0; c < kKeys; c += 2) {
-                    float2 p = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), scale2, ref2);
-                    p.x = ex2(p.x);
-                    p.y = ex2(p.y);
-                    l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], p);
-                    sv[c / 2] = Pair<T>::narrow(p.x, p.y);
+                for (int part = 0; part < Z::kParts; ++part) {
+#pragma unroll
+                    for (int c = part * kPart; c < (part + 1) * kPart; c += 2) {
+                        float2 p = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), scale2, ref2);
+                        p.x = ex2(p.x);
+                        p.y = ex2(p.y);
+                        l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], p);
+                        sv[c / 2] = Pair<T>::narrow(p.x, p.y);
+                    }
+                    if constexpr (kPart == 32) tc::st16(col_s + part * 16, sv + part * 16);
+                    else tc::st8(col_s + part * 8, sv + part * 8);
+                    tc::wait_st();
+                    // its phases are not to be passed over
+                    if (part == Z::kParts - 1 && running && !product_done()) break;
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(p_full + buf * Z::kParts + part);
                 }
+                if (!ok) break;
                 l2[0] = add2(l2[0], l2[1]);
                 l += l2[0].x + l2[0].y;
-#pragma unroll
-                for (int c = 0; c < kKeys / 2; c += 32) tc::st32(col_s + c, sv + c);
-                tc::wait_st();
-                if (running && !product_done()) break;  // its phases are not to be passed over
-                tc::fence_before();
-                mbar_arrive(p_full + buf);
             }
             if (!ok) break;
             // ---- the piece's rows ----
@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
             const long long out_row = token * a.H + static_cast<long long>(kvh) * a.group + q_head;
             const long long slot_row =
                 static_cast<long long>(2 * cta + (walk.begins ? 1 : 0)) * tile_rows(DP) + r0 + row;
-            const bool bad = *const_cast<volatile int *>(&s_bad[my_number & 3]) == my_number;
+            bool nan = false;
             const float inv = e.end > 0 ? 1.f / l : 0.f;
             float *const state = uniform && whole ? t.whole_acc + out_row * a.D : t.acc + slot_row * a.D;
             float2 *const state_ml = uniform && whole ? t.whole_ml + out_row : t.ml + slot_row;
@@ -336,13 +336,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                 uint32_t o[32];
                 tc::ld32(o, col_o + c);
                 tc::wait_ld();
-                if (!mine || bad) continue;
+                if (!mine) continue;
 #pragma unroll
                 for (int k = 0; k < 32; k += 8) {
                     if (c + k >= a.D) break;
                     float y[8];
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = __uint_as_float(o[k + i]);
+                    for (int i = 0; i < 8; ++i) {
+                        y[i] = __uint_as_float(o[k + i]);
+                        nan |= y[i] != y[i];
+                    }
                     if (to_out) {
                         uint4 w;
                         w.x = Pair<T>::narrow(y[0] * inv, y[1] * inv);
@@ -357,13 +360,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                 }
             }
             tc::fence_before();  // O has been read before the next item's first P is handed over
-            if (mine && !bad && !to_out) *state_ml = make_float2(M, l);
-            if (bad) {
-                // position by position, a row after the other of the warp's
-                const Seen counted{it.first, it.lo, it.lo + it.n - it.first};
+            if (mine && !to_out) *state_ml = make_float2(M, l);
+            unsigned again = __ballot_sync(kFull, nan && hidden);
+            if (again != 0) {
+                // position by position, a row after the other, over what was just written
+                __syncwarp();
                 const int i0 = walk.j0 * kKeys, i1 = min(it.n, walk.j1 * kKeys);
-                for (int r = 0; r < 32; ++r) {
-                    if (r0 + (row & 96) + r >= it.rows) break;
+                for (; again != 0; again &= again - 1) {
+                    const int r = __ffs(again) - 1;
                     const int rtok = __shfl_sync(kFull, tok, r), rhead = __shfl_sync(kFull, q_head, r);
                     const long long rtoken = it.token + static_cast<long long>(rtok);
                     const int h = kvh * a.group + rhead;
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     attend::row_state<T>(a, it.b, kvh,
                                          static_cast<const T *>(a.Q) + rtoken * a.q_stride +
                                              static_cast<long long>(h) * a.D,
-                                         counted, i0, i1, lo, end, lane, y);
+                                         attend::Counted{it.lo, it.n - it.first}, i0, i1, lo, end, lane, y);
                     const long long row_out = rtoken * a.H + h;
                     const long long row_slot = __shfl_sync(kFull, slot_row, r);
                     float *const to = uniform && whole ? t.whole_acc + row_out * a.D : t.acc + row_slot * a.D;
@@ -401,84 +405,78 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
         // ------------------------------------------------------------ loads
         const int lw = warp - 8;
         const int chunks = (a.D + 15) / 16 * 2;  // 16-byte chunks of a row that the products read
-        constexpr int CPR = DP / 8;              // of a full row
+        const int blocks = (a.D + 63) / 64;      // 64-channel blocks
+        constexpr int CPR = DP / 8;              // chunks of a full row
         constexpr int kLanesRow = CPR < 32 ? CPR : 32, kRowsCopy = 32 / kLanesRow;
-        const int crow = lane / kLanesRow, cc = lane % kLanesRow;
-        int number = 0;
-        bool ok = true;
-        // Whether this lane's own copies of a tile hold a value that is not finite.
-        auto look_through = [&](int slot) {
-            const uint32_t base = ring + slot * Z::kSlotBytes;
-            uint32_t any = 0;
-            for (int g = lw; g < kKeys / 16; g += kLoadWarps)
-#pragma unroll 4
-                for (int i = 0; i < 16 / kRowsCopy; ++i) {
-                    if (cc >= chunks) continue;
-                    const uint4 w = lds128(base + swizzled(kKeys, g * 16 + i * kRowsCopy + crow, cc));
-                    any |= not_finite<T>(w.x) | not_finite<T>(w.y) | not_finite<T>(w.z) | not_finite<T>(w.w);
-                }
-            return any != 0;
-        };
         constexpr int kCopies = 16 / kRowsCopy;  // warp-wide copies of 16 rows
+        const int crow = lane / kLanesRow, cc = lane % kLanesRow;
         const bool in_row = cc < chunks, in_head = cc * 8 < a.D;
-        // 16 rows from r0 on; lane l (and l + 16) knows row l's address, or nullptr for zeros
-        auto copy16 = [&](uint32_t tile, int rows, int r0, const unsigned char *row) {
-            unsigned long long p[kCopies];
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i)
-                p[i] = __shfl_sync(kFull, reinterpret_cast<unsigned long long>(row), i * kRowsCopy + crow);
-            if (!in_row) return;
-#pragma unroll
-            for (int i = 0; i < kCopies; ++i) {
-                const bool there = p[i] != 0 && in_head;
-                const void *src = there ? reinterpret_cast<const void *>(p[i] + cc * 16) : a.Q;
-                cp_async16(tile + swizzled(rows, r0 + i * kRowsCopy + crow, cc), src, there ? 16 : 0);
-            }
+        // the warp's copies so far are done, and what it had to do for the tile
+        auto arrive = [&](uint64_t *bar) {
+            cp_async_hold(bar);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
         };
+        int number = 0;
         uint32_t used = 0;  // slots handed out
+        bool ok = true;
         while (ok && some && walk.next(t, shares)) {
-            const int my_number = number++;
             const TileItem it = attend::item_of(a, t, shares, tile_rows(DP), walk.item);
             const int stacks = stacks_of(it);
-            if (my_number > 0 && !(ok = wait_warp(q_free, (my_number - 1) & 1, kErrProducerWait))) break;
+            if (number > 0 && !(ok = wait_warp(q_free, (number - 1) & 1, kErrProducerWait))) break;
+            ++number;
             for (int g = lw; g < stacks * 8; g += kLoadWarps) {
+                // 16 rows: lane l (and l + 16) finds row l's address, 0 for zeros
                 const int r = g * 16 + (lane & 15);
-                const unsigned char *row = nullptr;
+                unsigned long long row = 0;
                 if (r < it.rows) {
                     const int tok = fast_div(it.head + r, t.div_group);
                     const int h = walk.kvh * a.group + (it.head + r - tok * a.group);
-                    row = static_cast<const unsigned char *>(a.Q) +
+                    row = reinterpret_cast<unsigned long long>(a.Q) +
                           ((it.token + static_cast<long long>(tok)) * a.q_stride + static_cast<long long>(h) * a.D) * 2;
                 }
-                copy16(q_smem + (g >> 3) * Z::kQBytes, 128, (g & 7) * 16, row);
+                const uint32_t tile = q_smem + (g >> 3) * Z::kQBytes;
+                unsigned long long from[kCopies];
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) from[i] = __shfl_sync(kFull, row, i * kRowsCopy + crow);
+                if (!in_row) continue;
+#pragma unroll
+                for (int i = 0; i < kCopies; ++i) {
+                    const bool there = from[i] != 0 && in_head;
+                    cp_async16(tile + swizzled(128, (g & 7) * 16 + i * kRowsCopy + crow, cc),
+                               there ? reinterpret_cast<const void *>(from[i] + cc * 16) : a.Q, there ? 16 : 0);
+                }
             }
-            cp_async_arrive(q_full);
-            int min_end = a.shared;
-            if (uniform && t.bound_ends) {
-                const int toks = fast_div(it.head + it.rows - 1, t.div_group) + 1;
-                for (int k = lane; k < toks; k += 32) min_end = min(min_end, attend::live_end(a, it.token + k));
-                min_end = __reduce_min_sync(kFull, min_end);
-            }
-            const Seen counted{it.first, it.lo, it.lo + it.n - it.first};
-            const Edges all = seen_by_all(it, 0, it.rows, min_end);
+            arrive(q_full);
+            const attend::Counted counted{it.lo, it.n - it.first};
             const unsigned row_bytes = static_cast<unsigned>(a.Hk) * a.D * 2;
             const size_t col = (static_cast<size_t>(walk.kvh) * a.D + (in_head ? cc * 8 : 0)) * 2;
             const unsigned char *const from_k = static_cast<const unsigned char *>(a.Kp ? a.Kp : a.K) + col;
             const unsigned char *const from_v = static_cast<const unsigned char *>(a.Kp ? a.Vp : a.V) + col;
             for (int j = walk.j0; j < walk.j1 && ok; ++j) {
-                // the rows that this lane copies from, of each of the warp's groups of 16
                 constexpr int kGroups = (kKeys / 16 + kLoadWarps - 1) / kLoadWarps;
+                const bool boxes = maps.box_rows > 0 && (j + 1) * kKeys <= counted.window;
                 unsigned at[kGroups][kCopies];
+                int box_row = 0;
+                if (boxes) {
+                    // lane l of the first warp: the first row of the tile's l-th box
+                    if (lw == 0 && lane * maps.box_rows < kKeys)
+                        box_row = static_cast<int>(
+                            attend::row_of(a, it.b, counted.at(j * kKeys + lane * maps.box_rows)));
+                } else {
+                    // the rows that this lane copies from, of each of the warp's groups of 16
 #pragma unroll
-                for (int i = 0; i < kGroups; ++i) {
-                    const int g = lw + i * kLoadWarps;
-                    const int x = j * kKeys + g * 16 + (lane & 15);
-                    unsigned row = kNoRow;
-                    if (g < kKeys / 16 && x < it.n) row = static_cast<unsigned>(attend::row_of(a, it.b, counted.at(x)));
+                    for (int i = 0; i < kGroups; ++i) {
+                        const int g = lw + i * kLoadWarps;
+                        const int x = j * kKeys + g * 16 + (lane & 15);
+                        unsigned row = kNoRow;
+                        if (g < kKeys / 16 && x < it.n)
+                            row = static_cast<unsigned>(attend::row_of(a, it.b, counted.at(x)));
 #pragma unroll
-                    for (int c = 0; c < kCopies; ++c) {
-                        at[i][c] = __shfl_sync(kFull, row, c * kRowsCopy + crow);
-                        if (!in_head) at[i][c] = kNoRow;
+                        for (int c = 0; c < kCopies; ++c) {
+                            at[i][c] = __shfl_sync(kFull, row, c * kRowsCopy + crow);
+                            if (!in_head) at[i][c] = kNoRow;
+                        }
                     }
                 }
 #pragma unroll
@@ -487,8 +485,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     const uint32_t round = used / Z::kSlots;
                     ++used;
                     if (round > 0 && !(ok = wait_warp(kv_free + slot, (round - 1) & 1, kErrProducerWait))) break;
-                    const unsigned char *const from = kv == 0 ? from_k : from_v;
                     const uint32_t tile = ring + slot * Z::kSlotBytes;
+                    if (boxes) {
+                        if (lane == 0) {
+                            if (lw == 0) mbar_arrive_expect_tx(kv_full + slot, blocks * kKeys * 128);
+                            else mbar_arrive(kv_full + slot);
+                        }
+                        __syncwarp();
+                        if (lw == 0 && lane * maps.box_rows < kKeys)
+                            for (int c = 0; c < blocks; ++c)
+                                box_g2s(tile + c * (kKeys * 128) + lane * maps.box_rows * 128,
+                                        kv == 0 ? &maps.k : &maps.v, c * 64, walk.kvh, box_row, kv_full + slot);
+                        continue;
+                    }
+                    const unsigned char *const from = kv == 0 ? from_k : from_v;
 #pragma unroll
                     for (int i = 0; i < kGroups; ++i) {
                         const int g = lw + i * kLoadWarps;
@@ -501,19 +511,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                                        from + static_cast<size_t>(row) * row_bytes, there ? 16 : 0);
                         }
                     }
-                    if (kv == 1 && in_part(all, j * kKeys, min(it.n, (j + 1) * kKeys))) {
-                        cp_async_commit();
-                        cp_async_wait<0>();
-                        if (look_through(slot)) *const_cast<volatile int *>(&s_bad[my_number & 3]) = my_number;
-                        mbar_arrive(kv_full + slot);
-                    } else {
-                        cp_async_arrive(kv_full + slot);
-                    }
+                    arrive(kv_full + slot);
                 }
             }
         }
+        // what was asked for has arrived before the shared memory is given up
         cp_async_commit();
         cp_async_wait<0>();
+        for (int i = 0; i < Z::kSlots; ++i) {
+            const uint32_t rounds = (used + Z::kSlots - 1 - i) / Z::kSlots;
+            if (rounds > 0) wait_warp(kv_full + i, (rounds - 1) & 1, kErrDrainWait);
+        }
     } else {
         // ---------------------------------------------------------- products
         if (tc::elect_one()) {
@@ -534,7 +542,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     const uint32_t u = used + 2 * j;
                     const int slot = u % Z::kSlots;
                     if (stack == 0 && !wait(kv_full + slot, (u / Z::kSlots) & 1, kErrConsumerWait)) return false;
-                    tc::fence_async();  // what the copies wrote is visible to the tensor cores
+                    tc::fence_async();  // what cp.async wrote is visible to the tensor cores
                     tc::fence_after();
                     const uint64_t qd = q_desc + stack * (Z::kQBytes >> 4), kd = k_desc + slot * (Z::kSlotBytes >> 4);
                     const uint32_t to = tmem + Z::kColS + buf * kKeys;
@@ -554,20 +562,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     const uint32_t u = used + 2 * j + 1;
                     const int slot = u % Z::kSlots;
                     if (stack == 0 && !wait(kv_full + slot, (u / Z::kSlots) & 1, kErrConsumerWait)) return false;
-                    if (!wait(p_full + buf, n_p[buf] & 1, kErrConsumerWait)) return false;
-                    ++n_p[buf];
+                    const uint32_t phase = n_p[buf]++ & 1;
                     tc::fence_async();
-                    tc::fence_after();
                     const uint64_t vd = v_desc + slot * (Z::kSlotBytes >> 4);
                     const uint32_t to = tmem + Z::kColO + stack * DP, from = tmem + Z::kColS + buf * kKeys;
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        tc::mma_tmem(to, from + k * 8, vd + k * (2048 >> 4), idesc_o, j > 0 || k > 0);
+                    for (int part = 0; part < Z::kParts; ++part) {
+                        if (!wait(p_full + buf * Z::kParts + part, phase, kErrConsumerWait)) return false;
+                        tc::fence_after();
+#pragma unroll
+                        for (int i = 0; i < kKeys / 16 / Z::kParts; ++i) {
+                            const int k = part * (kKeys / 16 / Z::kParts) + i;
+                            tc::mma_tmem(to, from + k * 8, vd + k * (2048 >> 4), idesc_o, j > 0 || k > 0);
+                        }
+                    }
                     tc::commit(o_done + stack);
                     if (stack == stacks - 1) tc::commit(kv_free + slot);
                     return true;
                 };
-                ok = wait(q_full, number & 1, kErrConsumerWait) && scores(0) && (steps < 2 || scores(1));
+                ok = wait(q_full, number & 1, kErrConsumerWait);
+                ok = ok && scores(0) && (steps < 2 || scores(1));
                 for (int n = 0; n < steps && ok; ++n) ok = values(n) && (n + 2 >= steps || scores(n + 2));
                 used += 2 * (walk.j1 - walk.j0);
                 ++number;

@@ -264,6 +264,10 @@ struct DeviceFacts {
 };
 int device_facts(DeviceFacts *out);  // a dattn_status, the message recorded
 
+// Tensor map of [rows, H, D] 16-bit elements whose box, box_rows rows of one head and 64
+// channels, lands swizzled by 128 bytes; a dattn_status, the message recorded.
+int encode_head_rows(CUtensorMap *map, const void *base, long long rows, int H, int D, int box_rows, int dtype);
+
 // Rotation of pair i of a token at position p: by the angle p theta_i, cos and
 // sin both multiplied by `magnitude`.  theta_i / (2 pi) travels as a binary
 // fraction in units of 2^-64.
@@ -384,7 +388,7 @@ struct TileItem {
     int b, token;     // sequence, first row's token
     int head, rows;   // first row's query head within the group, rows
     int p0;           // first token's position
-    int lo, first;    // positions that some row sees: [0, first) and [lo, first + ...), n in all
+    int lo, first;    // positions that some row sees: n - first from `lo` on, then [0, first)
     int n;
 };
 // What the planning kernel leaves ahead of the items.
@@ -406,9 +410,17 @@ struct TileArgs {
     FastDiv div_group;
     int ctas;                // CTAs at most
     int bound_ends;          // shared: a token may lie inside the shared positions
+    int align;               // an item's `lo` is a multiple (a power of two)
+};
+// Tensor maps of K and V (of the shared positions' own tensors where there are such) as
+// [rows, Hk, D], a box of box_rows rows of one head and 64 channels; box_rows 0: none.
+struct TileMaps {
+    CUtensorMap k, v;
+    int box_rows;
 };
 cudaError_t attend_tiles_configure(int max_smem);
-cudaError_t launch_attend_tiles(const AttendArgs &a, const TileArgs &t, int dtype, int dp, cudaStream_t stream);
+cudaError_t launch_attend_tiles(const AttendArgs &a, const TileArgs &t, const TileMaps &m, int dtype, int dp,
+                                cudaStream_t stream);
 
 // Merge of the chunks' states into `out`, with those of the shared positions where `t` is given.
 cudaError_t launch_attend_merge(const AttendArgs &a, const TokenArgs &w, const TileArgs *t, int dtype, int dp,

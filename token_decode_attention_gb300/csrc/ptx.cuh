@@ -137,6 +137,15 @@ __device__ __forceinline__ void tensor3d_g2s(void *dst, const void *tmap, int c0
         : "memory");
 }
 
+// A box of a 3D tensor map (a __grid_constant__ argument), without an L2 policy.
+__device__ __forceinline__ void box_g2s(uint32_t dst, const void *tmap, int c0, int c1, int c2, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(c0), "r"(c1), "r"(c2), "r"(smem_addr(bar))
+        : "memory");
+}
+
 // L2 prefetch of one 3D box of a tensor map (a hint, like bulk_prefetch_l2).
 __device__ __forceinline__ void tensor3d_prefetch_l2(const void *tmap, int c0, int c1, int c2) {
     asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(
@@ -169,10 +178,10 @@ __device__ __forceinline__ void cp_async_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One arrival of the calling thread on `bar` when its copies so far are done (one of the
-// arrivals that the barrier was set up for).
-__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+// `bar` stays in its phase until the calling thread's copies so far are done: one more
+// arrival, which comes then.  The phase must lack another arrival meanwhile.
+__device__ __forceinline__ void cp_async_hold(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
 }
 
 // Thread-block clusters: rank of this CTA in its cluster, the address of the
