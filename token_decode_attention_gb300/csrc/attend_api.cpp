@@ -360,6 +360,7 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
             while (s.page_size % m.box_rows != 0) m.box_rows /= 2;
         if (m.box_rows < kBoxRows) m.box_rows = 0;
         t.align = s.page_size > 0 && m.box_rows > 0 ? m.box_rows : 1;
+        t.out_32 = s.head_dim % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 31u) == 0 ? 1 : 0;
         if (m.box_rows > 0) {
             const long long map_rows = s.apart ? s.shared : static_cast<long long>(rows);
             for (auto &[map, base] : {std::pair{&m.k, s.apart ? Kp : K}, std::pair{&m.v, s.apart ? Vp : V}})

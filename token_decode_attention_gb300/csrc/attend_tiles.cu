@@ -103,7 +103,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttendArgs a, 
     }
 }
 
-constexpr int kJoinWarps = 4, kJoinRows = 32;  // rows of a CTA
+constexpr int kJoinWarps = 4, kJoinRows = 8;  // rows of a CTA
 
 // The pieces of the item that CTA boundary c cuts first, into `out`.  A warp takes a row,
 // lanes four channels each.

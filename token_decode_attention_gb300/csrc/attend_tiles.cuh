@@ -47,13 +47,18 @@ __device__ __forceinline__ long long units_before(const TileArgs &t, const Share
     return s.uniform ? static_cast<long long>(item) * s.uniform : t.before[item];
 }
 
-// The item that holds unit x of a key/value head.
+// The item that holds unit x of a key/value head, found by a whole warp: 32 items are
+// looked at in a round, so that a round trip to memory leaves a 32nd of them.
 __device__ __forceinline__ int item_at(const TileArgs &t, const Shares &s, long long x) {
     if (s.uniform) return static_cast<int>(x / s.uniform);
-    int lo = 0, hi = s.items;
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        (t.before[mid] <= x ? lo : hi) = mid;
+    const int lane = threadIdx.x & 31;
+    int lo = 0, n = s.items;
+    while (n > 1) {
+        const int step = (n + 31) / 32, i = lo + lane * step;
+        const unsigned below = __ballot_sync(0xffffffffu, lane * step < n && t.before[i] <= x);
+        const int last = 31 - __clz(below);  // lane 0's begins at or before x
+        lo += last * step;
+        n = min(step, n - last * step);
     }
     return lo;
 }

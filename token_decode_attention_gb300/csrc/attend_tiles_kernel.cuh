@@ -54,8 +54,7 @@ struct TileShape {
     static constexpr int kSlotBytes = kKeys * DP * 2;  // K or V of a tile
     static constexpr int kSlots = DP == 64 ? 8 : DP == 128 ? 5 : 5;
     static constexpr int kColS = 0, kColO = 2 * kKeys;  // tensor memory columns
-    static constexpr int kParts = 4;  // of a tile's keys, whose P is handed over by itself
-    static constexpr int kBars = 2 * kSlots + 9 + 2 * kParts;
+    static constexpr int kBars = 2 * kSlots + 11;
     static constexpr int kSmem = kStacks * kQBytes + kSlots * kSlotBytes + 1024;
 };
 
@@ -140,9 +139,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
     uint64_t *const q_full = bars + 2 * Z::kSlots, *const q_free = q_full + 1;
     uint64_t *const s_two = q_full + 2;   // [2] S of a stack is there (items of two stacks)
     uint64_t *const s_one = q_full + 4;   // [2] S of a buffer is there (items of one)
-    uint64_t *const o_done = q_full + 6;  // [2] O of a stack has its last tile
+    uint64_t *const o_done = q_full + 6;  // [2] O of a stack has its last tile (items of one stack: each)
     uint64_t *const drained = q_full + 8;
-    uint64_t *const p_full = q_full + 9;  // [2][kParts] a part of P of a buffer is there
+    uint64_t *const p_full = q_full + 9;  // [2] P of a buffer is there
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t q_smem = (smem_addr(smem_raw) + 1023u) & ~1023u;
@@ -159,9 +158,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_two + i, 1);
             mbar_init(s_one + i, 1);
+            mbar_init(p_full + i, 4);  // the stack's warps
             mbar_init(o_done + i, 1);
         }
-        for (int i = 0; i < 2 * Z::kParts; ++i) mbar_init(p_full + i, 4);  // the stack's warps
         mbar_init(drained, 1);
         fence_barrier_init();
     }
@@ -197,7 +196,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
         return last;
     };
 
-    // A softmax thread holds a row's scores of a tile; the registers come from the others:
     // 256 x 200 + 128 x 104 = 384 x 168, what the launch gave.
     if (warp < 8)
         asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -208,11 +206,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
         const int stack = warp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // lane 32 (warp % 4)
         const uint32_t col_o = tmem + lanes + Z::kColO + stack * DP;
-        uint32_t n_two = 0, n_one[2] = {0, 0}, n_o = 0;
+        uint32_t n_two = 0, n_one[2] = {0, 0}, n_o = 0, base = 0;
         bool ok = true;
         while (ok && some && walk.next(t, shares)) {
             const TileItem it = attend::item_of(a, t, shares, tile_rows(DP), walk.item);
             const int stacks = stacks_of(it);
+            const uint32_t begun = base;  // steps of the CTA before the item's
+            base += stacks * (walk.j1 - walk.j0);
             if (stack >= stacks) continue;
             const int r0 = stack * 128, r1 = min(it.rows, r0 + 128);
             const int tok = fast_div(it.head + r0 + row, t.div_group);
@@ -229,37 +229,43 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
             bool hidden = false;  // some row of the warp does not see some position
             for (int j = walk.j0; j < walk.j1; ++j) {
                 const int n = j - walk.j0;
-                const int buf = stacks == 2 ? stack : n & 1;
+                const int buf = (begun + (stacks == 2 ? stack : n)) & 1;
                 uint64_t *const full = stacks == 2 ? s_two + stack : s_one + buf;
                 uint32_t &phase = stacks == 2 ? n_two : n_one[buf];
                 if (!(ok = wait_warp(full, phase & 1, kErrConsumerWait))) break;
                 ++phase;
                 tc::fence_after();
                 const uint32_t col_s = tmem + lanes + Z::kColS + buf * kKeys;
+                // The loads bring the row's maximum along.  Tiles with hidden positions, a few
+                // of an item, are masked in a small loop of their own, in tensor memory:
+                // code that is large in all roles together starves for instructions.
                 uint32_t sv[kKeys];
-#pragma unroll
-                for (int c = 0; c < kKeys; c += 32) tc::ld32(sv + c, col_s + c);
-                tc::wait_ld();
                 const int x0 = j * kKeys;
                 if (all.cuts(x0, x0 + kKeys)) {
                     hidden = true;
-#pragma unroll
+#pragma unroll 1
                     for (int c = 0; c < kKeys; c += 32) {
+                        tc::ld32(sv, col_s + c);
                         const uint32_t h = e.hidden32(x0 + c);
+                        tc::wait_ld();
 #pragma unroll
                         for (int k = 0; k < 32; ++k)
-                            if (h >> k & 1) sv[c + k] = 0xff800000u;  // -infinity
+                            if (h >> k & 1) sv[k] = 0xff800000u;  // -infinity
+                        tc::st32(col_s + c, sv);
                     }
+                    tc::wait_st();
                 }
-                float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                float m[kKeys / 32];
 #pragma unroll
-                for (int c = 0; c < kKeys; c += 2)
-                    m4[(c >> 1) & 3] = max3(m4[(c >> 1) & 3], __uint_as_float(sv[c]), __uint_as_float(sv[c + 1]));
-                const float top = max3(fmaxf(m4[0], m4[1]), m4[2], m4[3]) * a.qscale;
+                for (int c = 0; c < kKeys / 32; ++c) m[c] = tc::ld32_max(sv + 32 * c, col_s + 32 * c);
+                tc::wait_ld();
+                float top = fmaxf(m[0], m[1]);
+                if constexpr (kKeys == 128) top = max3(top, m[2], m[3]);
+                top *= a.qscale;
                 // With one stack the last product with V may still run, with two it is done:
                 // this S was issued behind it.
                 bool running = stacks == 1 && n > 0;
-                n_o += n > 0;
+                n_o += running;
                 auto product_done = [&]() {
                     running = false;
                     ok = wait_warp(o_done + stack, (n_o - 1) & 1, kErrConsumerWait);
@@ -274,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     l *= f;
                     if (running && !product_done()) break;
                     if (n > 0) {
-#pragma unroll
+#pragma unroll 1
                         for (int c = 0; c < DP; c += 32) {
                             if (c >= a.D) break;
                             uint32_t o[32];
@@ -289,27 +295,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                 const float ref = M == -INFINITY ? 0.f : M;
                 const float2 scale2 = make_float2(a.qscale, a.qscale), ref2 = make_float2(-ref, -ref);
                 float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-                constexpr int kPart = kKeys / Z::kParts;
 #pragma unroll
-                for (int part = 0; part < Z::kParts; ++part) {
+                for (int part = 0; part < kKeys; part += 32) {
 #pragma unroll
-                    for (int c = part * kPart; c < (part + 1) * kPart; c += 2) {
+                    for (int c = part; c < part + 32; c += 2) {
                         float2 p = fma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), scale2, ref2);
                         p.x = ex2(p.x);
                         p.y = ex2(p.y);
                         l2[(c >> 1) & 1] = add2(l2[(c >> 1) & 1], p);
                         sv[c / 2] = Pair<T>::narrow(p.x, p.y);
                     }
-                    if constexpr (kPart == 32) tc::st16(col_s + part * 16, sv + part * 16);
-                    else tc::st8(col_s + part * 8, sv + part * 8);
-                    tc::wait_st();
-                    // its phases are not to be passed over
-                    if (part == Z::kParts - 1 && running && !product_done()) break;
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(p_full + buf * Z::kParts + part);
+                    tc::st16(col_s + part / 2, sv + part / 2);  // over S
                 }
-                if (!ok) break;
+                tc::wait_st();
+                if (running && !product_done()) break;  // its phases are not to be passed over
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + buf);
                 l2[0] = add2(l2[0], l2[1]);
                 l += l2[0].x + l2[0].y;
             }
@@ -330,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
             float *const state = uniform && whole ? t.whole_acc + out_row * a.D : t.acc + slot_row * a.D;
             float2 *const state_ml = uniform && whole ? t.whole_ml + out_row : t.ml + slot_row;
             const bool to_out = whole && !uniform;
-#pragma unroll
+#pragma unroll 1
             for (int c = 0; c < DP; c += 32) {
                 if (c >= a.D) break;
                 uint32_t o[32];
@@ -338,25 +340,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                 tc::wait_ld();
                 if (!mine) continue;
 #pragma unroll
-                for (int k = 0; k < 32; k += 8) {
-                    if (c + k >= a.D) break;
-                    float y[8];
+                for (int k = 0; k < 32; ++k) nan |= c + k < a.D && __uint_as_float(o[k]) != __uint_as_float(o[k]);
+                if (!to_out) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        y[i] = __uint_as_float(o[k + i]);
-                        nan |= y[i] != y[i];
+                    for (int k = 0; k < 32; k += 8)
+                        if (c + k < a.D) st_global_v8(state + c + k, o + k);
+                    continue;
+                }
+                T *const out = static_cast<T *>(a.out) + out_row * a.D + c;
+#pragma unroll
+                for (int k = 0; k < 32; k += 2)
+                    o[k / 2] = Pair<T>::narrow(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv);
+#pragma unroll
+                for (int k = 0; k < 32; k += 16) {
+                    if (t.out_32 && c + k + 8 < a.D) {
+                        st_global_v8(out + k, o + k / 2);
+                        continue;
                     }
-                    if (to_out) {
-                        uint4 w;
-                        w.x = Pair<T>::narrow(y[0] * inv, y[1] * inv);
-                        w.y = Pair<T>::narrow(y[2] * inv, y[3] * inv);
-                        w.z = Pair<T>::narrow(y[4] * inv, y[5] * inv);
-                        w.w = Pair<T>::narrow(y[6] * inv, y[7] * inv);
-                        *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + out_row * a.D + c + k) = w;
-                    } else {
-                        *reinterpret_cast<float4 *>(state + c + k) = make_float4(y[0], y[1], y[2], y[3]);
-                        *reinterpret_cast<float4 *>(state + c + k + 4) = make_float4(y[4], y[5], y[6], y[7]);
-                    }
+#pragma unroll
+                    for (int h = 0; h < 16; h += 8)
+                        if (c + k + h < a.D)
+                            *reinterpret_cast<uint4 *>(out + k + h) =
+                                make_uint4(o[(k + h) / 2], o[(k + h) / 2 + 1], o[(k + h) / 2 + 2], o[(k + h) / 2 + 3]);
                 }
             }
             tc::fence_before();  // O has been read before the next item's first P is handed over
@@ -423,31 +428,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
         while (ok && some && walk.next(t, shares)) {
             const TileItem it = attend::item_of(a, t, shares, tile_rows(DP), walk.item);
             const int stacks = stacks_of(it);
-            if (number > 0 && !(ok = wait_warp(q_free, (number - 1) & 1, kErrProducerWait))) break;
-            ++number;
-            for (int g = lw; g < stacks * 8; g += kLoadWarps) {
-                // 16 rows: lane l (and l + 16) finds row l's address, 0 for zeros
-                const int r = g * 16 + (lane & 15);
-                unsigned long long row = 0;
-                if (r < it.rows) {
-                    const int tok = fast_div(it.head + r, t.div_group);
-                    const int h = walk.kvh * a.group + (it.head + r - tok * a.group);
-                    row = reinterpret_cast<unsigned long long>(a.Q) +
-                          ((it.token + static_cast<long long>(tok)) * a.q_stride + static_cast<long long>(h) * a.D) * 2;
-                }
-                const uint32_t tile = q_smem + (g >> 3) * Z::kQBytes;
-                unsigned long long from[kCopies];
-#pragma unroll
-                for (int i = 0; i < kCopies; ++i) from[i] = __shfl_sync(kFull, row, i * kRowsCopy + crow);
-                if (!in_row) continue;
-#pragma unroll
-                for (int i = 0; i < kCopies; ++i) {
-                    const bool there = from[i] != 0 && in_head;
-                    cp_async16(tile + swizzled(128, (g & 7) * 16 + i * kRowsCopy + crow, cc),
-                               there ? reinterpret_cast<const void *>(from[i] + cc * 16) : a.Q, there ? 16 : 0);
-                }
-            }
-            arrive(q_full);
             const attend::Counted counted{it.lo, it.n - it.first};
             const unsigned row_bytes = static_cast<unsigned>(a.Hk) * a.D * 2;
             const size_t col = (static_cast<size_t>(walk.kvh) * a.D + (in_head ? cc * 8 : 0)) * 2;
@@ -479,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                         }
                     }
                 }
-#pragma unroll
+#pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
                     const int slot = used % Z::kSlots;
                     const uint32_t round = used / Z::kSlots;
@@ -513,6 +493,35 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     }
                     arrive(kv_full + slot);
                 }
+                if (!ok) break;
+                if (j > walk.j0) continue;
+                // the item's queries, behind its first tile: the last item's products may still
+                // read theirs
+                if (number > 0 && !(ok = wait_warp(q_free, (number - 1) & 1, kErrProducerWait))) break;
+                ++number;
+                for (int g = lw; g < stacks * 8; g += kLoadWarps) {
+                    // 16 rows: lane l (and l + 16) finds row l's address, 0 for zeros
+                    const int r = g * 16 + (lane & 15);
+                    unsigned long long row = 0;
+                    if (r < it.rows) {
+                        const int tok = fast_div(it.head + r, t.div_group);
+                        const int h = walk.kvh * a.group + (it.head + r - tok * a.group);
+                        row = reinterpret_cast<unsigned long long>(a.Q) +
+                              ((it.token + static_cast<long long>(tok)) * a.q_stride + static_cast<long long>(h) * a.D) * 2;
+                    }
+                    const uint32_t tile = q_smem + (g >> 3) * Z::kQBytes;
+                    unsigned long long from[kCopies];
+#pragma unroll
+                    for (int i = 0; i < kCopies; ++i) from[i] = __shfl_sync(kFull, row, i * kRowsCopy + crow);
+                    if (!in_row) continue;
+#pragma unroll
+                    for (int i = 0; i < kCopies; ++i) {
+                        const bool there = from[i] != 0 && in_head;
+                        cp_async16(tile + swizzled(128, (g & 7) * 16 + i * kRowsCopy + crow, cc),
+                                   there ? reinterpret_cast<const void *>(from[i] + cc * 16) : a.Q, there ? 16 : 0);
+                    }
+                }
+                arrive(q_full);
             }
         }
         // what was asked for has arrived before the shared memory is given up
@@ -528,63 +537,88 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
             constexpr uint32_t kIdescS = tc::instr_desc(128, kKeys, kBf16, false);
             const uint32_t idesc_o = tc::instr_desc(128, (a.D + 15) / 16 * 16, kBf16, true);
             const int ksteps = (a.D + 15) / 16;
-            const uint64_t q_desc = tc::smem_desc(q_smem, 0), k_desc = tc::smem_desc(ring, 0);
-            const uint64_t v_desc = tc::smem_desc(ring, kKeys * 128);
-            uint32_t used = 0, n_p[2] = {0, 0};
-            int number = 0;
-            bool ok = true;
-            while (ok && some && walk.next(t, shares)) {
-                const TileItem it = attend::item_of(a, t, shares, tile_rows(DP), walk.item);
-                const int stacks = stacks_of(it);
-                const int steps = stacks * (walk.j1 - walk.j0);
-                auto scores = [&](int n) {
-                    const int j = stacks == 2 ? n >> 1 : n, stack = stacks == 2 ? n & 1 : 0, buf = n & 1;
-                    const uint32_t u = used + 2 * j;
-                    const int slot = u % Z::kSlots;
-                    if (stack == 0 && !wait(kv_full + slot, (u / Z::kSlots) & 1, kErrConsumerWait)) return false;
-                    tc::fence_async();  // what cp.async wrote is visible to the tensor cores
+            const uint32_t q_desc = tc::smem_desc(q_smem, 0), k_desc = tc::smem_desc(ring, 0);
+            const uint32_t v_desc = tc::smem_desc(ring, kKeys * 128);
+            // Steps are a tile of a stack.  Scores run two steps ahead of values and into the
+            // next item: while softmax works on an item's last tiles, the first products of
+            // the next are under way.  A step has the buffer of its parity in the CTA.
+            struct Steps {
+                attend::Walk walk;
+                int stacks, left;  // of the item; steps to come
+                int stack, first;  // the next step's; whether its tile is the piece's first
+                uint32_t buf, use;  // its buffer; its tile's use of the ring
+            };
+            auto begin = [&](Steps &x) {  // the next item, if there is one
+                if (!some || !x.walk.next(t, shares)) return false;
+                x.stacks = stacks_of(attend::item_of(a, t, shares, tile_rows(DP), x.walk.item));
+                x.left = x.stacks * (x.walk.j1 - x.walk.j0);
+                x.stack = 0;
+                x.first = 1;
+                return true;
+            };
+            auto arrived = [&](uint32_t use) {
+                if (!wait(kv_full + use % Z::kSlots, use / Z::kSlots & 1, kErrConsumerWait)) return false;
+                tc::fence_async();  // what cp.async wrote is visible to the tensor cores
+                tc::fence_after();
+                return true;
+            };
+            auto step_done = [&](Steps &x) {
+                x.buf ^= 1;
+                --x.left;
+                if (++x.stack < x.stacks) return;
+                tc::commit(kv_free + x.use % Z::kSlots);
+                x.use += 2;
+                x.stack = 0;
+                x.first = 0;
+            };
+            Steps sc{walk, 1, 0, 0, 1, 0, 0}, va{walk, 1, 0, 0, 1, 0, 1};
+            uint32_t p_phase = 0;  // bit b: parity of buffer b's next P
+            int ahead = 0, number = 0;
+            bool more = some;
+            while (true) {
+                if (ahead < 2 && more) {
+                    if (sc.left == 0) {
+                        if (!(more = begin(sc))) continue;
+                        if (!wait(q_full, number++ & 1, kErrConsumerWait)) break;
+                    }
+                    if (sc.stack == 0 && !arrived(sc.use)) break;
+                    uint32_t qd = q_desc + sc.stack * (Z::kQBytes >> 4);
+                    uint32_t kd = k_desc + sc.use % Z::kSlots * (Z::kSlotBytes >> 4);
+                    const uint32_t to = tmem + Z::kColS + sc.buf * kKeys;
+#pragma unroll 1
+                    for (int k = 0; k < ksteps; k += 4) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (k + i < ksteps) tc::mma(to, qd + 2 * i, kd + 2 * i, kIdescS, k + i > 0);
+                        qd += 128 * 128 >> 4;
+                        kd += kKeys * 128 >> 4;
+                    }
+                    tc::commit(sc.stacks == 2 ? s_two + sc.stack : s_one + sc.buf);
+                    step_done(sc);
+                    if (sc.left == 0) tc::commit(q_free);
+                    ++ahead;
+                } else if (ahead > 0) {
+                    if (va.left == 0 && !begin(va)) break;
+                    if (va.stack == 0 && !arrived(va.use)) break;
+                    uint32_t vd = v_desc + va.use % Z::kSlots * (Z::kSlotBytes >> 4);
+                    uint32_t from = tmem + Z::kColS + va.buf * kKeys;
+                    const uint32_t to = tmem + Z::kColO + va.stack * DP, phase = p_phase >> va.buf & 1;
+                    p_phase ^= 1u << va.buf;
+                    if (!wait(p_full + va.buf, phase, kErrConsumerWait)) break;
                     tc::fence_after();
-                    const uint64_t qd = q_desc + stack * (Z::kQBytes >> 4), kd = k_desc + slot * (Z::kSlotBytes >> 4);
-                    const uint32_t to = tmem + Z::kColS + buf * kKeys;
-#pragma unroll
-                    for (int k = 0; k < DP / 16; ++k) {
-                        if (k >= ksteps) break;
-                        tc::mma(to, qd + (((k >> 2) * (128 * 128) + (k & 3) * 32) >> 4),
-                                kd + (((k >> 2) * (kKeys * 128) + (k & 3) * 32) >> 4), kIdescS, k > 0);
+#pragma unroll 1
+                    for (int k = 0; k < kKeys / 16; k += 2) {
+                        tc::mma_tmem(to, from, vd, idesc_o, k > 0 || !va.first);
+                        tc::mma_tmem(to, from + 8, vd + (2048 >> 4), idesc_o, 1);
+                        from += 16;
+                        vd += 4096 >> 4;
                     }
-                    tc::commit((stacks == 2 ? s_two : s_one) + buf);
-                    if (stack == stacks - 1) tc::commit(kv_free + slot);
-                    if (n == steps - 1) tc::commit(q_free);
-                    return true;
-                };
-                auto values = [&](int n) {
-                    const int j = stacks == 2 ? n >> 1 : n, stack = stacks == 2 ? n & 1 : 0, buf = n & 1;
-                    const uint32_t u = used + 2 * j + 1;
-                    const int slot = u % Z::kSlots;
-                    if (stack == 0 && !wait(kv_full + slot, (u / Z::kSlots) & 1, kErrConsumerWait)) return false;
-                    const uint32_t phase = n_p[buf]++ & 1;
-                    tc::fence_async();
-                    const uint64_t vd = v_desc + slot * (Z::kSlotBytes >> 4);
-                    const uint32_t to = tmem + Z::kColO + stack * DP, from = tmem + Z::kColS + buf * kKeys;
-#pragma unroll
-                    for (int part = 0; part < Z::kParts; ++part) {
-                        if (!wait(p_full + buf * Z::kParts + part, phase, kErrConsumerWait)) return false;
-                        tc::fence_after();
-#pragma unroll
-                        for (int i = 0; i < kKeys / 16 / Z::kParts; ++i) {
-                            const int k = part * (kKeys / 16 / Z::kParts) + i;
-                            tc::mma_tmem(to, from + k * 8, vd + k * (2048 >> 4), idesc_o, j > 0 || k > 0);
-                        }
-                    }
-                    tc::commit(o_done + stack);
-                    if (stack == stacks - 1) tc::commit(kv_free + slot);
-                    return true;
-                };
-                ok = wait(q_full, number & 1, kErrConsumerWait);
-                ok = ok && scores(0) && (steps < 2 || scores(1));
-                for (int n = 0; n < steps && ok; ++n) ok = values(n) && (n + 2 >= steps || scores(n + 2));
-                used += 2 * (walk.j1 - walk.j0);
-                ++number;
+                    if (va.stacks == 1 || va.left <= 2) tc::commit(o_done + va.stack);  // a stack's last
+                    step_done(va);
+                    --ahead;
+                } else {
+                    break;
+                }
             }
             // nothing runs on when the tensor memory is given back
             tc::commit(drained);

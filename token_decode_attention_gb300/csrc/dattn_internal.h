@@ -381,7 +381,7 @@ cudaError_t launch_attend_token(const AttendArgs &a, const TokenArgs &w, int dty
 __host__ __device__ constexpr int tile_stacks(int dp) { return dp <= 128 ? 2 : 1; }  // of 128 rows
 __host__ __device__ constexpr int tile_rows(int dp) { return 128 * tile_stacks(dp); }
 __host__ __device__ constexpr int tile_keys(int dp) { return dp <= 128 ? 128 : 64; }
-constexpr int kTileMinUnits = 4;  // key tiles (and what an item adds) of a CTA, of which there are
+constexpr int kTileMinUnits = 2;  // key tiles (and what an item adds) of a CTA, of which there are
                                   // fewer for less work
 // Items of one key/value head (the same for each).
 struct TileItem {
@@ -410,6 +410,7 @@ struct TileArgs {
     FastDiv div_group;
     int ctas;                // CTAs at most
     int bound_ends;          // shared: a token may lie inside the shared positions
+    int out_32;              // rows of out begin on 32-byte boundaries
     int align;               // an item's `lo` is a multiple (a power of two)
 };
 // Tensor maps of K and V (of the shared positions' own tensors where there are such) as
