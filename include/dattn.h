@@ -544,12 +544,12 @@ int dattn_attend_paged(const void *Q, const void *K_pages, const void *V_pages, 
  *       current_pos[b] counts in that cache: the token is at row
  *       min(current_pos[b], seq_len-1) of it and sees the whole prefix
  *   dattn_decode_shared_paged  one pool of pages: the first shared_len positions are
- *       those of the first sequence's pages (its row of block_table; entries of the other
- *       rows for pages that hold shared positions only are not used), the others each
- *       sequence's own.  current_pos[b] counts from the first shared position; a token
+ *       those of the first sequence's pages (its row of block_table, where all of them
+ *       are; entries of the other rows for pages that hold shared positions only are not
+ *       used), the others each sequence's own.  current_pos[b] counts from the first shared position; a token
  *       inside them sees the shared positions up to its own
  * workspace as in dattn_attend, of dattn_decode_shared_workspace_bytes: own_len is
- * seq_len, or page_size * max_pages.
+ * seq_len, or page_size * max_pages - shared_len.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
  */
 int dattn_decode_shared_workspace_bytes(int batch, int n_heads, int n_kv_heads, int head_dim,

@@ -345,7 +345,8 @@ def test_captured_and_recorded_calls(i):
 
 def workspace_bytes(c):
     if c.shared:
-        return dattn.dattn_decode_shared_workspace_bytes(c.B, c.H, c.Hk, c.D, c.shared, c.S)
+        own = c.S - c.shared if c.page else c.S
+        return dattn.dattn_decode_shared_workspace_bytes(c.B, c.H, c.Hk, c.D, c.shared, own)
     return dattn.dattn_attend_workspace_bytes(c.B, c.q.shape[0], c.counts is not None, c.H, c.Hk, c.D, c.S,
                                               c.window, c.sinks)
 

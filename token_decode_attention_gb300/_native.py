@@ -1158,8 +1158,8 @@ def _attend(name, q, prefix, k, v, block_table, current_pos, token_offsets, shar
     elif allocate:
         capacity = rows * table_pages if table_pages else rows
         if shared:
-            wn = _attend_workspace("dattn_decode_shared_workspace_bytes", dev, batch, h, hk, d,
-                                   shared_len, capacity)
+            wn = _attend_workspace("dattn_decode_shared_workspace_bytes", dev, batch, h, hk, d, shared_len,
+                                   capacity if prefix is not None else max(0, capacity - shared_len))
         else:
             wn = _attend_workspace("dattn_attend_workspace_bytes", dev, batch, n,
                                    0 if token_offsets is None else 1, h, hk, d, capacity, window, sinks)

@@ -102,6 +102,8 @@ struct Plan {
     }
 };
 
+constexpr double kTileUs = 1.9;      // of an SM, for a key tile of 256 rows of 128 channels
+constexpr double kBytesUs = 6.8e6;   // of the GPU
 constexpr int kBoxRows = 8;  // fewest rows of a page's box
 constexpr int kMaxColumns = 16;  // query heads of a key/value head in one CTA
 constexpr int kStaticSmem = 1024;  // the kernel's static shared memory at most
@@ -198,7 +200,6 @@ int tiles_plan(const Shape &s, int cap, const dattn::DeviceFacts &df, Plan *p) {
     const long long all_rows = static_cast<long long>(s.tokens) * group;
     p->tiles = true;
     t.div_group = dattn::fast_div_of(group);
-    t.bound_ends = s.shared > 0 && !s.apart ? 1 : 0;
     const long long items = (all_rows + rows - 1) / rows + (s.ragged ? s.batch : 0);
     if (items > 0x7fffff00LL) return fail(DATTN_ERR_UNSUPPORTED, "the batch is too large");
     t.max_items = static_cast<int>(items);
@@ -206,7 +207,15 @@ int tiles_plan(const Shape &s, int cap, const dattn::DeviceFacts &df, Plan *p) {
     const long long seen = s.shared > 0 ? s.shared : std::min<long long>(s.rows, static_cast<long long>(cap) + rows);
     const double units = static_cast<double>(items) * s.n_kv_heads * ((seen + keys - 1) / keys + 1);
     if (units * 1024.0 > 4.0e18) return fail(DATTN_ERR_UNSUPPORTED, "the batch is too large");
-    t.ctas = static_cast<int>(std::max(1.0, std::min<double>(df.sms, units / dattn::kTileMinUnits)));
+    double ctas = df.sms;
+    if (s.shared > 0) {
+        // The sequences' own positions are worked on at the same time, on the other SMs: as
+        // many for each as it has work, a key tile against the bytes of sequences half full.
+        const double own_bytes = 2.0 * cap * s.batch * s.n_kv_heads * s.head_dim;
+        const double tiles_us = units * kTileUs * p->dp / 128, own_us = own_bytes / kBytesUs * df.sms;
+        ctas = std::max(1.0, df.sms * tiles_us / (tiles_us + own_us));
+    }
+    t.ctas = static_cast<int>(std::max(1.0, std::min(ctas, units / dattn::kTileMinUnits)));
     if (s.ragged) {
         p->t_plan = p->take(sizeof(dattn::TilePlan));
         p->t_items = p->take(sizeof(dattn::TileItem) * items);
@@ -228,15 +237,17 @@ int make_plan(const Shape &s, Plan *out) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return fail_cuda(e, "cudaGetDevice");
-    const int cap = s.window > 0 && s.window < s.rows
+    // positions of its own that a sequence's token sees at most
+    const int cap = s.shared > 0 ? std::max(1, s.apart ? s.rows : s.rows - s.shared)
+                    : s.window > 0 && s.window < s.rows
                         ? static_cast<int>(std::min<long long>(s.rows, static_cast<long long>(s.window) + s.sinks))
                         : s.rows;
-    using Key = std::tuple<int, int, int, bool, int, int, int, int, int, bool>;
+    using Key = std::tuple<int, int, int, bool, int, int, int, int, int>;
     static std::mutex mutex;
     static std::map<Key, Plan> plans;
     static std::map<int, bool> configured;
     const Key key{dev, s.batch, s.tokens, s.ragged, s.n_heads, s.n_kv_heads, s.head_dim, cap,
-                  s.shared, s.apart};
+                  s.shared};
     std::lock_guard<std::mutex> lock(mutex);
     const auto it = plans.find(key);
     if (it != plans.end()) {
@@ -344,6 +355,7 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
     dattn::TileArgs t = p.t;
     cudaError_t e = cudaSuccess;
     if (p.tiles) {
+        t.bound_ends = s.shared > 0 && !s.apart ? 1 : 0;
         if (s.ragged) {
             at(p.t_plan, t.plan);
             at(p.t_items, t.items);
@@ -465,9 +477,11 @@ int dattn_decode_shared_workspace_bytes(int batch, int n_heads, int n_kv_heads, 
                                         int own_len, size_t *bytes) {
     return guarded([&]() -> int {
         if (int st = check_shared(shared_len)) return st;
+        if (own_len < 0) return fail(DATTN_ERR_INVALID_ARG, "own_len=%d must not be negative", own_len);
         Shape s = shape_of(batch, batch, false, n_heads, n_kv_heads, head_dim);
         s.shared = shared_len;
-        s.rows = own_len;
+        s.apart = true;
+        s.rows = std::max(1, own_len);
         return workspace_of(s, bytes);
     });
 }

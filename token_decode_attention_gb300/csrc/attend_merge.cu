@@ -111,7 +111,13 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const AttendArgs a, 
 template <typename T>
 cudaError_t launch(const AttendArgs &a, const TokenArgs &w, const TileArgs &t, int dp, cudaStream_t stream) {
     const long long rows = static_cast<long long>(a.B) * a.H;
-    const bool many = w.chunks > 8 || (w.own_only && t.ctas > 8);
+    // states of a row: its chunks, and about as many pieces as CTAs share an item
+    long long states = w.chunks;
+    if (w.own_only) {
+        const long long items = (static_cast<long long>(a.B) * a.group + tile_rows(dp) - 1) / tile_rows(dp) * a.Hk;
+        states += 1 + t.ctas / items;
+    }
+    const bool many = states > 8;
     const long long blocks = many ? rows : (rows + kWarps - 1) / kWarps;
     if (blocks > 0x7fffffffLL) return cudaErrorInvalidValue;
     cudaLaunchConfig_t cfg = {};

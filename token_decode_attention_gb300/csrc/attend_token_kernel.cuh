@@ -112,7 +112,11 @@ __global__ void __launch_bounds__(kTokenWarps * 32, token_ctas_per_sm(DP))
     const int grp = static_cast<int>(unit) - b * w.head_groups;
 
     if constexpr (CLUSTER) cluster_arrive_relaxed();
-    pdl_wait_primary();
+    // Beside the kernel of the shared positions, which began when everything before it was
+    // done, nothing is waited for; the last CTA alone stays until that kernel has ended, so
+    // that what waits for this one has both.
+    const bool stays = w.own_only && blockIdx.x == gridDim.x - 1;
+    if (!w.own_only) pdl_wait_primary();
 
     Seen v = attend::seen_by(a, attend::live_end(a, b) - 1);
     if (w.own_only) v.lo = min(a.shared, v.end);  // the shared positions are another kernel's
@@ -125,7 +129,10 @@ __global__ void __launch_bounds__(kTokenWarps * 32, token_ctas_per_sm(DP))
     } else {
         from = min(chunk * w.chunk_tiles, tiles);
         to = min(from + w.chunk_tiles, tiles);
-        if (from >= to && chunk > 0) return;  // the merge knows how many chunks there are
+        if (from >= to && chunk > 0) {  // the merge knows how many chunks there are
+            if (stays) pdl_wait_primary();
+            return;
+        }
     }
 
     const int HG = w.heads_per_cta, PH = w.phases;
@@ -395,6 +402,7 @@ __global__ void __launch_bounds__(kTokenWarps * 32, token_ctas_per_sm(DP))
             if (ch == 0) w.ws_ml[r] = make_float2(top, lsum);
         }
     }
+    if (stays) pdl_wait_primary();
     if constexpr (CLUSTER) {
         cluster_sync_all();  // every record has arrived
         for (int j = tid; j < share; j += kThreads) {
