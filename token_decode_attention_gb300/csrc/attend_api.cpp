@@ -92,7 +92,7 @@ struct Plan {
     dattn::TileArgs t{};
     size_t ws_bytes = 0;
     // where the parts of the workspace begin
-    size_t ws_acc = 0, ws_ml = 0, t_plan = 0, t_items = 0, t_before = 0, t_seq = 0, t_acc = 0, t_ml = 0,
+    size_t ws_acc = 0, ws_ml = 0, t_plan = 0, t_items = 0, t_before = 0, t_seq = 0, t_cuts = 0, t_acc = 0, t_ml = 0,
            t_whole_acc = 0, t_whole_ml = 0;
 
     size_t take(size_t bytes) {
@@ -220,6 +220,7 @@ int tiles_plan(const Shape &s, int cap, const dattn::DeviceFacts &df, Plan *p) {
         p->t_plan = p->take(sizeof(dattn::TilePlan));
         p->t_items = p->take(sizeof(dattn::TileItem) * items);
         p->t_before = p->take(sizeof(long long) * (items + 1));
+        p->t_cuts = p->take(sizeof(dattn::TileCut) * t.ctas);
         p->t_seq = p->take(sizeof(int) * (static_cast<size_t>(s.batch) + 1));
     } else {
         const size_t states = static_cast<size_t>(s.batch) * s.n_heads;
@@ -361,6 +362,7 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
             at(p.t_items, t.items);
             at(p.t_before, t.before);
             at(p.t_seq, t.seq_items);
+            at(p.t_cuts, t.cuts);
         } else {
             at(p.t_whole_acc, t.whole_acc);
             at(p.t_whole_ml, t.whole_ml);

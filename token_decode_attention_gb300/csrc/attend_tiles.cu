@@ -105,8 +105,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const AttendArgs a, 
 
 constexpr int kJoinWarps = 4, kJoinRows = 8;  // rows of a CTA
 
-// The pieces of the item that CTA boundary c cuts first, into `out`.  A warp takes a row,
-// lanes four channels each.
+// The pieces of the item that the beginning of CTA c's share is the first to cut, into
+// `out`.  A warp takes a row, lanes four channels each.
 template <typename T>
 __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs a, const TileArgs t, int dp) {
     const int parts = tile_rows(dp) / kJoinRows;
@@ -114,14 +114,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) join_kernel(const AttendArgs 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait_primary();
     pdl_launch_dependents();
-    const attend::Shares s = attend::shares_of(a, t, dp);
-    if (c >= s.ctas || s.items == 0) return;
-    const long long x = range_begin(c, s.all, s.ctas);
-    const int kvh = static_cast<int>(x / s.total);
-    const int item = attend::item_at(t, s, x - kvh * s.total);
-    const int2 who = attend::holders(s, kvh, attend::units_before(t, s, item), attend::units_before(t, s, item + 1));
-    if (who.x != c - 1 || who.y < c) return;
-    const TileItem it = attend::item_of(a, t, s, tile_rows(dp), item);
+    const TileCut cut = t.cuts[c];
+    if (cut.first < 0) return;
+    const int2 who = make_int2(cut.first, cut.last);
+    const int kvh = cut.kvh;
+    const int4 *const at = reinterpret_cast<const int4 *>(t.items + cut.item);
+    const int4 x0 = at[0], x1 = at[1];
+    const TileItem it{x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
     for (int r = part * kJoinRows + warp; r < min(it.rows, (part + 1) * kJoinRows); r += kJoinWarps) {
         const int tok = fast_div(it.head + r, t.div_group);
         const long long row = (it.token + static_cast<long long>(tok)) * a.H +

@@ -177,6 +177,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
     attend::Walk walk{};
     const bool some = cta < shares.ctas && shares.items > 0;
     if (some) walk.start(t, shares, cta);
+    if (!uniform && tid == kThreads - 1) {
+        // an item whose first tiles are the CTA's before has its pieces merged by join_kernel
+        TileCut cut{0, 0, -1, 0};
+        if (some && cta > 0 && walk.x < walk.x1) {
+            const int2 who = attend::holders(shares, walk.kvh, walk.at, walk.end);
+            if (who.x == cta - 1 && who.y >= cta) cut = TileCut{walk.kvh, walk.item, who.x, who.y};
+        }
+        t.cuts[cta] = cut;
+    }
 
     // A wait that ran out is recorded; every role then leaves its loop, warps as a whole.
     auto wait = [&](uint64_t *bar, uint32_t parity, unsigned code) {

@@ -391,6 +391,10 @@ struct TileItem {
     int lo, first;    // positions that some row sees: n - first from `lo` on, then [0, first)
     int n;
 };
+// An item of key/value head kvh that CTAs first .. last share; first -1: none.
+struct TileCut {
+    int kvh, item, first, last;
+};
 // What the planning kernel leaves ahead of the items.
 struct TilePlan {
     long long total;  // key tiles of the items of one key/value head, and what an item adds
@@ -403,6 +407,7 @@ struct TileArgs {
     long long *before;       // [items + 1] tiles (and what an item adds) ahead of each item
     int *seq_items;          // [B + 1] items ahead of each sequence
     int max_items;
+    TileCut *cuts;           // [ctas] what the beginning of a CTA's share is the first to cut
     float *acc;              // [2 ctas, tile_rows, D] states of pieces of items
     float2 *ml;              // [2 ctas, tile_rows]
     float *whole_acc;        // shared: [B,H,D] states of items that one CTA held
