@@ -517,7 +517,7 @@ int dattn_decode_paged_q8(const void *Q, const void *K_pages, const void *V_page
  * workspace: device scratch, 16-byte aligned, of dattn_attend_workspace_bytes (`ragged`
  * non-zero where token_offsets is given; NULL where that is 0); calls on different
  * streams need different ones.  head_dim: a multiple of 8, at most 256; tokens x n_heads
- * below 2^31.
+ * below 2^31; a sequence has fewer than 2^31 - 1024 positions, a cache fewer than 2^31.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.
  */
 int dattn_attend_workspace_bytes(int batch, int tokens, int ragged, int n_heads, int n_kv_heads,

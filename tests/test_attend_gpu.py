@@ -250,6 +250,77 @@ def test_equal_scores_of_the_lowest_value():
     Case("bf16", 4, 2, 64, 200, [199, 7], seed=23, edit=edit).check()
 
 
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("page", [0, 24, 64])
+def test_bad_values_in_pieces_that_ctas_share(D, page):
+    """Long contexts of few rows, cut among CTAs: a value that is not finite lies where some
+    rows see it and others do not, and behind what any row sees."""
+    def edit(c):
+        for p, bad in ((2390, float("inf")), (2396, float("nan")), (2402, float("nan")), (700, -float("inf"))):
+            at = c.at(0, p)
+            c.v[at][:, 3] = bad
+            c.k[at][1, 2] = bad
+    c = Case("bf16", 8, 2, D, 2496, [2400, 1500], counts=[20, 1], page=page, window=1700, sinks=3, seed=33, edit=edit)
+    got, (ref, tol) = c.run(), c.expected()
+    fine = (got.double() - ref).abs() <= tol
+    for i in range(20):
+        p = 2381 + i
+        sees = [x for x in (2390, 2396) if x <= p] + ([700] if 700 > p - 1700 else [])
+        if not sees:
+            assert bool(fine[i].all())
+        else:
+            assert bool(fine[i, :4, :3].all()) and bool(fine[i, :4, 4:].all())  # the other channels of head 0
+            assert not bool(torch.isfinite(got[i, :4, 3]).any())
+    assert bool(fine[20].all())
+
+
+@pytest.mark.parametrize("page", [0, 48])
+def test_bad_values_in_a_shared_prefix(page):
+    """Tokens inside the shared positions see only what is before them."""
+    if page:
+        def edit(c):
+            c.v[c.at(0, 1000)][0, 5] = float("nan")
+            c.v[c.at(0, 1500)][1, 6] = float("inf")
+        last = [999, 1000, 1499, 1500, 1700, 3, 1600]
+        c = Case("f16", 8, 2, 128, 1728, last, page=page, shared=1600, seed=34, edit=edit)
+    else:
+        def edit(c):
+            c.vp[1000, 0, 5] = float("nan")
+            c.v[2, 7, 1, 6] = float("inf")  # behind sequence 2's live positions
+        last = [9, 0, 6, 3]
+        c = Case("f16", 8, 2, 128, 10, last, shared=1600, seed=34, edit=edit)
+    got, (ref, tol) = c.run(), c.expected()
+    finite = torch.isfinite(ref)
+    assert torch.equal(torch.isnan(ref), torch.isnan(got.double()))
+    assert bool(((got.double() - ref).abs() <= tol)[finite].all())
+
+
+def test_offsets_past_32_bits():
+    """Caches of more than 2^32 bytes, the live rows at their far end."""
+    S, Hk, D, H = 700000, 8, 256, 16
+    k, v = (torch.zeros((2, S, Hk, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    assert k.numel() > 2 ** 31
+    small = Case("bf16", H, Hk, D, 128, [127, 100], counts=[3, 2], window=60, sinks=2, seed=35)
+    tail = S - 128  # the small case's positions from 64 on lie there, its sinks at the beginning
+    for big, x in ((k, small.k), (v, small.v)):
+        big[:, tail:] = x.cuda()
+        big[:, :2] = x[:, :2].cuda()
+    ref, tol = small.expected()
+    d = small.cuda()
+    pos = d["pos"] + tail
+    got = dattn.attend(d["q"], k, v, pos, window=60, sinks=2, token_offsets=d["offsets"]).cpu().double()
+    assert bool(((got - ref).abs() <= tol).all())
+    # one token each: the last of either sequence
+    pick = torch.tensor([2, 4])
+    got = dattn.attend(d["q"][pick.cuda()].contiguous(), k, v, pos, window=60, sinks=2).cpu().double()
+    assert bool(((got - ref[pick]).abs() <= tol[pick]).all())
+    # the same rows as pages of 100 positions
+    table = torch.arange(2 * S // 100, dtype=torch.int32, device="cuda").view(2, -1)
+    got = dattn.attend(d["q"], k.view(-1, 100, Hk, D), v.view(-1, 100, Hk, D), pos, window=60, sinks=2,
+                       token_offsets=d["offsets"], block_table=table).cpu().double()
+    assert bool(((got - ref).abs() <= tol).all())
+
+
 # ----------------------------------------------------------------- the calls
 
 @pytest.mark.parametrize("counts,shared", [(None, 0), ([20, 3], 0), (None, 50)])

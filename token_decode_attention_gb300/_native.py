@@ -1036,33 +1036,35 @@ _BF16 = torch.bfloat16
 _ATTEND_WORKSPACE: dict[tuple, int] = {}  # the size depends on the shape and the device only
 
 
-def _attend_workspace(query: str, dev: int, *key) -> int:
-    n = _ATTEND_WORKSPACE.get((query, dev, key))
-    if n is None:
-        size = ctypes.c_size_t(0)
-        _check(getattr(load(), query)(*key, ctypes.byref(size)), query)
-        if len(_ATTEND_WORKSPACE) >= 1024:  # a program that never repeats a shape
-            _ATTEND_WORKSPACE.clear()
-        n = _ATTEND_WORKSPACE[query, dev, key] = int(size.value)
+def _attend_workspace(key: tuple) -> int:
+    """Bytes for (device, shared, the arguments of the size query); `shared` tells the two
+    queries apart."""
+    size = ctypes.c_size_t(0)
+    query = "dattn_decode_shared_workspace_bytes" if key[1] else "dattn_attend_workspace_bytes"
+    _check(getattr(load(), query)(*key[2:], ctypes.byref(size)), query)
+    if len(_ATTEND_WORKSPACE) >= 1024:  # a program that never repeats a shape
+        _ATTEND_WORKSPACE.clear()
+    n = _ATTEND_WORKSPACE[key] = int(size.value)
     return n
 
 
 def dattn_attend_workspace_bytes(batch: int, tokens: int, ragged: bool, n_heads: int, n_kv_heads: int,
                                  head_dim: int, seq_len: int, window: int = 0, sinks: int = 0) -> int:
-    return _attend_workspace("dattn_attend_workspace_bytes", _device(), batch, tokens,
-                             1 if ragged else 0, n_heads, n_kv_heads, head_dim, seq_len, window, sinks)
+    return _attend_workspace((_device(), False, batch, tokens, 1 if ragged else 0, n_heads, n_kv_heads,
+                              head_dim, seq_len, window, sinks))
 
 
 def dattn_decode_shared_workspace_bytes(batch: int, n_heads: int, n_kv_heads: int, head_dim: int,
                                         shared_len: int, own_len: int) -> int:
-    return _attend_workspace("dattn_decode_shared_workspace_bytes", _device(), batch, n_heads,
-                             n_kv_heads, head_dim, shared_len, own_len)
+    return _attend_workspace((_device(), True, batch, n_heads, n_kv_heads, head_dim, shared_len, own_len))
 
 
 def _attend(name, q, prefix, k, v, block_table, current_pos, token_offsets, shared_len, window, sinks,
             out, workspace, stream, allocate):
     """Checks and marshalling of dattn_attend and dattn_decode_shared (`prefix`: a pair of
     tensors, or `shared_len` positions of the first sequence's pages)."""
+    if window >> 31 or sinks >> 31 or (shared_len or 0) >> 31:
+        raise ValueError(f"window={window}, sinks={sinks} and shared_len={shared_len} must be from 0 to 2^31 - 1")
     dev = _device()
     fresh = out is None and allocate
     kp, vp = prefix or (None, None)
@@ -1158,11 +1160,13 @@ def _attend(name, q, prefix, k, v, block_table, current_pos, token_offsets, shar
     elif allocate:
         capacity = rows * table_pages if table_pages else rows
         if shared:
-            wn = _attend_workspace("dattn_decode_shared_workspace_bytes", dev, batch, h, hk, d, shared_len,
-                                   capacity if prefix is not None else max(0, capacity - shared_len))
+            key = (dev, True, batch, h, hk, d, shared_len,
+                   capacity if prefix is not None else max(0, capacity - shared_len))
         else:
-            wn = _attend_workspace("dattn_attend_workspace_bytes", dev, batch, n,
-                                   0 if token_offsets is None else 1, h, hk, d, capacity, window, sinks)
+            key = (dev, False, batch, n, 0 if token_offsets is None else 1, h, hk, d, capacity, window, sinks)
+        wn = _ATTEND_WORKSPACE.get(key)
+        if wn is None:
+            wn = _attend_workspace(key)
     if _RECORDING and handle in _RECORDING and (fresh or (wn and wp is None)) and allocate:
         raise ValueError(f"a recorded call needs buffers that outlive the batch: pass out and "
                          f"workspace (dattn_{name}_workspace_bytes)")

@@ -243,12 +243,12 @@ int make_plan(const Shape &s, Plan *out) {
                     : s.window > 0 && s.window < s.rows
                         ? static_cast<int>(std::min<long long>(s.rows, static_cast<long long>(s.window) + s.sinks))
                         : s.rows;
-    using Key = std::tuple<int, int, int, bool, int, int, int, int, int>;
+    using Key = std::tuple<int, int, int, bool, int, int, int, int, int, int>;
     static std::mutex mutex;
     static std::map<Key, Plan> plans;
     static std::map<int, bool> configured;
     const Key key{dev, s.batch, s.tokens, s.ragged, s.n_heads, s.n_kv_heads, s.head_dim, cap,
-                  s.shared};
+                  s.shared > 0 ? 0 : s.rows, s.shared};
     std::lock_guard<std::mutex> lock(mutex);
     const auto it = plans.find(key);
     if (it != plans.end()) {

@@ -40,6 +40,7 @@ using attend::Seen;
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kLoadWarps = 3, kThreads = 384;
+constexpr int kAgainWaits = 100;  // time limits of a wait while rows are computed again
 constexpr unsigned kNoRow = 0xffffffffu;  // zeros (a cache has fewer than 2^31 rows)
 // The running maximum M is kept kHeadroom (log2) below the largest exponent when it was set
 // and moved when one exceeds M + kTrigger: weights lie below 2^12 (f16 holds up to 65504)
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t bars[Z::kBars];
     __shared__ uint32_t s_tmem;
+    __shared__ int s_again;  // warps that compute rows again
 
     uint64_t *const kv_full = bars, *const kv_free = bars + Z::kSlots;
     uint64_t *const q_full = bars + 2 * Z::kSlots, *const q_free = q_full + 1;
@@ -163,6 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
         }
         mbar_init(drained, 1);
         fence_barrier_init();
+        s_again = 0;
     }
     tc::fence_before();
     __syncthreads();
@@ -188,8 +191,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
     }
 
     // A wait that ran out is recorded; every role then leaves its loop, warps as a whole.
+    // Rows of very long contexts that are computed again may keep the others waiting longer.
     auto wait = [&](uint64_t *bar, uint32_t parity, unsigned code) {
-        if (mbar_wait_bounded(bar, parity, kWaitLimitNs)) return true;
+        for (int i = 0; i < kAgainWaits; ++i) {
+            if (mbar_wait_bounded(bar, parity, kWaitLimitNs)) return true;
+            if (*const_cast<volatile int *>(&s_again) == 0) break;
+        }
         atomicOr(a.err, code);
         return false;
     };
@@ -379,6 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
             if (again != 0) {
                 // position by position, a row after the other, over what was just written
                 __syncwarp();
+                if (lane == 0) atomicAdd(&s_again, 1);
                 const int i0 = walk.j0 * kKeys, i1 = min(it.n, walk.j1 * kKeys);
                 for (; again != 0; again &= again - 1) {
                     const int r = __ffs(again) - 1;
@@ -413,6 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     if (lane == 0 && !to_out)
                         *(uniform && whole ? t.whole_ml + row_out : t.ml + row_slot) = make_float2(y.M, y.l);
                 }
+                if (lane == 0) atomicSub(&s_again, 1);
             }
         }
     } else if (warp < 8 + kLoadWarps) {
