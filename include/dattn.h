@@ -600,7 +600,8 @@ int dattn_batch_destroy(dattn_batch *batch);
 
 /*
  * Device-side error word of the current device.  Every wait inside the fused
- * kernel's shared-memory pipeline is bounded (about one second); a wait that
+ * kernel's shared-memory pipeline is bounded (about one second; ten in dattn_attend
+ * with token_offsets and in dattn_decode_shared); a wait that
  * runs out records a code here, abandons its CTA's output and returns instead
  * of hanging the GPU.  The paged decode records invalid block-table entries
  * here too.  This call synchronises the device and returns DATTN_OK if no

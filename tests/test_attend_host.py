@@ -39,7 +39,7 @@ int device_facts(DeviceFacts *out) {
 cudaError_t attend_token_configure(int) { return cudaSuccess; }
 cudaError_t attend_tiles_configure(int) { return cudaSuccess; }
 cudaError_t attend_token_max_clusters(int, int, bool, int, int cluster, int *n) { *n = 304 / cluster; return cudaSuccess; }
-int encode_head_rows(CUtensorMap *, const void *, long long, int, int, int, int) { ++g_maps; return DATTN_OK; }
+int encode_head_rows(CUtensorMap *, const void *, long long, long long, int, int, int, int, int) { ++g_maps; return DATTN_OK; }
 cudaError_t launch_attend_token(const AttendArgs &a, const TokenArgs &w, int, int, int, cudaStream_t) {
     g_a = a; g_w = w; ++g_token; return cudaSuccess;
 }
@@ -112,11 +112,15 @@ def test_each_call_takes_its_kernels(run):
     CHECK(c.paged() == DATTN_OK && g_token == 2 && g_tiles == 0);
     c.off = A;
     c.T = 9;
-    CHECK(c.dense() == DATTN_OK && g_tiles == 1 && g_token == 2 && g_maps == 2 && g_t.plan != nullptr);
-    CHECK(g_m.box_rows == 128 && g_t.align == 1);
+    CHECK(c.dense() == DATTN_OK && g_tiles == 1 && g_token == 2 && g_maps == 3 && g_t.plan != nullptr);
+    CHECK(g_m.box_rows == 128 && g_t.align == 1 && g_m.q_tokens == 64);
     CHECK(c.paged() == DATTN_OK && g_tiles == 2 && g_m.box_rows == 16 && g_t.align == 16);
     c.page = 3;   // no box divides it
-    CHECK(c.paged() == DATTN_OK && g_tiles == 3 && g_m.box_rows == 0 && g_t.align == 1 && g_maps == 4);
+    CHECK(c.paged() == DATTN_OK && g_tiles == 3 && g_m.box_rows == 0 && g_t.align == 1 && g_maps == 7);
+    c.H = 6;      // a stack is no whole number of tokens
+    c.qs = 384;
+    CHECK(c.dense() == DATTN_OK && g_m.q_tokens == 0 && g_maps == 9);
+    g_tiles = 3;
     Call s;
     CHECK(s.prefix() == DATTN_OK && g_tiles == 4 && g_token == 3 && g_merge == 1);
     CHECK(g_t.plan == nullptr && g_t.bound_ends == 0 && g_w.own_only == 1 && g_a.own_base == 16 && g_a.S == 80);

@@ -104,6 +104,7 @@ struct Plan {
 
 constexpr double kTileUs = 1.9;      // of an SM, for a key tile of 256 rows of 128 channels
 constexpr double kBytesUs = 6.8e6;   // of the GPU
+constexpr long long kMaxMapStride = 1LL << 38;  // elements between rows that a tensor map takes
 constexpr int kBoxRows = 8;  // fewest rows of a page's box
 constexpr int kMaxColumns = 16;  // query heads of a key/value head in one CTA
 constexpr int kStaticSmem = 1024;  // the kernel's static shared memory at most
@@ -378,8 +379,15 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
         if (m.box_rows > 0) {
             const long long map_rows = s.apart ? s.shared : static_cast<long long>(rows);
             for (auto &[map, base] : {std::pair{&m.k, s.apart ? Kp : K}, std::pair{&m.v, s.apart ? Vp : V}})
-                if (int st = dattn::encode_head_rows(map, base, map_rows, s.n_kv_heads, s.head_dim, m.box_rows, dtype))
+                if (int st = dattn::encode_head_rows(map, base, map_rows, kv_row, s.n_kv_heads, s.head_dim, m.box_rows,
+                                                     1, dtype))
                     return st;
+        }
+        if (128 % a.group == 0 && q_stride < kMaxMapStride) {
+            m.q_tokens = 128 / a.group;
+            if (int st = dattn::encode_head_rows(&m.q, Q, s.tokens, q_stride, s.n_heads, s.head_dim, m.q_tokens,
+                                                 a.group, dtype))
+                return st;
         }
         at(p.t_acc, t.acc);
         at(p.t_ml, t.ml);

@@ -14,7 +14,7 @@
 //             tiles never touch it.
 //   8-10      loads: K and V tiles into a ring of slots, Q once an item.  Tiles inside the
 //             window are boxes of TMA (a whole tile of a dense cache, of a paged one as many
-//             rows as divide a page); others, 16-byte cp.async of any rows (sinks, the
+//             rows as divide a page), a stack's Q too where it is whole tokens; others, 16-byte cp.async of any rows (sinks, the
 //             item's end, odd pages): positions that no row sees are not read and zero.
 //   11        issues the products: S of the next tile while softmax works on the last one.
 // While one stack's softmax runs, the tensor cores work for the other.
@@ -40,7 +40,9 @@ using attend::Seen;
 
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kLoadWarps = 3, kThreads = 384;
-constexpr int kAgainWaits = 100;  // time limits of a wait while rows are computed again
+// Time limit of a wait: a warp that computes 32 rows of a context of millions of positions
+// again (below) keeps the other roles waiting for seconds.
+constexpr unsigned long long kTileWaitLimitNs = 10 * kWaitLimitNs;
 constexpr unsigned kNoRow = 0xffffffffu;  // zeros (a cache has fewer than 2^31 rows)
 // The running maximum M is kept kHeadroom (log2) below the largest exponent when it was set
 // and moved when one exceeds M + kTrigger: weights lie below 2^12 (f16 holds up to 65504)
@@ -135,7 +137,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
     extern __shared__ unsigned char smem_raw[];
     __shared__ uint64_t bars[Z::kBars];
     __shared__ uint32_t s_tmem;
-    __shared__ int s_again;  // warps that compute rows again
 
     uint64_t *const kv_full = bars, *const kv_free = bars + Z::kSlots;
     uint64_t *const q_full = bars + 2 * Z::kSlots, *const q_free = q_full + 1;
@@ -165,7 +166,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
         }
         mbar_init(drained, 1);
         fence_barrier_init();
-        s_again = 0;
     }
     tc::fence_before();
     __syncthreads();
@@ -191,12 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
     }
 
     // A wait that ran out is recorded; every role then leaves its loop, warps as a whole.
-    // Rows of very long contexts that are computed again may keep the others waiting longer.
     auto wait = [&](uint64_t *bar, uint32_t parity, unsigned code) {
-        for (int i = 0; i < kAgainWaits; ++i) {
-            if (mbar_wait_bounded(bar, parity, kWaitLimitNs)) return true;
-            if (*const_cast<volatile int *>(&s_again) == 0) break;
-        }
+        if (mbar_wait_bounded(bar, parity, kTileWaitLimitNs)) return true;
         atomicOr(a.err, code);
         return false;
     };
@@ -386,7 +382,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
             if (again != 0) {
                 // position by position, a row after the other, over what was just written
                 __syncwarp();
-                if (lane == 0) atomicAdd(&s_again, 1);
                 const int i0 = walk.j0 * kKeys, i1 = min(it.n, walk.j1 * kKeys);
                 for (; again != 0; again &= again - 1) {
                     const int r = __ffs(again) - 1;
@@ -421,7 +416,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     if (lane == 0 && !to_out)
                         *(uniform && whole ? t.whole_ml + row_out : t.ml + row_slot) = make_float2(y.M, y.l);
                 }
-                if (lane == 0) atomicSub(&s_again, 1);
             }
         }
     } else if (warp < 8 + kLoadWarps) {
@@ -517,6 +511,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                 // read theirs
                 if (number > 0 && !(ok = wait_warp(q_free, (number - 1) & 1, kErrProducerWait))) break;
                 ++number;
+                if (maps.q_tokens > 0) {
+                    // a stack is whole tokens: 64 channels of its rows are a box
+                    if (lane == 0) {
+                        if (lw == 0) mbar_arrive_expect_tx(q_full, stacks * blocks * 128 * 128);
+                        else mbar_arrive(q_full);
+                    }
+                    __syncwarp();
+                    if (lw == 0 && lane < stacks * blocks) {
+                        const int st = lane / blocks, c = lane - st * blocks;
+                        box_g2s(q_smem + st * Z::kQBytes + c * (128 * 128), &maps.q, c * 64, walk.kvh * a.group,
+                                it.token + st * maps.q_tokens, q_full);
+                    }
+                    continue;
+                }
                 for (int g = lw; g < stacks * 8; g += kLoadWarps) {
                     // 16 rows: lane l (and l + 16) finds row l's address, 0 for zeros
                     const int r = g * 16 + (lane & 15);
@@ -545,6 +553,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
         // what was asked for has arrived before the shared memory is given up
         cp_async_commit();
         cp_async_wait<0>();
+        if (number > 0) wait_warp(q_full, (number - 1) & 1, kErrDrainWait);
         for (int i = 0; i < Z::kSlots; ++i) {
             const uint32_t rounds = (used + Z::kSlots - 1 - i) / Z::kSlots;
             if (rounds > 0) wait_warp(kv_full + i, (rounds - 1) & 1, kErrDrainWait);

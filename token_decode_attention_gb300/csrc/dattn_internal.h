@@ -23,7 +23,7 @@ constexpr unsigned kErrSelftestWait = 8u;
 constexpr unsigned kErrPageIndex = 16u;  // a block-table entry outside [0, num_pages)
 constexpr unsigned kErrAppendPosition = 32u;  // an append position outside the cache
 
-// Time limit of every pipeline wait in the library's kernels.
+// Time limit of the pipeline waits in the library's kernels (attend_tiles_kernel.cuh: ten times that).
 constexpr unsigned long long kWaitLimitNs = 1000000000ull;  // one second
 
 // Arguments of the stream-K decode kernel.
@@ -264,9 +264,11 @@ struct DeviceFacts {
 };
 int device_facts(DeviceFacts *out);  // a dattn_status, the message recorded
 
-// Tensor map of [rows, H, D] 16-bit elements whose box, box_rows rows of one head and 64
-// channels, lands swizzled by 128 bytes; a dattn_status, the message recorded.
-int encode_head_rows(CUtensorMap *map, const void *base, long long rows, int H, int D, int box_rows, int dtype);
+// Tensor map of [rows, H, D] 16-bit elements, rows `stride` elements apart, whose box, box_rows
+// rows of box_heads heads and 64 channels, lands swizzled by 128 bytes; a dattn_status, the
+// message recorded.
+int encode_head_rows(CUtensorMap *map, const void *base, long long rows, long long stride, int H, int D,
+                     int box_rows, int box_heads, int dtype);
 
 // Rotation of pair i of a token at position p: by the angle p theta_i, cos and
 // sin both multiplied by `magnitude`.  theta_i / (2 pi) travels as a binary
@@ -419,10 +421,11 @@ struct TileArgs {
     int align;               // an item's `lo` is a multiple (a power of two)
 };
 // Tensor maps of K and V (of the shared positions' own tensors where there are such) as
-// [rows, Hk, D], a box of box_rows rows of one head and 64 channels; box_rows 0: none.
+// [rows, Hk, D], a box of box_rows rows of one head and 64 channels; box_rows 0: none.  Of Q
+// as [tokens, H, D], a box of q_tokens tokens of a group's heads, 128 rows; q_tokens 0: none.
 struct TileMaps {
-    CUtensorMap k, v;
-    int box_rows;
+    CUtensorMap k, v, q;
+    int box_rows, q_tokens;
 };
 cudaError_t attend_tiles_configure(int max_smem);
 cudaError_t launch_attend_tiles(const AttendArgs &a, const TileArgs &t, const TileMaps &m, int dtype, int dp,
