@@ -111,8 +111,7 @@ def _any_case(rng):
     else:
         most = min(16384, room // 4, int(math.sqrt(2 ** 42 / (heads * dim))))
         tokens = _log(rng, 1, max(1, most))
-        counts = _bring(dict(c, batch=batch, tokens=tokens, ragged=True, seq_len=tokens, fresh=True))
-        longest = max(n for n, _ in counts)
+        longest = -(-3 * tokens // batch) + 1
         more = max(1, min(16384, room // batch, 2 ** 40 // (heads * dim * tokens)))
         fresh = rng.random() < 0.4
         seq_len = longest + (0 if fresh else _log(rng, 1, more))
