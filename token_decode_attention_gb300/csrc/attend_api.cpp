@@ -108,6 +108,8 @@ constexpr long long kMaxMapStride = 1LL << 38;  // elements between rows that a 
 constexpr int kBoxRows = 8;  // fewest rows of a page's box
 constexpr int kMaxColumns = 16;  // query heads of a key/value head in one CTA
 constexpr int kStaticSmem = 1024;  // the kernel's static shared memory at most
+constexpr size_t kWorkspaceAlign = 16;  // what a caller's workspace lies on
+constexpr size_t kStateAlign = 32;      // what states of many tokens lie on, stored 32 bytes at a time
 constexpr size_t kKeptPlans = 1024;  // a program that never repeats a shape starts anew
 
 // One token per sequence, `cap` positions seen at most.  Measured (graph replay, inputs
@@ -268,6 +270,7 @@ int make_plan(const Shape &s, Plan *out) {
         if (int st = tiles_plan(s, cap, df, &p)) return st;
     if (!s.ragged)
         if (int st = token_plan(s, cap, df, &p)) return st;
+    if (p.tiles) p.ws_bytes += kStateAlign - kWorkspaceAlign;  // the parts begin on kStateAlign
     if (plans.size() >= kKeptPlans) plans.clear();
     plans[key] = p;
     *out = p;
@@ -313,7 +316,7 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
     if (p.ws_bytes > 0) {
         if (workspace == nullptr)
             return fail(DATTN_ERR_WORKSPACE, "workspace of %zu bytes required, got NULL", p.ws_bytes);
-        if (reinterpret_cast<uintptr_t>(workspace) & 15u)
+        if (reinterpret_cast<uintptr_t>(workspace) % kWorkspaceAlign != 0)
             return fail(DATTN_ERR_WORKSPACE, "workspace is not 16-byte aligned");
         if (workspace_bytes < p.ws_bytes)
             return fail(DATTN_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu", p.ws_bytes,
@@ -349,7 +352,8 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
     a.window = s.window;
     a.sinks = s.sinks;
     a.qscale = static_cast<float>(1.4426950408889634 / std::sqrt(static_cast<double>(s.head_dim)));
-    char *const ws = static_cast<char *>(workspace);
+    const size_t align = p.tiles ? kStateAlign : kWorkspaceAlign;
+    char *const ws = reinterpret_cast<char *>(round_up(reinterpret_cast<uintptr_t>(workspace), align));
     auto at = [&](size_t offset, auto *&part) {
         part = reinterpret_cast<std::remove_reference_t<decltype(part)>>(ws + offset);
     };
