@@ -2,7 +2,12 @@
 and the launches: where the parts of a workspace lie, what overlaps, and refusals of the binding."""
 from __future__ import annotations
 
-from .test_attend_host import run  # noqa: F401  (the fixture)
+import pytest
+import torch
+
+import token_decode_attention_gb300 as dattn
+
+from .test_attend_host import run, tensors  # noqa: F401  (`run` is the fixture)
 
 
 def test_states_lie_on_32_bytes_whatever_the_workspace_starts_on(run):  # noqa: F811
@@ -30,3 +35,17 @@ def test_states_lie_on_32_bytes_whatever_the_workspace_starts_on(run):  # noqa: 
         }
     }
     """)
+
+
+# ------------------------------------------------------------------ the binding
+
+@pytest.mark.parametrize("call", ["function", "entry"])
+def test_a_shared_call_needs_its_length(call):
+    """No shared_len is not "nothing shared": that would be another operator."""
+    q, k, v, pos = tensors()
+    table = torch.zeros(2, 4, dtype=torch.int32)
+    with pytest.raises(TypeError, match="shared_len"):
+        if call == "function":
+            dattn.decode_shared_paged(q, k, v, table, pos, None)
+        else:
+            dattn.dattn_decode_shared_paged(q, k, v, torch.empty_like(q), table, pos, None)

@@ -1233,8 +1233,8 @@ def dattn_decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, out, current_po
 
 def dattn_decode_shared_paged(q, k_pages, v_pages, out, block_table, current_pos, shared_len: int,
                               workspace=None, stream=None) -> None:
-    _attend("decode_shared", q, None, k_pages, v_pages, _table(block_table), current_pos, None, shared_len,
-            0, 0, out, workspace, stream, False)
+    _attend("decode_shared", q, None, k_pages, v_pages, _table(block_table), current_pos, None,
+            _length(shared_len), 0, 0, out, workspace, stream, False)
 
 
 def decode_shared(q, k_prefix, v_prefix, k_cache, v_cache, current_pos, out=None, workspace=None,
@@ -1251,10 +1251,16 @@ def decode_shared_paged(q, k_pages, v_pages, block_table, current_pos, shared_le
     """Decode attention over a paged cache whose sequences share their first ``shared_len``
     positions, which are read once, through the first sequence's row of ``block_table``."""
     return _attend("decode_shared", q, None, k_pages, v_pages, _table(block_table), current_pos, None,
-                   shared_len, 0, 0, out, workspace, stream, True)
+                   _length(shared_len), 0, 0, out, workspace, stream, True)
 
 
 def _table(block_table):
     if block_table is None:
         raise TypeError("block_table must be a torch.Tensor")
     return block_table
+
+
+def _length(shared_len):
+    if shared_len is None:  # without it _attend is the call that shares nothing
+        raise TypeError("shared_len must be an int")
+    return shared_len
