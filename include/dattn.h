@@ -498,7 +498,8 @@ int dattn_decode_paged_q8(const void *Q, const void *K_pages, const void *V_page
  *   K_cache, V_cache  [batch, seq_len, n_kv_heads, head_dim], or pages [num_pages,
  *        page_size, n_kv_heads, head_dim] with block_table as in dattn_decode_paged_f16
  *        (seq_len = page_size * max_pages); the new tokens' rows are there already
- *   out  [tokens, n_heads, head_dim], dense; shares no byte with the inputs (INVALID_ARG)
+ *   out  [tokens, n_heads, head_dim], dense; shares no byte with the inputs, the arrays of
+ *        positions, offsets and pages included (INVALID_ARG)
  * token_offsets and current_pos are those of dattn_rope_append_q8: sequence b brings
  * tokens token_offsets[b] .. token_offsets[b+1]-1, the last at position
  * min(current_pos[b], seq_len-1) and the ones before it at the positions before;
@@ -515,7 +516,8 @@ int dattn_decode_paged_q8(const void *Q, const void *K_pages, const void *V_page
  * left behind may be freed; an invalid one is reported as DATTN_ERR_BAD_PAGE, as in
  * dattn_decode_paged_f16.
  * workspace: device scratch, 16-byte aligned, of dattn_attend_workspace_bytes (`ragged`
- * non-zero where token_offsets is given; NULL where that is 0); calls on different
+ * non-zero where token_offsets is given; NULL where that is 0); it shares no byte with the
+ * call's tensors (INVALID_ARG; the cache is not compared), calls on different
  * streams need different ones.  head_dim: a multiple of 8, at most 256; tokens x n_heads
  * below 2^31; a sequence has fewer than 2^31 - 1024 positions, a cache fewer than 2^31.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.

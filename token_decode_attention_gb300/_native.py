@@ -1156,6 +1156,7 @@ def _attend(name, q, prefix, k, v, block_table, current_pos, token_offsets, shar
     if workspace is not None:
         wp = _tensor(workspace, "workspace", None, getattr(workspace, "dtype", None))
         _on_device((("workspace", workspace),), dev)
+        _apart_from_caches(workspace, k, v)
         wn = workspace.numel() * workspace.element_size()
     elif allocate:
         capacity = rows * table_pages if table_pages else rows
@@ -1252,6 +1253,15 @@ def decode_shared_paged(q, k_pages, v_pages, block_table, current_pos, shared_le
     positions, which are read once, through the first sequence's row of ``block_table``."""
     return _attend("decode_shared", q, None, k_pages, v_pages, _table(block_table), current_pos, None,
                    _length(shared_len), 0, 0, out, workspace, stream, True)
+
+
+def _apart_from_caches(workspace, k, v) -> None:
+    """The C entry compares the workspace with everything but the caches."""
+    at = workspace.data_ptr()
+    end = at + workspace.numel() * workspace.element_size()
+    for name, t in (("K", k), ("V", v)):
+        if at < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < end:
+            raise ValueError(f"the workspace overlaps the {name} cache")
 
 
 def _table(block_table):

@@ -72,14 +72,20 @@ int check_pages(Shape *s) {
     return DATTN_OK;
 }
 
-// `out` may share no byte with what the call reads.
-int check_apart(const void *out, double out_bytes, const void *p, double bytes, const char *name) {
-    const double a = static_cast<double>(reinterpret_cast<uintptr_t>(out));
-    const double b = static_cast<double>(reinterpret_cast<uintptr_t>(p));
-    if (a < b + bytes && b < a + out_bytes)
-        return fail(DATTN_ERR_INVALID_ARG, "out overlaps %s", name);
-    return DATTN_OK;
-}
+// What a call writes may share no byte with what it reads, nor `out` with the workspace.
+struct Written {
+    const void *at;
+    double bytes;
+    const char *name;
+
+    int apart(const void *p, double n, const char *what) const {
+        if (p == nullptr) return DATTN_OK;
+        const double a = static_cast<double>(reinterpret_cast<uintptr_t>(at));
+        const double b = static_cast<double>(reinterpret_cast<uintptr_t>(p));
+        if (a < b + n && b < a + bytes) return fail(DATTN_ERR_INVALID_ARG, "%s overlaps %s", name, what);
+        return DATTN_OK;
+    }
+};
 
 // ------------------------------------------------------------------- plans
 
@@ -303,14 +309,21 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
         return fail(DATTN_ERR_UNSUPPORTED, "the cache must hold fewer than 2^31 positions in all");
     if (rows * kv_row > 4.0e18 || static_cast<double>(s.tokens) * q_stride > 4.0e18)
         return fail(DATTN_ERR_INVALID_ARG, "the tensors are too large");
-    const double out_bytes = 2.0 * s.tokens * q_row, kv_bytes = 2.0 * rows * kv_row;
-    if (int st = check_apart(out, out_bytes, Q, 2.0 * ((s.tokens - 1.0) * q_stride + q_row), "Q")) return st;
-    if (int st = check_apart(out, out_bytes, K, kv_bytes, "the K cache")) return st;
-    if (int st = check_apart(out, out_bytes, V, kv_bytes, "the V cache")) return st;
-    if (s.apart) {
-        if (int st = check_apart(out, out_bytes, Kp, 2.0 * s.shared * kv_row, "K_prefix")) return st;
-        if (int st = check_apart(out, out_bytes, Vp, 2.0 * s.shared * kv_row, "V_prefix")) return st;
-    }
+    const double kv_bytes = 2.0 * rows * kv_row;
+    const Written result{out, 2.0 * s.tokens * q_row, "out"};
+    // the inputs but the cache
+    auto apart = [&](const Written &w) {
+        if (int st = w.apart(Q, 2.0 * ((s.tokens - 1.0) * q_stride + q_row), "Q")) return st;
+        if (int st = w.apart(current_pos, 4.0 * s.batch, "current_pos")) return st;
+        if (int st = w.apart(token_offsets, 4.0 * (s.batch + 1.0), "token_offsets")) return st;
+        if (int st = w.apart(s.block_table, 4.0 * s.batch * s.max_pages, "block_table")) return st;
+        if (!s.apart) return static_cast<int>(DATTN_OK);
+        if (int st = w.apart(Kp, 2.0 * s.shared * kv_row, "K_prefix")) return st;
+        return w.apart(Vp, 2.0 * s.shared * kv_row, "V_prefix");
+    };
+    if (int st = apart(result)) return st;
+    if (int st = result.apart(K, kv_bytes, "the K cache")) return st;
+    if (int st = result.apart(V, kv_bytes, "the V cache")) return st;
     Plan p;
     if (int st = make_plan(s, &p)) return st;
     if (p.ws_bytes > 0) {
@@ -321,6 +334,9 @@ int attend(const void *Q, const void *Kp, const void *Vp, const void *K, const v
         if (workspace_bytes < p.ws_bytes)
             return fail(DATTN_ERR_WORKSPACE, "workspace of %zu bytes required, got %zu", p.ws_bytes,
                         workspace_bytes);
+        const Written scratch{workspace, static_cast<double>(p.ws_bytes), "the workspace"};
+        if (int st = apart(scratch)) return st;
+        if (int st = scratch.apart(out, result.bytes, "out")) return st;
     }
     dattn::DeviceFacts df;
     if (int st = dattn::device_facts(&df)) return st;
