@@ -508,7 +508,9 @@ int dattn_decode_paged_q8(const void *Q, const void *K_pages, const void *V_page
  * 0 .. p, the last `window` positions (0: all) and the first `sinks` ones:
  *   out[t,h,:] = sum_j softmax_j(Q[t,h,:] . K[j,e,:] / sqrt(head_dim)) V[j,e,:]
  * over the positions j it sees and e = h / (n_heads / n_kv_heads).  Products accumulate
- * in fp32, the running maximum and sum are fp32, out is rounded once.  Positions a token
+ * in fp32, the running maximum and sum are fp32, out is rounded once.  Weights of up to 2^15
+ * a position meet V before their sum is divided out: bf16 values beyond 2^80 may overflow,
+ * f16 ones do not.  Positions a token
  * does not see never enter its row, whatever their contents (NaN included).  A token
  * whose position would be negative sees nothing: its row is zeros and
  * dattn_device_error() reports DATTN_ERR_BAD_POSITION.  Table entries are used only for

@@ -36,3 +36,28 @@ def test_workspaces_on_16_bytes(i, offset):
     out = c.call(c.cuda(), workspace=ws[offset: offset + max(n, 16)])
     assert torch.equal(out.cpu(), first)
     assert bool((ws[:offset] == 255).all()) and bool((ws[offset + max(n, 16):] == 255).all())
+
+
+# ------------------------------------------------------ values at the ends of the types
+
+FORMS = {"token": dict(S=300, last=[299, 77]), "ragged": dict(S=300, last=[280, 9], counts=[180, 3]),
+         "window": dict(S=300, last=[280, 9], counts=[180, 3], window=50, sinks=3),
+         "shared": dict(S=40, last=[39, 5, 20], shared=260)}
+
+
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype,D", [("f16", 64), ("f16", 128), ("f16", 256), ("bf16", 128)])
+def test_the_largest_values_stay_finite(form, dtype, D):
+    """A mean of the type's largest value (bf16: 2^80) is that value: weights that are rounded
+    up do not carry it beyond."""
+    def edit(c):
+        top = 65504.0 if dtype == "f16" else 2.0 ** 80
+        for x in (c.v, c.vp):
+            if x is not None:
+                x[:] = top
+                x[..., 1::2] = -top
+        c.q *= 2
+    c = Case(dtype, 8, 2, D, seed=41, edit=edit, **FORMS[form])
+    got = c.run()
+    assert bool(torch.isfinite(got).all()), int((~torch.isfinite(got)).sum())
+    c.check(got)

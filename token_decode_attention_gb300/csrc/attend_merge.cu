@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kWarps * 32) merge_kernel(const AttendArgs a, 
         const int ch = 4 * lane + 128 * j;
         if (ch < a.D)
             *reinterpret_cast<uint2 *>(static_cast<T *>(a.out) + row * a.D + ch) =
-                make_uint2(Pair<T>::narrow(y[j].x * inv, y[j].y * inv), Pair<T>::narrow(y[j].z * inv, y[j].w * inv));
+                make_uint2(Pair<T>::result(y[j].x * inv, y[j].y * inv), Pair<T>::result(y[j].z * inv, y[j].w * inv));
     }
 }
 

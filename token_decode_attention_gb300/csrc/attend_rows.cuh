@@ -25,7 +25,10 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// 16-bit types: two values of a word to fp32, two fp32 to a word (to nearest).
+// 16-bit types: two values of a word to fp32, two fp32 to a word (to nearest).  result: of
+// outputs whose weights were rounded to the type while their sum was not, so that a mean of
+// f16 values may come out up to 2^-11 too large, and infinite: no mean of finite values is
+// beyond the largest one.
 template <typename T>
 struct Pair;
 template <>
@@ -37,6 +40,11 @@ struct Pair<__half> {
         const __half2 h = __floats2half2_rn(x, y);
         return *reinterpret_cast<const uint32_t *>(&h);
     }
+    static constexpr float kLargest = 65504.f;
+    static __device__ __forceinline__ float bounded(float x) {
+        return fabsf(x) < INFINITY ? fminf(fmaxf(x, -kLargest), kLargest) : x;
+    }
+    static __device__ __forceinline__ uint32_t result(float x, float y) { return narrow(bounded(x), bounded(y)); }
 };
 template <>
 struct Pair<__nv_bfloat16> {
@@ -47,6 +55,9 @@ struct Pair<__nv_bfloat16> {
         const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
         return *reinterpret_cast<const uint32_t *>(&h);
     }
+    static constexpr float kLargest = INFINITY;  // outputs that overflow did so in fp32
+    static __device__ __forceinline__ float bounded(float x) { return x; }
+    static __device__ __forceinline__ uint32_t result(float x, float y) { return narrow(x, y); }
 };
 
 struct Seen {

@@ -100,6 +100,13 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// The largest of three absolute values, NaN where one is.
+__device__ __forceinline__ float max3_abs_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // What a row sees of an item's positions, in the item's count: of the `window` ones from
 // the item's `lo` on those in [lo, end) and below `sinks`; the sinks behind them, up to n, all.
 struct Edges {
@@ -359,8 +366,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                 tc::ld32(o, col_o + c);
                 tc::wait_ld();
                 if (!mine) continue;
+                float big = 0.f;  // the largest absolute value, NaN where one is
 #pragma unroll
-                for (int k = 0; k < 32; ++k) nan |= c + k < a.D && __uint_as_float(o[k]) != __uint_as_float(o[k]);
+                for (int k = 0; k < 32; k += 8)
+                    if (c + k < a.D)
+#pragma unroll
+                        for (int h = k; h < k + 8; h += 2)
+                            big = max3_abs_nan(big, __uint_as_float(o[h]), __uint_as_float(o[h + 1]));
+                nan |= big != big;
                 if (!to_out) {
 #pragma unroll
                     for (int k = 0; k < 32; k += 8)
@@ -368,9 +381,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     continue;
                 }
                 T *const out = static_cast<T *>(a.out) + out_row * a.D + c;
+                float times = inv;
+                if (!kBf16 && big * inv > Pair<T>::kLargest) {  // rare: see Pair::result
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(Pair<T>::bounded(__uint_as_float(o[k]) * inv));
+                    times = 1.f;
+                }
 #pragma unroll
                 for (int k = 0; k < 32; k += 2)
-                    o[k / 2] = Pair<T>::narrow(__uint_as_float(o[k]) * inv, __uint_as_float(o[k + 1]) * inv);
+                    o[k / 2] = Pair<T>::narrow(__uint_as_float(o[k]) * times, __uint_as_float(o[k + 1]) * times);
 #pragma unroll
                 for (int k = 0; k < 32; k += 16) {
                     if (t.out_32 && c + k + 8 < a.D) {
