@@ -46,6 +46,43 @@ FORMS = {"token": dict(S=300, last=[299, 77]), "ragged": dict(S=300, last=[280, 
 
 
 @pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("dtype,D,q,k", [
+    ("f16", 64, 1536.0, 1536.0), ("f16", 128, 2048.0, 2560.0), ("f16", 128, -3000.0, 2500.0),
+    ("f16", 128, 5120.0, 5120.0), ("f16", 256, 65504.0, 65504.0), ("f16", 128, -65504.0, 40000.0),
+    ("bf16", 64, 2.0 ** 20, 3 * 2.0 ** 17), ("bf16", 128, 2.0 ** 50, 2.0 ** 50), ("bf16", 256, -2.0 ** 30, 2.0 ** 28)])
+def test_equal_scores_of_any_size(form, dtype, D, q, k):
+    """One key at every position: each weighs the same, however far from 0 its score lies.
+    The result is a mean of V, |V| <= size; a weight is rounded once (eps / 2 of it), sums of
+    n <= 300 terms are off by n 2^-24 each, the result is rounded once.
+
+    All positions of a call but a shared prefix's are one kernel's, which adds the D equal
+    products in one order, so their scores are the same whatever was rounded.  The prefix's and a
+    sequence's own are two kernels': their sums agree where no partial sum needs rounding, that
+    is where the odd part of q k times D fits 24 bits.  Where it does not (65504^2 = 2^10 x
+    4190209: 22 bits, times 256) the scores may differ by D 2^-24 of 10^10, and with them the
+    parts' weights as far as the general tolerance says; the result is finite all the same."""
+    def edit(c):
+        c.q[:] = q
+        c.k[:] = k
+        if c.kp is not None:
+            c.kp[:] = k
+    c = Case(dtype, 4, 2, D, seed=40, edit=edit, **FORMS[form])
+    got = c.run()
+    ref, general = c.expected()  # the scores are equal in 64 bits too
+    half = torch.finfo(c.t).eps / 2
+    size = max(float(x.double().abs().max()) for x in (c.v, c.vp) if x is not None)
+    tol = size * (half + 2 * 300 * 2.0 ** -24)
+    tol = tol + (ref.abs() + tol) * half + torch.finfo(c.t).tiny
+    odd = int(abs(q)) * int(k)
+    odd //= odd & -odd
+    if form == "shared" and odd * D >= 2 ** 24:
+        tol = torch.maximum(tol, general)
+        assert bool(torch.isfinite(got).all())
+    bad = ~((got.double() - ref).abs() <= tol)
+    assert not bool(bad.any()), (int(bad.sum()), got[bad][0], ref[bad][0])
+
+
+@pytest.mark.parametrize("form", FORMS)
 @pytest.mark.parametrize("dtype,D", [("f16", 64), ("f16", 128), ("f16", 256), ("bf16", 128)])
 def test_the_largest_values_stay_finite(form, dtype, D):
     """A mean of the type's largest value (bf16: 2^80) is that value: weights that are rounded

@@ -30,7 +30,8 @@
 //
 // A hidden position gets weight zero; 0 times a V that is not finite still makes the row's
 // O a NaN.  Rows with a NaN in a piece with hidden positions are computed again position
-// by position (attend::row_state), which touches what they see only.
+// by position (attend::row_state), which touches what they see only.  So are rows whose
+// scores lie beyond kFar.
 //
 // Work split: attend_tiles.cuh.  Pieces of items leave their states to the merge kernels.
 #pragma once
@@ -57,6 +58,11 @@ constexpr unsigned kNoRow = 0xffffffffu;  // zeros (a cache has fewer than 2^31 
 // and moved when one exceeds M + kTrigger: weights lie below 2^12 (f16 holds up to 65504)
 // and the largest is at least 2^4, which keeps f16 weights normal down to 2^-18 of it.
 constexpr float kHeadroom = 4.f, kTrigger = 12.f;
+// An exponent is the exact product of score and scale less M, and M a rounded one: from
+// scores of 2^26 on (log2 units), where fp32 goes in steps of 8, the largest exponent can
+// pass f16's range.  Rows whose M reached kFar are computed again with the rounded score less
+// M, as the one-token kernel does; below it the two differ by 2^-10 at most.
+constexpr float kFar = 16384.f;
 
 template <int DP>
 struct TileShape {
@@ -254,6 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
             const Edges all = seen_by_all(it, r0, r1, min_end);
             float M = -INFINITY, l = 0.f;
             bool hidden = false;  // some row of the warp does not see some position
+            bool far = false;     // the row's M was beyond kFar
             for (int j = walk.j0; j < walk.j1; ++j) {
                 const int n = j - walk.j0;
                 const int buf = (begun + (stacks == 2 ? stack : n)) & 1;
@@ -305,6 +312,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
                     const float f = M == -INFINITY ? 0.f : ex2(M - nm);
                     M = nm;
                     l *= f;
+                    far |= fabsf(nm) >= kFar && nm != -INFINITY;
                     if (running && !product_done()) break;
                     if (n > 0) {
 #pragma unroll 1
@@ -405,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
             }
             tc::fence_before();  // O has been read before the next item's first P is handed over
             if (mine && !to_out) *state_ml = make_float2(M, l);
-            unsigned again = __ballot_sync(kFull, nan && hidden);
+            unsigned again = __ballot_sync(kFull, mine && (far || (nan && hidden)));
             if (again != 0) {
                 // position by position, a row after the other, over what was just written
                 __syncwarp();
