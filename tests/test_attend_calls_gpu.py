@@ -9,7 +9,7 @@ import torch
 import token_decode_attention_gb300 as dattn
 from token_decode_attention_gb300 import _native
 
-from ._attend import TYPES, Case
+from ._attend import Case, half_step
 from .test_attend_gpu import cases_of_calls, workspace_bytes
 
 pytestmark = pytest.mark.gpu
@@ -98,3 +98,79 @@ def test_the_largest_values_stay_finite(form, dtype, D):
     got = c.run()
     assert bool(torch.isfinite(got).all()), int((~torch.isfinite(got)).sum())
     c.check(got)
+
+
+# ------------------------------- tiles whose last block of channels is not full, long walks
+
+def check_fast(c, got):
+    """Case.check with a sequence's rows at once."""
+    ref, tol = c.out0.double(), torch.zeros(c.out0.shape, dtype=torch.float64)
+    group, t, half = c.H // c.Hk, 0, torch.finfo(c.t).eps / 2
+    for b in range(c.B):
+        n, end = (1 if c.counts is None else c.counts[b]), min(c.last[b], c.S - 1)
+        if c.shared and not c.page:
+            end += c.shared
+        if n == 0:
+            continue
+        K, V = (x.double().repeat_interleave(group, 1).transpose(0, 1) for x in c.rows(b, range(end + 1)))
+        q = c.q[t: t + n].double().transpose(0, 1)  # [H, n, D]
+        p, j = torch.arange(end - n + 1, end + 1)[:, None], torch.arange(end + 1)
+        sees = j <= p
+        if c.window:
+            sees &= (j > p - c.window) | (j < c.sinks)
+        s = (q @ K.transpose(1, 2) / c.D ** 0.5).masked_fill(~sees, -float("inf"))
+        w = torch.softmax(s, -1)
+        r, size, m = w @ V, w @ V.abs(), sees.sum(-1)[:, None]
+        dot = (q.abs() @ K.abs().transpose(1, 2) / c.D ** 0.5).masked_fill(~sees, 0).amax(-1, keepdim=True)
+        most = s.masked_fill(~sees, 0).abs().amax(-1, keepdim=True)
+        d = (c.D + 8) * 2.0 ** -24 * dot + 4 * 2.0 ** -24 * most + 2.0 ** -21
+        e = size * (2 * (d + m * 2.0 ** -24) + half)
+        if c.t is torch.float16:
+            e = e + m * 2.0 ** -25 * V.abs().amax(1, keepdim=True)
+        ref[t: t + n], tol[t: t + n] = r.transpose(0, 1), (e + half_step(r.abs() + e, c.t)).transpose(0, 1)
+        t += n
+    bad = ~((got.double() - ref).abs() <= tol)
+    assert not bool(bad.any()), (int(bad.sum()), bad.nonzero()[0].tolist(), got[bad][0], ref[bad][0], tol[bad][0])
+
+
+def test_the_fast_check_is_the_other():
+    c = Case("f16", 4, 2, 72, 90, [80, 3, 89], counts=[50, 0, 7], window=30, sinks=2, pad=3, seed=42)
+    got = c.run()
+    check_fast(c, got)
+    c.check(got)
+
+
+@pytest.mark.parametrize("D", [8, 72, 80, 136, 200])
+@pytest.mark.parametrize("page", [0, 16, 64])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (290, 5)])
+def test_boxes_with_a_block_of_channels_in_part(D, page, window, sinks):
+    """Whole key tiles inside the window come as boxes of 64 channels, the last one's zero filled."""
+    c = Case("bf16" if D % 16 else "f16", 8, 2, D, 704, [700, 510], counts=[150, 3], page=page, window=window,
+             sinks=sinks, seed=43)
+    check_fast(c, c.run())
+
+
+@pytest.mark.parametrize("D", [8, 72, 80, 136, 200])
+@pytest.mark.parametrize("page", [0, 16, 64])
+def test_boxes_of_a_shared_prefix_with_a_block_of_channels_in_part(D, page):
+    if page:
+        c = Case("f16", 8, 2, D, 768, [700, 640, 767, 512], page=page, shared=512, seed=44)
+    else:
+        c = Case("bf16", 8, 2, D, 50, [49, 0, 17], shared=517, seed=44)
+    check_fast(c, c.run())
+
+
+@pytest.mark.parametrize("dtype,H,Hk,D,counts", [
+    ("bf16", 16, 1, 64, (3, 12, 1, 16, 8, 9, 20, 0, 16, 2)),    # 16 rows a token: one stack up to 8 tokens
+    ("f16", 16, 1, 128, (12, 3, 16, 1, 9, 8, 2, 30)),
+    ("f16", 12, 1, 72, (12, 3, 16, 1, 21, 11, 10, 2)),          # 12 rows a token: stacks end inside one
+    ("bf16", 16, 2, 256, (3, 12, 1, 16, 8, 9)),                 # one stack always
+])
+@pytest.mark.parametrize("window,sinks,page", [(0, 0, 0), (100, 3, 16)])
+def test_ctas_that_take_items_of_one_and_of_two_stacks_in_turn(dtype, H, Hk, D, counts, window, sinks, page):
+    """Eight items and more for each CTA, of one and of two stacks in every order."""
+    B = 1200
+    counts = [counts[(i * 7 + i // 50) % len(counts)] for i in range(B)]
+    last = [max(n, 1) - 1 + (i * 37) % (240 - n) for i, n in enumerate(counts)]
+    c = Case(dtype, H, Hk, D, 240, last, counts=counts, window=window, sinks=sinks, page=page, seed=45)
+    check_fast(c, c.run())
