@@ -507,12 +507,14 @@ int dattn_decode_paged_q8(const void *Q, const void *K_pages, const void *V_page
  * padding, their rows of `out` are left as they were.  A token at position p sees, of
  * 0 .. p, the last `window` positions (0: all) and the first `sinks` ones:
  *   out[t,h,:] = sum_j softmax_j(Q[t,h,:] . K[j,e,:] / sqrt(head_dim)) V[j,e,:]
- * over the positions j it sees and e = h / (n_heads / n_kv_heads).  Products accumulate
- * in fp32, the running maximum and sum are fp32, out is rounded once.  Weights of up to 2^15
- * a position meet V before their sum is divided out: bf16 values beyond 2^80 may overflow,
- * f16 ones do not.  Positions a token
- * does not see never enter its row, whatever their contents (NaN included).  A token
- * whose position would be negative sees nothing: its row is zeros and
+ * over the positions j it sees and e = h / (n_heads / n_kv_heads).  Products accumulate in
+ * fp32, the running maximum and the sum of weights are fp32.  A weight meets V rounded: to
+ * two numbers of `dtype` without token_offsets (off by at most 1.5 x 2^-15 of it in bf16,
+ * 1.5 x 2^-21 in f16), to one with them (2^-8, 2^-11; the rms error of outputs is about 1.4
+ * times what their own rounding makes).  out is rounded once.  Weights of up to 2^15 a position meet V
+ * before their sum is divided out: bf16 values beyond 2^80 may overflow, f16 ones do not.
+ * Positions a token does not see never enter its row, whatever their contents (NaN
+ * included).  A token whose position would be negative sees nothing: its row is zeros and
  * dattn_device_error() reports DATTN_ERR_BAD_POSITION.  Table entries are used only for
  * pages with a position that some token of the call sees, so those that a window has
  * left behind may be freed; an invalid one is reported as DATTN_ERR_BAD_PAGE, as in
@@ -542,7 +544,8 @@ int dattn_attend_paged(const void *Q, const void *K_pages, const void *V_pages, 
  * Decode attention of a batch whose sequences share their first `shared_len` positions
  * (a system prompt, samples of one prompt): the shared keys and values are read once
  * for all sequences.  One token per sequence, types, heads and q_stride as in
- * dattn_attend, every position up to the token's own visible.
+ * dattn_attend, every position up to the token's own visible.  Weights of shared positions
+ * meet V rounded to one number of `dtype`, the others to two.
  *   dattn_decode_shared        K_prefix, V_prefix [shared_len, n_kv_heads, head_dim] and
  *       a cache [batch, seq_len, n_kv_heads, head_dim] of what follows them;
  *       current_pos[b] counts in that cache: the token is at row
@@ -550,8 +553,8 @@ int dattn_attend_paged(const void *Q, const void *K_pages, const void *V_pages, 
  *   dattn_decode_shared_paged  one pool of pages: the first shared_len positions are
  *       those of the first sequence's pages (its row of block_table, where all of them
  *       are; entries of the other rows for pages that hold shared positions only are not
- *       used), the others each sequence's own.  current_pos[b] counts from the first shared position; a token
- *       inside them sees the shared positions up to its own
+ *       used), the others each sequence's own.  current_pos[b] counts from the first
+ *       shared position; a token inside them sees the shared positions up to its own
  * workspace as in dattn_attend, of dattn_decode_shared_workspace_bytes: own_len is
  * seq_len, or page_size * max_pages - shared_len.
  * Errors: INVALID_ARG, UNSUPPORTED, MISALIGNED, WORKSPACE, CUDA.

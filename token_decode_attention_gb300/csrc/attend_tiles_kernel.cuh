@@ -6,6 +6,10 @@
 // over 128 query rows (a token's query heads of one key/value head are neighbouring rows, so
 // they share its keys) and key tiles of 128 (64 above 128 channels), M a running maximum.
 // What bounds it: 4 D flops for each query row and key; a key tile is loaded once for 256 rows.
+// P is rounded to the cache's type, the type of V's product (2^-8 or 2^-11 of a weight at most;
+// the sum of weights keeps them unrounded): errors of many weights mostly cancel, the rms error
+// of outputs is about 1.4 times what their own rounding makes, and a second part as in the
+// one-token kernel would be half as many products again.
 //
 // Roles of a CTA's 12 warps, one CTA on an SM:
 //   0-3, 4-7  softmax of the first and second 128 rows (the stacks): a thread a row.  S comes

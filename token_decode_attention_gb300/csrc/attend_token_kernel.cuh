@@ -9,10 +9,11 @@
 // m16n8k16): S^T = K Q^T over 16 positions and out^T = V^T P^T over 16 channels, the query
 // heads in the 8 columns.  A tcgen05 instruction wants 64 rows at least; a decode has as
 // many as query heads share a key, and at HBM's rate the tensor pipe idles either way.
-// P enters as the sum of two 16-bit numbers, so that the weights keep 2^-16 (bf16) or 2^-20
-// (f16) where one number keeps 2^-9 or 2^-12: their rounding alone would move bf16 outputs
-// by half of what their own rounding does.  Both parts are positive wherever the weight is
-// (the first is rounded down from slightly less than it): an infinite V stays infinite.
+// P enters as the sum of two 16-bit numbers, so that the weights are off by at most 1.5 x 2^-15
+// (bf16) or 1.5 x 2^-21 (f16) where one number is off by up to 2^-8 or 2^-11: their rounding
+// alone would move outputs by as much as the outputs' own rounding does.  Both parts are
+// positive wherever the weight is (the first is rounded down from slightly less than it): an
+// infinite V stays infinite.
 //
 // Work split: the seen positions are counted through (attend_rows.cuh) and cut into tiles
 // of 16.  A CTA takes a chunk of one unit, a (sequence, group of key/value heads); each of
