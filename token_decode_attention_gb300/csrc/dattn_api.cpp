@@ -617,24 +617,6 @@ int encode_kv_box(CUtensorMap *map, const void *base, long long rows, int H, int
     return DATTN_OK;
 }
 
-int encode_swizzled_box(CUtensorMap *map, const void *base, long long rows, long long stride, int H, int D,
-                        int box_rows, int box_heads, int dtype) {
-    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
-    if (enc == nullptr) return fail(DATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
-    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
-                                static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
-    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
-    const cuuint32_t unit[3] = {1, 1, 1};
-    const CUresult r = enc(map, dtype == dattn::kDtypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
-                           3, const_cast<void *>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    if (r != CUDA_SUCCESS) return fail(DATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
-    return DATTN_OK;
-}
-
 int launch_decode(const Plan &p, const void *Q, const void *K, const void *V, void *out, int B,
                   int H, int D, int S, const uint32_t *cur_pos, void *workspace,
                   cudaStream_t stream, const Paging &pg = Paging()) {
@@ -733,7 +715,20 @@ int device_facts(DeviceFacts *out) {
 }
 int encode_head_rows(CUtensorMap *map, const void *base, long long rows, long long stride, int H, int D,
                      int box_rows, int box_heads, int dtype) {
-    return encode_swizzled_box(map, base, rows, stride, H, D, box_rows, box_heads, dtype);
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (enc == nullptr) return fail(DATTN_ERR_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(H),
+                                static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+    const cuuint32_t unit[3] = {1, 1, 1};
+    const CUresult r = enc(map, dtype == kDtypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
+                                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                           3, const_cast<void *>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(DATTN_ERR_CUDA, "cuTensorMapEncodeTiled failed (%d)", int(r));
+    return DATTN_OK;
 }
 }  // namespace dattn
 
