@@ -174,3 +174,22 @@ def test_ctas_that_take_items_of_one_and_of_two_stacks_in_turn(dtype, H, Hk, D, 
     last = [max(n, 1) - 1 + (i * 37) % (240 - n) for i, n in enumerate(counts)]
     c = Case(dtype, H, Hk, D, 240, last, counts=counts, window=window, sinks=sinks, page=page, seed=45)
     check_fast(c, c.run())
+
+
+# -------------------------------------------------------------------- pinned host memory
+
+@pytest.mark.parametrize("i", range(6))
+def test_queries_positions_and_output_in_pinned_memory(i):
+    """What a step brings from the host and takes back, of every form."""
+    c = cases_of_calls()[i]
+    first = c.run()
+    d = c.cuda()
+    for name in ("q", "pos", "offsets", "table"):
+        if d[name] is not None:
+            d[name] = d[name].cpu().pin_memory()
+    host = torch.empty_like(c.out0).pin_memory()
+    assert c.call(d, out=host) is host
+    torch.cuda.synchronize()
+    assert torch.equal(host, first)
+    out = c.call(d)
+    assert out.is_cuda and torch.equal(out.cpu(), first)
