@@ -193,3 +193,64 @@ def test_queries_positions_and_output_in_pinned_memory(i):
     assert torch.equal(host, first)
     out = c.call(d)
     assert out.is_cuda and torch.equal(out.cpu(), first)
+
+
+# ------------------------------------------------------------- values that are not finite
+
+def prompt(n, H=32, Hk=8, D=128, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda").manual_seed(46)
+    q, k, v = (torch.randn(s, generator=g, device="cuda").to(dtype) for s in ((n, H, D), (1, n, Hk, D), (1, n, Hk, D)))
+    pos, off = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([n - 1], [0, n]))
+    return lambda **kw: dattn.attend(q, k, v, pos, token_offsets=off, **kw), q, k, v
+
+
+@pytest.mark.parametrize("where", ["key", "value", "middle"])
+def test_a_value_that_is_not_finite_costs_little(where):
+    """A prompt whose tokens see a NaN takes about as long as one whose tokens see none: what
+    rows are computed again for is hidden values alone.  (Position by position the whole
+    prompt takes 400 times as long; the limit of 20 leaves room for a busy clock.)"""
+    n = 4096
+    call, q, k, v = prompt(n)
+    first = call()
+
+    def ms():
+        start, end = (torch.cuda.Event(enable_timing=True) for _ in range(2))
+        times = []
+        for _ in range(5):
+            start.record()
+            call()
+            end.record()
+            end.synchronize()
+            times.append(start.elapsed_time(end))
+        return sorted(times)[2]
+    plain = ms()
+    at = n // 2 if where == "middle" else 0
+    (k if where == "key" else v)[0, at, 2, 5] = float("nan")
+    got = call()
+    hit = torch.zeros_like(first, dtype=torch.bool)
+    hit[at:, 8:12, slice(None) if where == "key" else 5] = True  # heads of key/value head 2
+    assert bool(torch.isnan(got[hit]).all())
+    assert torch.equal(got[~hit], first[~hit])
+    assert ms() < 20 * plain
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("D", [64, 256])
+def test_values_that_some_rows_of_an_item_see(bad, D):
+    """The rows before a bad value, in its own item and the next, come out as without it."""
+    n = 700
+    call, q, k, v = prompt(n, 8, 2, D, torch.float16)
+    first = call()
+    for at in (0, 1, 30, 31, 333, 699):
+        old = v[0, at, 1].clone()
+        v[0, at, 1, 3] = bad
+        got = call()
+        assert not bool(torch.isfinite(got[at:, 4:, 3]).any())
+        keep = torch.ones_like(first, dtype=torch.bool)
+        keep[at:, 4:, 3] = False
+        # rows that are computed again weigh in fp32 what the others round to f16: 2^-11 of a
+        # weight, and the output's own rounding
+        off = (got.double() - first.double()).abs()[keep]
+        size = float(v[torch.isfinite(v)].abs().max())
+        assert bool((off <= size * 2.0 ** -10 + 2.0 ** -10 * first.double().abs()[keep]).all())
+        v[0, at, 1] = old

@@ -157,24 +157,57 @@ __device__ void row_state(const AttendArgs &a, int b, int kvh, const T *q, Count
         r.l = fmaf(r.l, f, p);
 #pragma unroll
         for (int c = 0; c < 4; ++c) r.acc[c][0] *= f, r.acc[c][1] *= f;
-        for (unsigned left = who; left != 0; left &= left - 1) {
-            const int j = __ffs(left) - 1;
-            const float w = __shfl_sync(kAll, p, j);
-            const long long row = __shfl_sync(kAll, at, j);
-            const int there = __shfl_sync(kAll, apart, j);
-            const T *vr = static_cast<const T *>(there ? a.Vp : a.V) + row;
+        // eight positions' loads in flight
+#pragma unroll 1
+        for (int j0 = 0; j0 < 32; j0 += 8) {
+            if ((who >> j0 & 0xffu) == 0) continue;
+            uint32_t x[8][4];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const int ch = 2 * (lane + 32 * c);
-                if (ch >= a.D) continue;
-                const float2 x = Pair<T>::wide(__ldg(reinterpret_cast<const uint32_t *>(vr + ch)));
-                r.acc[c][0] = fmaf(w, x.x, r.acc[c][0]);
-                r.acc[c][1] = fmaf(w, x.y, r.acc[c][1]);
+            for (int u = 0; u < 8; ++u) {
+                const long long row = __shfl_sync(kAll, at, j0 + u);
+                const int there = __shfl_sync(kAll, apart, j0 + u);
+                const T *vr = static_cast<const T *>(there ? a.Vp : a.V) + row;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const int ch = 2 * (lane + 32 * c);
+                    x[u][c] = (who >> (j0 + u) & 1) && ch < a.D ? __ldg(reinterpret_cast<const uint32_t *>(vr + ch)) : 0u;
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float w = __shfl_sync(kAll, p, j0 + u);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    const float2 y = Pair<T>::wide(x[u][c]);
+                    r.acc[c][0] = fmaf(w, y.x, r.acc[c][0]);
+                    r.acc[c][1] = fmaf(w, y.y, r.acc[c][1]);
+                }
             }
         }
     }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) r.l += __shfl_xor_sync(kAll, r.l, o);
+}
+
+// Whether the value of position pos of sequence b holds something that is not finite.  Not
+// inlined: hardly ever called, from a kernel whose code is large already (16384 tokens 1.60
+// and 1.58 ms).
+template <typename T>
+__device__ __noinline__ bool value_not_finite(const AttendArgs &a, int b, int kvh, int pos) {
+    const bool apart = a.Kp != nullptr && pos < a.own_base;
+    const T *v = static_cast<const T *>(apart ? a.Vp : a.V) +
+                 row_of(a, b, pos) * static_cast<long long>(a.Hk) * a.D + static_cast<long long>(kvh) * a.D;
+    bool bad = false;
+    for (int c = 0; c < a.D; c += 8) {
+        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(v + c));
+        const uint32_t words[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const float2 y = Pair<T>::wide(words[e]);
+            bad |= !(fabsf(y.x) < INFINITY) || !(fabsf(y.y) < INFINITY);
+        }
+    }
+    return bad;
 }
 
 }  // namespace attend

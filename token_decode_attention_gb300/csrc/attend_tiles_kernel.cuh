@@ -33,9 +33,9 @@
 // shared evenly 1.86; every role's loops unrolled 2.0 (instruction fetch).
 //
 // A hidden position gets weight zero; 0 times a V that is not finite still makes the row's
-// O a NaN.  Rows with a NaN in a piece with hidden positions are computed again position
-// by position (attend::row_state), which touches what they see only.  So are rows whose
-// scores lie beyond kFar.
+// O a NaN.  Where a position that some rows of a piece do not see holds such a value, the
+// piece's rows with a NaN are computed again position by position (attend::row_state), which
+// touches what they see only.  So are rows whose scores lie beyond kFar.
 //
 // Work split: attend_tiles.cuh.  Pieces of items leave their states to the merge kernels.
 #pragma once
@@ -417,7 +417,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_tiles_kernel(const AttendA
             }
             tc::fence_before();  // O has been read before the next item's first P is handed over
             if (mine && !to_out) *state_ml = make_float2(M, l);
-            unsigned again = __ballot_sync(kFull, mine && (far || (nan && hidden)));
+            // A sum of weights that is NaN comes of a score that the row sees, and all of its
+            // outputs are; other NaN may come of a hidden value, where there is one.
+            bool doubt = mine && nan && l == l;
+            if (hidden && __any_sync(kFull, doubt)) {
+                bool bad = false;
+                for (int x = walk.j0 * kKeys; x < walk.j1 * kKeys && !bad; x += 32) {
+                    const unsigned h = all.hidden32(x);
+                    const bool there = x + lane < it.n && (h >> lane & 1) != 0;
+                    const attend::Counted counted{it.lo, it.n - it.first};
+                    if (h != 0) bad = __any_sync(kFull, there && attend::value_not_finite<T>(a, it.b, kvh, counted.at(x + lane)));
+                }
+                doubt &= bad;
+            } else {
+                doubt = false;
+            }
+            unsigned again = __ballot_sync(kFull, mine && (far || doubt));
             if (again != 0) {
                 // position by position, a row after the other, over what was just written
                 __syncwarp();
