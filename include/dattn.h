@@ -544,7 +544,8 @@ int dattn_attend_paged(const void *Q, const void *K_pages, const void *V_pages, 
  * Decode attention of a batch whose sequences share their first `shared_len` positions
  * (a system prompt, samples of one prompt): the shared keys and values are read once
  * for all sequences.  One token per sequence, types, heads and q_stride as in
- * dattn_attend, every position up to the token's own visible.  Weights of shared positions
+ * dattn_attend, every position up to the token's own visible.  Pays where the prefix is
+ * long: for one of some hundred positions dattn_attend takes less.  Weights of shared positions
  * meet V rounded to one number of `dtype`, the others to two.
  *   dattn_decode_shared        K_prefix, V_prefix [shared_len, n_kv_heads, head_dim] and
  *       a cache [batch, seq_len, n_kv_heads, head_dim] of what follows them;

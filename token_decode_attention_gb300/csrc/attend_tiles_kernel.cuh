@@ -25,12 +25,13 @@
 //             the last one, into the next item.
 // While one stack's softmax runs, the tensor cores work for the other.
 //
-// Measured (graph replay): 16384 tokens, 32 heads on 8 of 128, bf16, 1.62 ms, 1355 TFLOP/s, 70 %
+// Measured (graph replay): 16384 tokens, 32 heads on 8 of 128, bf16, 1.58 ms, 1390 TFLOP/s, 72 %
 // of a large matrix product's burst; tensor pipe busy half of the cycles.  Bound by the chain
 // S, softmax, P, V of a stack and its hand-overs, not by bytes: half of them loaded, or the
 // softmax left out, it takes 1.5 ms.  Tried, ms: tiles by 16-byte copies 1.88, by TMA
 // gathers of four rows 4.5; P handed over in halves 1.66, in quarters 1.72; registers
-// shared evenly 1.86; every role's loops unrolled 2.0 (instruction fetch).
+// shared evenly 1.86; every role's loops unrolled 2.0 (instruction fetch).  168 bytes of the
+// softmax role's registers and up to 72 of the loads' are spilled.
 //
 // A hidden position gets weight zero; 0 times a V that is not finite still makes the row's
 // O a NaN.  Where a position that some rows of a piece do not see holds such a value, the
