@@ -510,9 +510,10 @@ int dattn_decode_paged_q8(const void *Q, const void *K_pages, const void *V_page
  * over the positions j it sees and e = h / (n_heads / n_kv_heads).  Products accumulate in
  * fp32, the running maximum and the sum of weights are fp32.  A weight meets V rounded: to
  * two numbers of `dtype` without token_offsets (off by at most 1.5 x 2^-15 of it in bf16,
- * 1.5 x 2^-21 in f16), to one with them (2^-8, 2^-11; the rms error of outputs is about 1.4
- * times what their own rounding makes).  out is rounded once.  Weights of up to 2^15 a position meet V
- * before their sum is divided out: bf16 values beyond 2^80 may overflow, f16 ones do not.
+ * 1.5 x 2^-21 in f16 or 2^-35 of the row's largest), to one with them (2^-8; 2^-11 or 2^-28
+ * of the largest; the rms error of outputs is about 1.4 times what their own rounding
+ * makes).  out is rounded once.  Weights of up to 2^15 a position meet V before their sum is
+ * divided out: bf16 values beyond 2^80 may overflow, f16 ones do not.
  * Positions a token does not see never enter its row, whatever their contents (NaN
  * included).  A token whose position would be negative sees nothing: its row is zeros and
  * dattn_device_error() reports DATTN_ERR_BAD_POSITION.  Table entries are used only for

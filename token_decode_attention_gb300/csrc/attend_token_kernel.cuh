@@ -24,8 +24,8 @@
 //
 // Measured (graph replay, inputs larger than L2 in all): 64 sequences of 8 key/value heads of
 // 128 behind a window of 4096, bf16 in pages of 64, 807 MB, 119 us, 6.8 TB/s, a copy's rate
-// (a read-only stream can reach 7.5); one of 131072 positions, 537 MB, 83.4 us, 6.4 TB/s; one of 1028, 4.2 MB, 5.7 us, bound
-// by latency (launch, position, first tiles, exchange).
+// (a read-only stream can reach 7.5); one of 131072 positions, 537 MB, 83.4 us, 6.4 TB/s; one
+// of 1028, 4.2 MB, 5.7 us, bound by latency (launch, position, first tiles, exchange).
 #pragma once
 
 #include <type_traits>

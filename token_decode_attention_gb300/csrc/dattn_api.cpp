@@ -713,6 +713,7 @@ int device_facts(DeviceFacts *out) {
     *out = DeviceFacts{di.sms, di.max_smem_optin, di.err_word};
     return DATTN_OK;
 }
+
 int encode_head_rows(CUtensorMap *map, const void *base, long long rows, long long stride, int H, int D,
                      int box_rows, int box_heads, int dtype) {
     PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
@@ -723,7 +724,7 @@ int encode_head_rows(CUtensorMap *map, const void *base, long long rows, long lo
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t unit[3] = {1, 1, 1};
     const CUresult r = enc(map, dtype == kDtypeF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16
-                                                          : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                                                   : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
                            3, const_cast<void *>(base), dims, strides, box, unit, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
